@@ -9,7 +9,9 @@ If the library has not been built, importing works but every call raises
     dx = grad_input(dy, w, stride=2, padding=(1, 1), input_hw=(56, 56))
 
 The C entry points mirror these names (include/conv2d_grad_input.h; the test
-hooks are in include/conv2d_grad_input_testing.h and are thread-local).
+hooks are in include/conv2d_grad_input_testing.h and are thread-local).  The
+sequence operators (causal_conv, state_scan, block_norm; include/sequence_ops.h)
+are in ``conv2d_backward_amd.sequence`` and reached from here as well.
 """
 from __future__ import annotations
 
@@ -21,7 +23,22 @@ __all__ = [
     "make_params", "validate", "plan", "grad_weight", "grad_weight_plan", "grad_bias", "backward", "forward", "forward_plan", "set_fwd_variant", "set_variant", "set_halo_tile", "set_halo_split", "set_halo_fusion", "set_gw_variant", "set_gw_tile", "release_workspaces", "set_profile_events", "mfma_peak", "library_path", "exported_names",
     "OK", "EINVAL", "EUNSUPPORTED", "EHIP", "VARIANT_AUTO", "VARIANT_GENERIC", "VARIANT_HALO", "VARIANT_STEM",
     "VARIANT_COL2IM",
+    "causal_conv", "causal_conv_backward", "causal_conv_step", "state_scan", "state_scan_backward",
+    "state_scan_step", "block_norm", "block_norm_backward", "ScanGrads", "NormGrads", "SCAN_CHECKPOINT",
 ]
+
+_SEQUENCE = __all__[__all__.index("causal_conv"):]
+
+
+def __getattr__(name):
+    # The sequence operators' module imports torch, which the rest of the binding
+    # does at a call: so it is loaded when one of them is first named.
+    if name in _SEQUENCE:
+        from . import sequence
+
+        globals().update({n: getattr(sequence, n) for n in _SEQUENCE})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "libconv2d_gi.so")
@@ -133,7 +150,11 @@ def exported_names():
             "conv2d_gi_plan", "conv2d_gi_set_halo_tile", "conv2d_gi_set_halo_split",
             "conv2d_gi_set_halo_fusion", "conv2d_gw_set_variant", "conv2d_gw_set_tile",
             "conv2d_gi_set_profile_events",
-            "conv2d_gi_release_workspaces", "conv2d_gi_version", "conv2d_gi_mfma_peak_probe"]
+            "conv2d_gi_release_workspaces", "conv2d_gi_version", "conv2d_gi_mfma_peak_probe",
+            "causal_conv_forward", "causal_conv_backward", "causal_conv_step",
+            "causal_conv_workspace", "state_scan_forward", "state_scan_backward",
+            "state_scan_step", "state_scan_workspace", "block_norm_forward",
+            "block_norm_backward", "block_norm_workspace"]
 
 
 def make_params(N, Ci, H, W, Co, kH, kW, stride, pad_h, pad_w, oH=None, oW=None):

@@ -32,6 +32,11 @@ SOURCES = [
     "kernels_gw_f32.hip",
     "kernels_fwd_f32.hip",
     "noalloc.hip",
+    "kernels_causal_conv.hip",
+    "kernels_state_scan.hip",
+    "kernels_state_scan_bwd.hip",
+    "kernels_block_norm.hip",
+    "seq_api.cpp",
     "kernels_peak.hip",
 ]
 

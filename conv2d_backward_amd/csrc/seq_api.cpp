@@ -1,0 +1,194 @@
+// seq_api.cpp -- entry points of the sequence operators: argument checks, then
+// the launchers of seq_kernels.h.
+//
+// Entry points and their contract are declared in include/sequence_ops.h.
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+
+#include "api_internal.h"
+#include "seq_kernels.h"
+#include "sequence_ops.h"
+
+namespace {
+
+// Grid sizes: batch items are a grid's y, rows and row pieces its x.
+constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxRows = (int64_t)1 << 24;
+constexpr int64_t kMaxPositions = (int64_t)1 << 26;
+
+int check_sizes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
+    if (dtype != SEQ_F32 && dtype != SEQ_BF16 && dtype != SEQ_F16) return CONV2D_GI_EINVAL;
+    if (B < 1 || D < 1 || L < 1) return CONV2D_GI_EINVAL;
+    if (B > kMaxBatch || B * D >= kMaxRows || L > kMaxPositions) return CONV2D_GI_EUNSUPPORTED;
+    return CONV2D_GI_OK;
+}
+
+int check_taps(int32_t K) {
+    if (K < 1) return CONV2D_GI_EINVAL;
+    return K > SEQ_MAX_TAPS ? CONV2D_GI_EUNSUPPORTED : CONV2D_GI_OK;
+}
+
+int check_states(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
+    if (N < 1 || G < 1 || D % G != 0) return CONV2D_GI_EINVAL;
+    if (N > SEQ_MAX_STATES) return CONV2D_GI_EUNSUPPORTED;
+    // The join of dB and dC walks every padded position of [2, B, G, N, L] in one grid.
+    if (B * G * N > ((int64_t)1 << 40) / (L + 128)) return CONV2D_GI_EUNSUPPORTED;
+    return CONV2D_GI_OK;
+}
+
+// An output's rows must not share elements: dense positions, channels and batch
+// items apart by at least what they hold.
+bool is_apart(const seq_tensor &t, int64_t B, int64_t D, int64_t L) {
+    const int64_t c = t.channel < 0 ? -t.channel : t.channel;
+    const int64_t b = t.batch < 0 ? -t.batch : t.batch;
+    const int64_t row = L, item = (D - 1) * c + L, all = (B - 1) * b + L;
+    if (D == 1) return B == 1 || b >= row;
+    if (B == 1) return c >= row;
+    // Channels inside a batch item, or batch items inside a channel.
+    return (c >= row && b >= item) || (b >= row && c >= all);
+}
+
+bool is_workspace(const void *p, int64_t bytes, int64_t needed) {
+    return needed == 0 || (p && bytes >= needed && reinterpret_cast<uintptr_t>(p) % 16 == 0);
+}
+
+int status(hipError_t e) { return e == hipSuccess ? CONV2D_GI_OK : gi::record_hip_error(e); }
+
+}  // namespace
+
+extern "C" {
+
+int causal_conv_forward(const causal_conv_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc == CONV2D_GI_OK) rc = check_taps(a->K);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !a->y.data || !a->w) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->y, a->B, a->D, a->L)) return CONV2D_GI_EINVAL;
+    return status(seq::launch_conv_forward(*a, stream));
+}
+
+int64_t causal_conv_workspace(int32_t B, int32_t D, int32_t L, int32_t K) {
+    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK || check_taps(K) != CONV2D_GI_OK) return -1;
+    return seq::conv_backward_workspace(B, D, L, K);
+}
+
+int causal_conv_backward(const causal_conv_backward_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc == CONV2D_GI_OK) rc = check_taps(a->K);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->gy.data || !a->x.data || !a->w) return CONV2D_GI_EINVAL;
+    if (a->dx.data && !is_apart(a->dx, a->B, a->D, a->L)) return CONV2D_GI_EINVAL;
+    if (!a->dx.data && !a->dw && !a->db) return CONV2D_GI_OK;
+    if ((a->dw || a->db) &&
+        !is_workspace(a->workspace, a->workspace_bytes,
+                      seq::conv_backward_workspace(a->B, a->D, a->L, a->K)))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_conv_backward(*a, stream));
+}
+
+int causal_conv_step(const causal_conv_step_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, 1);
+    if (rc == CONV2D_GI_OK) rc = check_taps(a->K);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !a->y.data || !a->w || (!a->state && a->K > 1)) return CONV2D_GI_EINVAL;
+    if (a->lines < 1 || (!a->slots && a->lines < a->B)) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->y, a->B, a->D, 1)) return CONV2D_GI_EINVAL;
+    return status(seq::launch_conv_step(*a, stream));
+}
+
+int state_scan_forward(const state_scan_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc == CONV2D_GI_OK) rc = check_states(a->B, a->D, a->L, a->N, a->G);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !a->dt.data || !a->Bm.data || !a->Cm.data || !a->y.data || !a->A)
+        return CONV2D_GI_EINVAL;
+    if (!is_apart(a->y, a->B, a->D, a->L)) return CONV2D_GI_EINVAL;
+    return status(seq::launch_scan_forward(*a, stream));
+}
+
+int64_t state_scan_workspace(int32_t B, int32_t D, int32_t L, int32_t N, int32_t G) {
+    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK ||
+        check_states(B, D, L, N, G) != CONV2D_GI_OK)
+        return -1;
+    return seq::scan_backward_workspace(B, D, L, N, G);
+}
+
+int state_scan_backward(const state_scan_backward_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc == CONV2D_GI_OK) rc = check_states(a->B, a->D, a->L, a->N, a->G);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->gout.data || !a->x.data || !a->dt.data || !a->Bm.data || !a->Cm.data || !a->A ||
+        !a->checkpoints || !a->dx.data || !a->ddt.data || !a->dBm || !a->dCm || !a->dA)
+        return CONV2D_GI_EINVAL;
+    if (!a->z.data != !a->dz.data) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->dx, a->B, a->D, a->L) || !is_apart(a->ddt, a->B, a->D, a->L) ||
+        (a->dz.data && !is_apart(a->dz, a->B, a->D, a->L)))
+        return CONV2D_GI_EINVAL;
+    if (!is_workspace(a->workspace, a->workspace_bytes,
+                      seq::scan_backward_workspace(a->B, a->D, a->L, a->N, a->G)))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_scan_backward(*a, stream));
+}
+
+int state_scan_step(const state_scan_step_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, 1);
+    if (rc == CONV2D_GI_OK) rc = check_states(a->B, a->D, 1, a->N, a->G);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !a->dt.data || !a->Bm.data || !a->Cm.data || !a->y.data || !a->A ||
+        !a->state)
+        return CONV2D_GI_EINVAL;
+    if (a->lines < 1 || (!a->slots && a->lines < a->B)) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->y, a->B, a->D, 1)) return CONV2D_GI_EINVAL;
+    return status(seq::launch_scan_step(*a, stream));
+}
+
+int block_norm_forward(const block_norm_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (a->D > SEQ_MAX_NORM_CHANNELS) return CONV2D_GI_EUNSUPPORTED;
+    if (!(a->eps >= 0.f)) return CONV2D_GI_EINVAL;
+    if (!a->y.data || !a->r.data || !a->r_out.data) return CONV2D_GI_EINVAL;
+    if (!a->w_pre != !a->u.data) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->r_out, a->B, a->D, a->L) ||
+        (a->u.data && !is_apart(a->u, a->B, a->D, a->L)))
+        return CONV2D_GI_EINVAL;
+    if (!is_workspace(a->workspace, a->workspace_bytes,
+                      seq::norm_workspace(a->B, a->D, a->L, 0)))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_norm_forward(*a, stream));
+}
+
+int64_t block_norm_workspace(int32_t B, int32_t D, int32_t L, int32_t backward) {
+    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK || D > SEQ_MAX_NORM_CHANNELS) return -1;
+    return seq::norm_workspace(B, D, L, backward != 0);
+}
+
+int block_norm_backward(const block_norm_backward_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (a->D > SEQ_MAX_NORM_CHANNELS) return CONV2D_GI_EUNSUPPORTED;
+    if (!(a->eps >= 0.f)) return CONV2D_GI_EINVAL;
+    if (!a->y.data || !a->r_out.data || !a->dy.data || !a->dr.data) return CONV2D_GI_EINVAL;
+    if ((a->gu.data && !a->w_pre) || !a->gate.data != !a->dgate.data) return CONV2D_GI_EINVAL;
+    if ((a->dscale && !a->scale) || (a->dw_post && !a->w_post) || (a->dw_pre && !a->w_pre))
+        return CONV2D_GI_EINVAL;
+    if (!is_apart(a->dy, a->B, a->D, a->L) || !is_apart(a->dr, a->B, a->D, a->L) ||
+        (a->dgate.data && !is_apart(a->dgate, a->B, a->D, a->L)))
+        return CONV2D_GI_EINVAL;
+    if ((a->dscale || a->dw_post || a->dw_pre) &&
+        !is_workspace(a->workspace, a->workspace_bytes,
+                      seq::norm_workspace(a->B, a->D, a->L, 1)))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_norm_backward(*a, stream));
+}
+
+}  // extern "C"
