@@ -44,8 +44,7 @@ __global__ __launch_bounds__(kThreads) void conv_forward(ConvFwd<E> a) {
     const int64_t r = (int64_t)blockIdx.x * rows + threadIdx.x / a.row_threads;
     if (r >= (int64_t)a.B * a.D) return;
     const int b = (int)(r / a.D), d = (int)(r - (int64_t)b * a.D);
-    const int64_t t0 =
-        ((int64_t)blockIdx.y * a.row_threads + threadIdx.x % a.row_threads) * kV;
+    const int t0 = (int)(blockIdx.y * a.row_threads + threadIdx.x % a.row_threads) * kV;
     const int len = length_of(a.lengths, b, a.L);
     const auto *x = a.x.row(b, d);
     float past[K];  // K-1 used
@@ -57,7 +56,7 @@ __global__ __launch_bounds__(kThreads) void conv_forward(ConvFwd<E> a) {
             // The last K-1 positions of the sequence; of the given state where it is shorter.
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
-                const int64_t t = (int64_t)len + j;  // into full
+                const int t = len + j;  // into full
                 float v = 0.f;
                 if (t >= K - 1) {
                     v = E::up(x[t - (K - 1)]);
@@ -164,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void conv_backward(ConvBwd<E> a) {
         const float bias = a.bias ? a.bias[d] : 0.f;
         for (int i = first; i < last; ++i) {
             const int b = i / a.s.segments * a.s.batch + bb;
-            const int64_t t0 = ((int64_t)(i % a.s.segments) * along + lane) * kV;
+            const int t0 = (i % a.s.segments * along + lane) * kV;
             if (b >= a.B || t0 >= a.L) continue;
             const int len = length_of(a.lengths, b, a.L);
             const auto *x = a.x.row(b, d);

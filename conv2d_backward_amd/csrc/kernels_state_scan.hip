@@ -22,9 +22,7 @@
 namespace seq {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kNB = 16;  // states whose B and C are in LDS at once
+constexpr int kStaged = 4096;  // floats of B, and as many of C, in LDS at once
 
 template <class E>
 struct ScanFwd {
@@ -37,17 +35,33 @@ struct ScanFwd {
     int softplus;
 };
 
-// A work-group: 4 waves, each RPW = 64/16 rows (channels) of 16 lanes, each lane T
-// positions.  LDS: B and C of kNB states over a chunk of 16 T positions (fp32,
-// in the order the lanes read them), then A log2(e) and the running state of
-// every (state, channel).
-template <class E, int T>
-__global__ __launch_bounds__(kThreads) void scan_forward(ScanFwd<E> a) {
-    constexpr int LANES = 16, RPW = 64 / LANES, CH = kWaves * RPW, CHUNK = LANES * T;
+// Octet o of a group of states goes where its lanes read it: [state][T/4][LANES][4].
+template <class E, int LANES, int T>
+__device__ __forceinline__ void stage_store(float *to, int o, const Octet<E> &v) {
+    constexpr int PER = LANES * T / 8;  // octets of a state
+    const int n = o / PER, t = o % PER * 8;
+    float4 *p = reinterpret_cast<float4 *>(to + n * (LANES * T));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int lane = (t + 4 * h) / T, q = (t + 4 * h) % T / 4;
+        p[q * LANES + lane] =
+            float4{v.at(4 * h), v.at(4 * h + 1), v.at(4 * h + 2), v.at(4 * h + 3)};
+    }
+}
+
+// A work-group: W waves, each 64/LANES rows (channels) of LANES lanes, each lane
+// T consecutive positions of a chunk of LANES * T; NI states at a time, whose
+// chains have nothing to do with each other.  LDS: B and C of NB states over the
+// chunk (fp32, in the order the lanes read them), then A log2(e) and the
+// running state of every (state, channel).
+template <class E, int W, int LANES, int T, int NI, int OCC>
+__global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
+    constexpr int kThreads = 64 * W, CH = W * 64 / LANES, CHUNK = LANES * T, NB = kStaged / CHUNK;
     constexpr int Q = T / 4;
+    static_assert(NB % NI == 0, "whole groups of states");
     extern __shared__ float lds[];
-    float *sB = lds, *sC = lds + kNB * CHUNK;
-    float2 *sAh = reinterpret_cast<float2 *>(lds + 2 * kNB * CHUNK);  // [N][CH]
+    float *sB = lds, *sC = lds + kStaged;
+    float2 *sAh = reinterpret_cast<float2 *>(lds + 2 * kStaged);  // [N][CH]
     const int tid = threadIdx.x, lane = tid % LANES, ch = tid / LANES;
     const int Dg = a.D / a.G;
     const int g = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles, b = blockIdx.y;
@@ -56,7 +70,7 @@ __global__ __launch_bounds__(kThreads) void scan_forward(ScanFwd<E> a) {
     const int d = g * Dg + (live ? in_group : Dg - 1);
     const int len = length_of(a.lengths, b, a.L);
     const int64_t row = (int64_t)b * a.D + d;
-    const int NP = (a.N + kNB - 1) / kNB * kNB;
+    const int NP = (a.N + NB - 1) / NB * NB;
     for (int i = tid; i < NP * CH; i += kThreads) {
         const int n = i / CH, c = i % CH;
         const int dc = g * Dg + std::min(tile * CH + c, Dg - 1);
@@ -75,6 +89,20 @@ __global__ __launch_bounds__(kThreads) void scan_forward(ScanFwd<E> a) {
     const int nck = (a.L + SEQ_SCAN_CHECKPOINT - 1) / SEQ_SCAN_CHECKPOINT;
     // With checkpoints every chunk is run (their states are wanted), else those with positions.
     const int end = a.checkpoints ? a.L : len;
+    // B and C of the next group of states travel while this one's chains run.
+    constexpr int PRE = kStaged / 8 / kThreads;
+    Octet<E> next[2 * PRE];
+    const auto prefetch = [&](int c, int n0) {
+#pragma unroll
+        for (int k = 0; k < PRE; ++k) {
+            const int o = k * kThreads + tid, n = n0 + o / (CHUNK / 8);
+            const int t = c + o % (CHUNK / 8) * 8, end_n = n < a.N ? len : 0;  // past N: zeros
+            const int64_t state = (int64_t)g * a.N + n;
+            next[k].load(a.Bm.row(b, state), t, end_n);
+            next[PRE + k].load(a.Cm.row(b, state), t, end_n);
+        }
+    };
+    if (end > 0) prefetch(0, 0);
     int c0 = 0;
     for (; c0 < end; c0 += CHUNK) {
         const int t0 = c0 + lane * T;
@@ -85,77 +113,89 @@ __global__ __launch_bounds__(kThreads) void scan_forward(ScanFwd<E> a) {
             load_row<E, T>(x, t0, len, xv);
             load_row<E, T>(dt, t0, len, s);
 #pragma unroll
+            for (int i = 0; i < T; ++i) s[i] += bias;
+            if (a.softplus) {
+#pragma unroll
+                for (int i = 0; i < T; ++i) s[i] = softplus(s[i]);
+            }
+            if (c0 + CHUNK > len) {
+#pragma unroll
+                for (int i = 0; i < T; ++i)  // 0: the state passes unchanged
+                    s[i] = len - t0 > i ? s[i] : 0.f;
+            }
+#pragma unroll
             for (int i = 0; i < T; ++i) {
-                const float raw = s[i] + bias;
-                const float step = a.softplus ? softplus(raw) : raw;
-                s[i] = t0 + i < len ? step : 0.f;  // 0: the state passes unchanged
                 u[i] = s[i] * xv[i];
                 acc[i] = skip * xv[i];
                 total += s[i];
             }
         }
-        for (int n0 = 0; n0 < a.N; n0 += kNB) {
-            const int nb = std::min(kNB, a.N - n0);
+        const bool mark = a.checkpoints && live && t0 % SEQ_SCAN_CHECKPOINT == 0 && t0 < a.L;
+        for (int n0 = 0; n0 < a.N; n0 += NB) {
             __syncthreads();
-            for (int i = tid; i < nb * (CHUNK / 4); i += kThreads) {
-                const int n = i / (CHUNK / 4), q = i % (CHUNK / 4);
-                const int64_t t = c0 + 4 * q;
-                const int at = n * CHUNK + (q % Q * LANES + q / Q) * 4;
-                float v[4];
-                load_row<E, 4>(a.Bm.row(b, (int64_t)g * a.N + n0 + n), t, len, v);
-                *reinterpret_cast<float4 *>(sB + at) = float4{v[0], v[1], v[2], v[3]};
-                load_row<E, 4>(a.Cm.row(b, (int64_t)g * a.N + n0 + n), t, len, v);
-                *reinterpret_cast<float4 *>(sC + at) = float4{v[0], v[1], v[2], v[3]};
-            }
+#pragma unroll
+            for (int k = 0; k < PRE; ++k) stage_store<E, LANES, T>(sB, k * kThreads + tid, next[k]);
+#pragma unroll
+            for (int k = 0; k < PRE; ++k)
+                stage_store<E, LANES, T>(sC, k * kThreads + tid, next[PRE + k]);
             __syncthreads();
-            for (int n = 0; n < nb; ++n) {
+            const bool more = n0 + NB < a.N;
+            if (more || c0 + CHUNK < end)
+                prefetch(more ? c0 : c0 + CHUNK, more ? n0 + NB : 0);
+            const int nb = std::min(NB, a.N - n0);
+            for (int n = 0; n < nb; n += NI) {
                 float2 *ah = sAh + (n0 + n) * CH + ch;
-                const float A2 = ah->x, carry = ah->y;
-                float da[T], in[T];
-                float hq = 0.f;
+                const float *pB = sB + n * CHUNK + lane * 4, *pC = sC + n * CHUNK + lane * 4;
+                float da[NI][T], in[NI][T], h[NI], P[NI], carry[NI];
 #pragma unroll
-                for (int j = 0; j < Q; ++j) {
-                    const float4 B4 =
-                        *reinterpret_cast<const float4 *>(sB + n * CHUNK + (j * LANES + lane) * 4);
-                    in[4 * j] = u[4 * j] * B4.x;
-                    in[4 * j + 1] = u[4 * j + 1] * B4.y;
-                    in[4 * j + 2] = u[4 * j + 2] * B4.z;
-                    in[4 * j + 3] = u[4 * j + 3] * B4.w;
+                for (int k = 0; k < NI; ++k) {
+                    const float2 v = ah[k * CH];
+                    carry[k] = v.y;
+                    P[k] = exp2_fast(total * v.x);
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) {
+                        const float4 B4 =
+                            *reinterpret_cast<const float4 *>(pB + k * CHUNK + j * LANES * 4);
+                        const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            da[k][4 * j + i] = exp2_fast(s[4 * j + i] * v.x);
+                            in[k][4 * j + i] = u[4 * j + i] * Bv[i];
+                        }
+                    }
+                    // Lane 0 starts from the running state.
+                    h[k] = lane == 0 ? carry[k] : 0.f;
                 }
 #pragma unroll
-                for (int i = 0; i < T; ++i) {
-                    da[i] = exp2_fast(s[i] * A2);
-                    hq = __builtin_fmaf(da[i], hq, in[i]);
-                }
-                float P = exp2_fast(total * A2);
-                // Lane 0 starts from the running state; then (P, Q) over the row.
-                float hs = __builtin_fmaf(P, lane == 0 ? carry : 0.f, hq);
-                hs = __builtin_fmaf(P, dpp0<kRowShr + 1>(hs), hs);
-                P *= dpp0<kRowShr + 1>(P);
-                hs = __builtin_fmaf(P, dpp0<kRowShr + 2>(hs), hs);
-                P *= dpp0<kRowShr + 2>(P);
-                hs = __builtin_fmaf(P, dpp0<kRowShr + 4>(hs), hs);
-                P *= dpp0<kRowShr + 4>(P);
-                hs = __builtin_fmaf(P, dpp0<kRowShr + 8>(hs), hs);
-                // Lane l's state in is lane l-1's state out; lane 0 gets lane 15's: the next carry.
-                const float turned = dpp0<kRowRor + 1>(hs);
-                float h = lane == 0 ? carry : turned;
-                if (lane == 0) ah->y = turned;
-                if (a.checkpoints && live && t0 % SEQ_SCAN_CHECKPOINT == 0 && t0 < a.L)
-                    a.checkpoints[(row * nck + t0 / SEQ_SCAN_CHECKPOINT) * a.N + n0 + n] = h;
+                for (int i = 0; i < T; ++i)
 #pragma unroll
-                for (int j = 0; j < Q; ++j) {
-                    const float4 C4 =
-                        *reinterpret_cast<const float4 *>(sC + n * CHUNK + (j * LANES + lane) * 4);
-                    h = __builtin_fmaf(da[4 * j], h, in[4 * j]);
-                    acc[4 * j] = __builtin_fmaf(C4.x, h, acc[4 * j]);
-                    h = __builtin_fmaf(da[4 * j + 1], h, in[4 * j + 1]);
-                    acc[4 * j + 1] = __builtin_fmaf(C4.y, h, acc[4 * j + 1]);
-                    h = __builtin_fmaf(da[4 * j + 2], h, in[4 * j + 2]);
-                    acc[4 * j + 2] = __builtin_fmaf(C4.z, h, acc[4 * j + 2]);
-                    h = __builtin_fmaf(da[4 * j + 3], h, in[4 * j + 3]);
-                    acc[4 * j + 3] = __builtin_fmaf(C4.w, h, acc[4 * j + 3]);
+                    for (int k = 0; k < NI; ++k)
+                        h[k] = __builtin_fmaf(da[k][i], h[k], in[k][i]);
+                // Lane l's state in is lane l-1's state out; lane 0 gets the last lane's, the
+                // next chunk's running state.
+                float turned[NI];
+                scan_lanes<LANES>(h, P, turned);
+#pragma unroll
+                for (int k = 0; k < NI; ++k) {
+                    h[k] = lane == 0 ? carry[k] : turned[k];
+                    if (lane == 0) ah[k * CH].y = turned[k];
+                    if (mark && n0 + n + k < a.N)
+                        a.checkpoints[(row * nck + t0 / SEQ_SCAN_CHECKPOINT) * a.N + n0 + n + k] =
+                            h[k];
                 }
+#pragma unroll
+                for (int j = 0; j < Q; ++j)
+#pragma unroll
+                    for (int k = 0; k < NI; ++k) {
+                        const float4 C4 =
+                            *reinterpret_cast<const float4 *>(pC + k * CHUNK + j * LANES * 4);
+                        const float Cv[4] = {C4.x, C4.y, C4.z, C4.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            h[k] = __builtin_fmaf(da[k][4 * j + i], h[k], in[k][4 * j + i]);
+                            acc[4 * j + i] = __builtin_fmaf(Cv[i], h[k], acc[4 * j + i]);
+                        }
+                    }
             }
         }
         if (live && t0 < a.L) {
@@ -165,8 +205,10 @@ __global__ __launch_bounds__(kThreads) void scan_forward(ScanFwd<E> a) {
 #pragma unroll
                 for (int i = 0; i < T; ++i) acc[i] *= zv[i] * sigmoid(zv[i]);
             }
+            if (c0 + CHUNK > len) {
 #pragma unroll
-            for (int i = 0; i < T; ++i) acc[i] = t0 + i < len ? acc[i] : 0.f;
+                for (int i = 0; i < T; ++i) acc[i] = len - t0 > i ? acc[i] : 0.f;
+            }
             store_row<E, T>(y, t0, a.L, acc);
         }
     }
@@ -174,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void scan_forward(ScanFwd<E> a) {
         float zero[T];
 #pragma unroll
         for (int i = 0; i < T; ++i) zero[i] = 0.f;
-        for (int64_t t = c0 + lane * T; t < a.L; t += CHUNK) store_row<E, T>(y, t, a.L, zero);
+        for (int t = c0 + lane * T; t < a.L; t += CHUNK) store_row<E, T>(y, t, a.L, zero);
     }
     if (a.state_out) {
         __syncthreads();
@@ -186,6 +228,8 @@ __global__ __launch_bounds__(kThreads) void scan_forward(ScanFwd<E> a) {
         }
     }
 }
+
+constexpr int kThreads = 256;  // of scan_step
 
 template <class E>
 struct ScanStep {
@@ -242,16 +286,56 @@ __global__ __launch_bounds__(kThreads) void scan_step(ScanStep<E> a) {
     }
 }
 
-template <class E>
+template <class E, int W, int LANES, int T, int NI, int OCC>
 hipError_t forward(const state_scan_args &a, hipStream_t s) {
-    constexpr int T = 8, CH = kWaves * 4;
+    constexpr int CH = W * 64 / LANES, NB = kStaged / (LANES * T);
     ScanFwd<E> k{view<E>(a.x), view<E>(a.dt), view<E>(a.z), view<E>(a.Bm), view<E>(a.Cm),
                  view<E>(a.y), a.A, a.skip, a.dt_bias, a.state_in, a.state_out, a.checkpoints,
                  a.lengths, a.B, a.D, a.L, a.N, a.G, (a.D / a.G + CH - 1) / CH, a.softplus};
-    const int NP = (a.N + kNB - 1) / kNB * kNB;
-    const size_t bytes = (2 * kNB * 16 * T + 2 * (size_t)NP * CH) * sizeof(float);
-    scan_forward<E, T><<<dim3((unsigned)(a.G * k.tiles), (unsigned)a.B), kThreads, bytes, s>>>(k);
+    const int NP = (a.N + NB - 1) / NB * NB;
+    const size_t bytes = (2 * kStaged + 2 * (size_t)NP * CH) * sizeof(float);
+    if (bytes > 64 * 1024) {
+        hipError_t e =
+            hipFuncSetAttribute((const void *)scan_forward<E, W, LANES, T, NI, OCC>,
+                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != hipSuccess) return e;
+    }
+    scan_forward<E, W, LANES, T, NI, OCC>
+        <<<dim3((unsigned)(a.G * k.tiles), (unsigned)a.B), 64 * W, bytes, s>>>(k);
     return hipGetLastError();
+}
+
+// The widths LANES x T of a row's chunk.  A lane's T positions share the 18 (16
+// lanes: 15) instructions of the lane scan beside their 7 (v_exp_f32 takes the
+// time of two); rows of 64 lanes add 0.6 for B and C, which fewer channels
+// share.  A SIMD works on 4 waves at a time and leaves none idle: fewer waves
+// than 4 a SIMD make nothing faster, more take their turns.  So of
+//   chunks * T * (8 + 18 / T) * max(1, waves / 4096)
+// the least.  Measured (bf16, N = 16, us, 64 x 16 / 64 x 8 / 16 x 16 / 16 x 8):
+// [1, 4096, 8192] 203 / 218 / 277 / 444, [8, 4096, 1024] 182 / 190 / 166 / 204,
+// [5, 1000, 301] 47 / 26 / 29 / 28, [1, 1024, 8192] 97 / 104 / 255 / 420.
+template <class E>
+hipError_t forward_any(const state_scan_args &a, hipStream_t s) {
+    static const int kLanes[] = {64, 64, 64, 16, 16, 16}, kT[] = {16, 8, 4, 16, 8, 4};
+    int best = 0;
+    double least = 0;
+    for (int v = 0; v < 6; ++v) {
+        const int channels = (v < 3 ? 8 : 4) * 64 / kLanes[v], chunk = kLanes[v] * kT[v];
+        const int64_t rows = (int64_t)a.B * a.G * ((a.D / a.G + channels - 1) / channels) * channels;
+        const double waves = (double)rows * kLanes[v] / 64;
+        const double cost = ((a.L + chunk - 1) / chunk) *
+                            (v < 3 ? kT[v] * 8.6 + 18 : kT[v] * 8. + 15) *
+                            std::max(1., waves / 4096);
+        if (v == 0 || cost < least) best = v, least = cost;
+    }
+    switch (best) {
+        case 0: return forward<E, 8, 64, 16, 1, 4>(a, s);
+        case 1: return forward<E, 8, 64, 8, 1, 4>(a, s);
+        case 2: return forward<E, 8, 64, 4, 2, 4>(a, s);
+        case 3: return forward<E, 4, 16, 16, 1, 3>(a, s);
+        case 4: return forward<E, 4, 16, 8, 1, 4>(a, s);
+        default: return forward<E, 4, 16, 4, 2, 4>(a, s);
+    }
 }
 
 template <class E>
@@ -273,8 +357,8 @@ hipError_t step(const state_scan_step_args &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_scan_forward(const state_scan_args &a, hipStream_t s) {
-    return a.dtype == SEQ_F32 ? forward<F32>(a, s)
-           : a.dtype == SEQ_BF16 ? forward<BF16>(a, s) : forward<F16>(a, s);
+    return a.dtype == SEQ_F32 ? forward_any<F32>(a, s)
+           : a.dtype == SEQ_BF16 ? forward_any<BF16>(a, s) : forward_any<F16>(a, s);
 }
 hipError_t launch_scan_step(const state_scan_step_args &a, hipStream_t s) {
     return a.dtype == SEQ_F32 ? step<F32>(a, s)

@@ -77,29 +77,54 @@ __device__ __forceinline__ void store_vec(typename E::type *p, const float (&in)
 
 // Positions t .. t+V-1 of a row; those outside [0, end) are 0 and not read.
 template <class E, int V>
-__device__ __forceinline__ void load_row(const typename E::type *row, int64_t t, int64_t end,
+__device__ __forceinline__ void load_row(const typename E::type *row, int t, int end,
                                          float (&out)[V]) {
-    if (t >= 0 && t + V <= end) {
-        load_vec<E, V>(row + t, out);
+    const typename E::type *p = row + t;
+    if (t >= 0 && end - t >= V) {
+        load_vec<E, V>(p, out);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             out[i] = 0.f;
-            if (t + i >= 0 && t + i < end) out[i] = E::up(row[t + i]);
+            if (t >= -i && end - t > i) out[i] = E::up(p[i]);
         }
     }
 }
 
+// Eight positions as they are stored, for a load whose use comes later; those
+// outside [0, end) are 0 and not read.
+template <class E>
+struct Octet {
+    typename Vec<typename E::type, 8>::type v;
+    __device__ __forceinline__ void load(const typename E::type *row, int t, int end) {
+        const typename E::type *p = row + t;
+        if (end - t >= 8) {
+            v = *reinterpret_cast<const typename Vec<typename E::type, 8>::type *>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = 0;
+                if (end - t > i) v[i] = p[i];
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int i) const {
+        const typename E::type e = v[i];
+        return E::up(e);
+    }
+};
+
 // Writes positions t .. t+V-1 of a row of L positions (t >= 0).
 template <class E, int V>
-__device__ __forceinline__ void store_row(typename E::type *row, int64_t t, int64_t L,
+__device__ __forceinline__ void store_row(typename E::type *row, int t, int L,
                                           const float (&v)[V]) {
-    if (t + V <= L) {
-        store_vec<E, V>(row + t, v);
+    typename E::type *p = row + t;
+    if (L - t >= V) {
+        store_vec<E, V>(p, v);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (t + i < L) row[t + i] = E::down(v[i]);
+            if (L - t > i) p[i] = E::down(v[i]);
     }
 }
 
@@ -134,16 +159,16 @@ __device__ __forceinline__ float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.f + exp2_fast(-v * kLog2e));
 }
 
-// log(1 + e^v).  For the logarithm of 1 + e the rounded sum w = 1 + e stands in
-// for it with the factor e / (w - 1), which takes the rounding of w back out:
-// log(1 + e) = log(w) * e / (w - 1) up to a relative 2^-23 or so, for any e.
+// log(1 + e^v) = max(v, 0) + log(1 + e) with e = exp(-|v|) in (0, 1].  The sum
+// w = 1 + e loses c = e - (w - 1) <= 2^-24 of e, exactly known; log(1 + e) is
+// log(w) + c / w to second order in c, and c stands for c / w: they differ by
+// c e / w, at most 2^-25 of the result.  Where e is too small to change w the
+// result is c = e.
 __device__ __forceinline__ float softplus(float v) {
-    const float e = exp2_fast(-__builtin_fabsf(v) * kLog2e);
+    const float e = exp2_fast(__builtin_fabsf(v) * -kLog2e);
     const float w = 1.f + e;
-    const float d = w - 1.f;
-    const float l = __builtin_amdgcn_logf(w) * kLn2;
-    const float r = d == 0.f ? e : l * (e * __builtin_amdgcn_rcpf(d));
-    return __builtin_fmaxf(v, 0.f) + r;
+    const float c = e - (w - 1.f);
+    return __builtin_fmaxf(v, 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(w), kLn2, c);
 }
 
 // Lane moves inside rows of 16 lanes (DPP): lanes without a source get `old`.
@@ -159,6 +184,68 @@ __device__ __forceinline__ float dpp0(float v) {
         0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 constexpr int kRowShl = 0x100, kRowShr = 0x110, kRowRor = 0x120;  // + distance 1..15
+
+// Maps h -> P h + Q compose along the lanes of a row of LANES (16 or 64): with Q
+// in h, h[k] becomes the composition of lanes 0 .. l applied to 0, and turned[k]
+// lane l-1's result, in lane 0 the last lane's.  NI independent chains.  A DPP
+// operand must be two instructions older than its use, which the compiler does
+// not see to inside an asm block: chains alternate, and one alone waits.
+#define SEQ_STEP1(M) \
+    "v_fmac_f32_dpp %0, %0, %1 " M "\n\tv_mul_f32_dpp %1, %1, %1 " M "\n\ts_nop 0\n\t"
+#define SEQ_STEP2(M)                                                                  \
+    "v_fmac_f32_dpp %0, %0, %2 " M "\n\tv_fmac_f32_dpp %1, %1, %3 " M "\n\t"          \
+    "v_mul_f32_dpp %2, %2, %2 " M "\n\tv_mul_f32_dpp %3, %3, %3 " M "\n\t"
+#define SEQ_ALL " row_mask:0xf bank_mask:0xf"
+#define SEQ_ROW_STEPS(S, DIR) \
+    S("row_" DIR ":1" SEQ_ALL) S("row_" DIR ":2" SEQ_ALL) S("row_" DIR ":4" SEQ_ALL)
+
+template <int LANES>
+__device__ __forceinline__ void scan_chain(float &h, float &P, float &turned) {
+    if constexpr (LANES == 16) {
+        asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP1, "shr")
+            "v_fmac_f32_dpp %0, %0, %1 row_shr:8" SEQ_ALL "\n\ts_nop 1\n\t"
+            "v_mov_b32_dpp %2, %0 row_ror:1" SEQ_ALL
+            : "+v"(h), "+v"(P), "=&v"(turned));
+    } else {
+        asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP1, "shr") SEQ_STEP1("row_shr:8" SEQ_ALL)
+            SEQ_STEP1("row_bcast:15 row_mask:0xa bank_mask:0xf")
+            "v_fmac_f32_dpp %0, %0, %1 row_bcast:31 row_mask:0xc bank_mask:0xf\n\ts_nop 1\n\t"
+            "v_mov_b32_dpp %2, %0 wave_ror:1" SEQ_ALL
+            : "+v"(h), "+v"(P), "=&v"(turned));
+    }
+}
+
+template <int LANES>
+__device__ __forceinline__ void scan_chains(float &h0, float &h1, float &P0, float &P1,
+                                            float &turned0, float &turned1) {
+    if constexpr (LANES == 16) {
+        asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP2, "shr")
+            "v_fmac_f32_dpp %0, %0, %2 row_shr:8" SEQ_ALL "\n\t"
+            "v_fmac_f32_dpp %1, %1, %3 row_shr:8" SEQ_ALL "\n\ts_nop 0\n\t"
+            "v_mov_b32_dpp %4, %0 row_ror:1" SEQ_ALL "\n\t"
+            "v_mov_b32_dpp %5, %1 row_ror:1" SEQ_ALL
+            : "+v"(h0), "+v"(h1), "+v"(P0), "+v"(P1), "=&v"(turned0), "=&v"(turned1));
+    } else {
+        asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP2, "shr") SEQ_STEP2("row_shr:8" SEQ_ALL)
+            SEQ_STEP2("row_bcast:15 row_mask:0xa bank_mask:0xf")
+            "v_fmac_f32_dpp %0, %0, %2 row_bcast:31 row_mask:0xc bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %1, %1, %3 row_bcast:31 row_mask:0xc bank_mask:0xf\n\ts_nop 0\n\t"
+            "v_mov_b32_dpp %4, %0 wave_ror:1" SEQ_ALL "\n\t"
+            "v_mov_b32_dpp %5, %1 wave_ror:1" SEQ_ALL
+            : "+v"(h0), "+v"(h1), "+v"(P0), "+v"(P1), "=&v"(turned0), "=&v"(turned1));
+    }
+}
+
+template <int LANES, int NI>
+__device__ __forceinline__ void scan_lanes(float (&h)[NI], float (&P)[NI], float (&turned)[NI]) {
+    if constexpr (NI == 1) {
+        scan_chain<LANES>(h[0], P[0], turned[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < NI; k += 2)
+            scan_chains<LANES>(h[k], h[k + 1], P[k], P[k + 1], turned[k], turned[k + 1]);
+    }
+}
 
 // v of lane ^ M.
 __device__ __forceinline__ float lane_xor(float v, int m) { return __shfl_xor(v, m, 64); }
