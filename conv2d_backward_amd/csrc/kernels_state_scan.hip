@@ -35,20 +35,6 @@ struct ScanFwd {
     int softplus;
 };
 
-// Octet o of a group of states goes where its lanes read it: [state][T/4][LANES][4].
-template <class E, int LANES, int T>
-__device__ __forceinline__ void stage_store(float *to, int o, const Octet<E> &v) {
-    constexpr int PER = LANES * T / 8;  // octets of a state
-    const int n = o / PER, t = o % PER * 8;
-    float4 *p = reinterpret_cast<float4 *>(to + n * (LANES * T));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int lane = (t + 4 * h) / T, q = (t + 4 * h) % T / 4;
-        p[q * LANES + lane] =
-            float4{v.at(4 * h), v.at(4 * h + 1), v.at(4 * h + 2), v.at(4 * h + 3)};
-    }
-}
-
 // A work-group: W waves, each 64/LANES rows (channels) of LANES lanes, each lane
 // T consecutive positions of a chunk of LANES * T; NI states at a time, whose
 // chains have nothing to do with each other.  LDS: B and C of NB states over the
@@ -134,10 +120,10 @@ __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
         for (int n0 = 0; n0 < a.N; n0 += NB) {
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < PRE; ++k) stage_store<E, LANES, T>(sB, k * kThreads + tid, next[k]);
+            for (int k = 0; k < PRE; ++k) stage_octet<E, LANES, T>(sB, k * kThreads + tid, next[k]);
 #pragma unroll
             for (int k = 0; k < PRE; ++k)
-                stage_store<E, LANES, T>(sC, k * kThreads + tid, next[PRE + k]);
+                stage_octet<E, LANES, T>(sC, k * kThreads + tid, next[PRE + k]);
             __syncthreads();
             const bool more = n0 + NB < a.N;
             if (more || c0 + CHUNK < end)

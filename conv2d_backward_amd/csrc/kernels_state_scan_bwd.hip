@@ -21,24 +21,49 @@
 namespace seq {
 namespace {
 
-constexpr int LANES = 16, T = 8, CHUNK = LANES * T, RPW = 64 / LANES;
-static_assert(CHUNK == SEQ_SCAN_CHECKPOINT, "a chunk starts at every checkpoint");
+constexpr int LANES = 16, RPW = 64 / LANES;
 constexpr int kWaves = 8, kThreads = 64 * kWaves, CH = kWaves * RPW;
 constexpr int kNB = 16;  // states whose B and C are in LDS at once
-constexpr int kNR = 4;   // states summed over waves at once
-constexpr int kTailWaves = 4, kTailThreads = 64 * kTailWaves, kTailCH = kTailWaves * RPW;
+constexpr int kTailT = 8, kTailWaves = 4, kTailThreads = 64 * kTailWaves,
+              kTailCH = kTailWaves * RPW;
 
 struct Plan {
-    int tiles, chunks, segments, pitch;  // pitch: padded positions of a partial row
+    int T, chunk;        // positions of a lane and of a chunk
+    int tiles, chunks;   // channel tiles of a group, chunks of a row
+    int segments;
+    int marks;           // checkpoints of a row
+    int pitch;           // padded positions of a partial row of dB or dC
+    int joined;          // states summed over the waves at once
+    size_t lds;
     int64_t sums, params, tails, steps;  // workspace offsets, in floats
     int64_t floats;
 };
 
+constexpr size_t kLdsBytes = 160 * 1024;
+
+// LDS of a work-group: B and C, two halves of sums, states before, and A, q and dA.
+size_t lds_bytes(int T, int joined, int64_t N) {
+    const size_t NP = (N + kNB - 1) / kNB * kNB, chunk = LANES * T;
+    return (2 * kNB * chunk + 2 * joined * 2 * kWaves * chunk + kNB * CH + 3 * NP * CH) *
+           sizeof(float);
+}
+
 Plan make_plan(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
     Plan p;
+    // A lane of 16 positions spends half as much on the lane scans as one of 8
+    // (30 instructions for both chains, beside some 24 a position): 288 us for
+    // 311 at [4, 2048, 2048], N = 16.  Not where padding the row to whole chunks
+    // costs more (78 us for 116 at [5, 1000, 301]) nor where its sums do not fit.
+    const int64_t c16 = (L + 255) / 256 * (16 * 24 + 30), c8 = (L + 127) / 128 * (8 * 24 + 30);
+    p.T = c16 <= c8 && lds_bytes(16, 1, N) <= kLdsBytes ? 16 : 8;
+    p.joined = p.T == 16 ? 2 : 4;
+    while (lds_bytes(p.T, p.joined, N) > kLdsBytes) p.joined /= 2;
+    p.lds = lds_bytes(p.T, p.joined, N);
+    p.chunk = LANES * p.T;
     p.tiles = (int)((D / G + CH - 1) / CH);
-    p.chunks = (int)((L + CHUNK - 1) / CHUNK);
-    p.pitch = p.chunks * CHUNK;
+    p.chunks = (int)((L + p.chunk - 1) / p.chunk);
+    p.marks = (int)((L + SEQ_SCAN_CHECKPOINT - 1) / SEQ_SCAN_CHECKPOINT);
+    p.pitch = p.chunks * p.chunk;
     const int64_t groups = B * G * p.tiles;
     p.segments = groups >= 256 ? 1 : (int)std::min<int64_t>(p.chunks, (512 + groups - 1) / groups);
     p.sums = 0;
@@ -62,39 +87,18 @@ struct ScanBwd {
 };
 
 // Steps of a lane's positions; 0 beyond the length, where the state passes unchanged.
-template <class E>
+template <class E, int T>
 __device__ __forceinline__ void load_steps(const typename E::type *dt, int t0, int len, float bias,
                                            bool soft, float (&s)[T]) {
     load_row<E, T>(dt, t0, len, s);
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-        const float raw = s[i] + bias;
-        s[i] = t0 + i < len ? (soft ? softplus(raw) : raw) : 0.f;
+    for (int i = 0; i < T; ++i) s[i] += bias;
+    if (soft) {
+#pragma unroll
+        for (int i = 0; i < T; ++i) s[i] = softplus(s[i]);
     }
-}
-
-// Chains (P, Q) from the right: lane l's result is what reaches the state before
-// its first position, `carry` what comes from behind lane 15.
-__device__ __forceinline__ float scan_back(float P, float Q, float carry, int lane) {
-    float v = __builtin_fmaf(P, lane == LANES - 1 ? carry : 0.f, Q);
-    v = __builtin_fmaf(P, dpp0<kRowShl + 1>(v), v);
-    P *= dpp0<kRowShl + 1>(P);
-    v = __builtin_fmaf(P, dpp0<kRowShl + 2>(v), v);
-    P *= dpp0<kRowShl + 2>(P);
-    v = __builtin_fmaf(P, dpp0<kRowShl + 4>(v), v);
-    P *= dpp0<kRowShl + 4>(P);
-    return __builtin_fmaf(P, dpp0<kRowShl + 8>(v), v);
-}
-
-__device__ __forceinline__ float scan_forth(float P, float Q, float carry, int lane) {
-    float v = __builtin_fmaf(P, lane == 0 ? carry : 0.f, Q);
-    v = __builtin_fmaf(P, dpp0<kRowShr + 1>(v), v);
-    P *= dpp0<kRowShr + 1>(P);
-    v = __builtin_fmaf(P, dpp0<kRowShr + 2>(v), v);
-    P *= dpp0<kRowShr + 2>(P);
-    v = __builtin_fmaf(P, dpp0<kRowShr + 4>(v), v);
-    P *= dpp0<kRowShr + 4>(P);
-    return __builtin_fmaf(P, dpp0<kRowShr + 8>(v), v);
+#pragma unroll
+    for (int i = 0; i < T; ++i) s[i] = len - t0 > i ? s[i] : 0.f;
 }
 
 // Sum over the 16 lanes of a row, in every lane.
@@ -105,40 +109,11 @@ __device__ __forceinline__ float row_sum(float v) {
     return v + dpp0<kRowRor + 1>(v);
 }
 
-// lo of the lower half wave + hi-half counterpart, for two values at once:
-// lanes 0..31 get x summed over the halves, lanes 32..63 y.
-__device__ __forceinline__ float meet32(float x, float y) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x),
-                                                    __builtin_bit_cast(unsigned, y), false, false);
-    const unsigned p = r[0], q = r[1];
-    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
-}
-// The same between the 16-lane rows of each half: even rows get x, odd rows y.
-__device__ __forceinline__ float meet16(float x, float y) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
-                                                    __builtin_bit_cast(unsigned, y), false, false);
-    const unsigned p = r[0], q = r[1];
-    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
-}
-
-// Stages B or C of nb states from position c0, in the order the lanes read them.
-template <class E>
-__device__ __forceinline__ void stage(const View<E> &m, int64_t b, int64_t first, int nb, int c0,
-                                      int len, float *to, int tid, int threads) {
-    for (int i = tid; i < nb * (CHUNK / 4); i += threads) {
-        const int n = i / (CHUNK / 4), q = i % (CHUNK / 4);
-        float v[4];
-        load_row<E, 4>(m.row(b, first + n), c0 + 4 * q, len, v);
-        *reinterpret_cast<float4 *>(to + n * CHUNK + (q % (T / 4) * LANES + q / (T / 4)) * 4) =
-            float4{v[0], v[1], v[2], v[3]};
-    }
-}
-
-__device__ __forceinline__ void fetch(const float *from, int n, int lane, float (&v)[T]) {
+template <int T>
+__device__ __forceinline__ void fetch(const float *from, int lane, float (&v)[T]) {
 #pragma unroll
     for (int j = 0; j < T / 4; ++j) {
-        const float4 f =
-            *reinterpret_cast<const float4 *>(from + n * CHUNK + (j * LANES + lane) * 4);
+        const float4 f = *reinterpret_cast<const float4 *>(from + (j * LANES + lane) * 4);
         v[4 * j] = f.x;
         v[4 * j + 1] = f.y;
         v[4 * j + 2] = f.z;
@@ -146,16 +121,53 @@ __device__ __forceinline__ void fetch(const float *from, int n, int lane, float 
     }
 }
 
-template <class E>
+// x summed over the half waves in lanes 0..31, y in lanes 32..63.
+__device__ __forceinline__ float meet32(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x),
+                                                    __builtin_bit_cast(unsigned, y), false, false);
+    const unsigned p = r[0], q = r[1];
+    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
+}
+// x summed over the two rows of 16 lanes of each half in its first row, y in its second.
+__device__ __forceinline__ float meet16(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
+                                                    __builtin_bit_cast(unsigned, y), false, false);
+    const unsigned p = r[0], q = r[1];
+    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
+}
+
+// F floats at an address that is a multiple of their size.
+template <int F>
+struct alignas(4 * F) Whole {
+    float v[F];
+};
+
+// A wave's four channels meet: row k of 16 lanes ends with the sums of positions
+// k T/4 .. (k+1) T/4 - 1 of each lane.
+template <int T>
+__device__ __forceinline__ Whole<T / 4> meet_rows(const float (&v)[T]) {
+    Whole<T / 4> sum;
+#pragma unroll
+    for (int i = 0; i < T / 4; ++i)
+        sum.v[i] = meet16(meet32(v[i], v[T / 2 + i]), meet32(v[T / 4 + i], v[3 * T / 4 + i]));
+    return sum;
+}
+
+// A work-group: 8 waves of 4 channels, 16 lanes a channel, T positions a lane,
+// NI states at a time.
+template <class E, int T, int NI>
 __global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
+    constexpr int CHUNK = LANES * T, F = T / 4;  // F: sums of a lane
+    constexpr int OCTETS = 2 * kNB * CHUNK / 8, PRE = OCTETS / kThreads;
+    static_assert(OCTETS % kThreads == 0 && kNB * CH == kThreads, "whole rounds of threads");
     extern __shared__ float lds[];
-    float *sB = lds, *sC = sB + kNB * CHUNK;
-    float *sums = sC + kNB * CHUNK;                 // [kNR][2][kWaves][CHUNK]
-    float *sH = sums + kNR * 2 * kWaves * CHUNK;    // [kNB][CH]: states before the chunk
+    float *sBC = lds;                                        // [B or C][kNB][CHUNK]
+    float *sums = sBC + 2 * kNB * CHUNK;                     // 2 of [joined][B or C][kWaves][64][F]
+    float *sH = sums + 2 * a.p.joined * 2 * kWaves * CHUNK;  // [kNB][CH]: states before
     const int NP = (a.N + kNB - 1) / kNB * kNB;
-    float *sA = sH + kNB * CH;                      // [NP][CH]: A log2(e)
-    float *sG = sA + NP * CH;                       // [NP][CH]: what comes from behind
-    float *sD = sG + NP * CH;                       // [NP][CH]: dA so far
+    float *sA = sH + kNB * CH;                               // [NP][CH]: A log2(e)
+    float *sG = sA + NP * CH;                                // [NP][CH]: what comes from behind
+    float *sD = sG + NP * CH;                                // [NP][CH]: dA so far
     const int tid = threadIdx.x, lane = tid % LANES, ch = tid / LANES, wave = tid / 64;
     const int Dg = a.D / a.G;
     const int g = blockIdx.x / a.p.tiles, tile = blockIdx.x % a.p.tiles;
@@ -185,12 +197,33 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
     float sum_skip = 0.f, sum_bias = 0.f;
     const int c_lo = (int)((int64_t)a.p.chunks * seg / a.p.segments);
     const int c_hi = (int)((int64_t)a.p.chunks * (seg + 1) / a.p.segments);
+    // B, C and the checkpoints of the next group of states travel while this one's chains run.
+    Octet<E> next[PRE];
+    float next_h = 0.f;
+    const auto prefetch = [&](int c, int n0) {
+#pragma unroll
+        for (int k = 0; k < PRE; ++k) {
+            const int o = k * kThreads + tid, per = kNB * CHUNK / 8;
+            const int n = n0 + o % per / (CHUNK / 8), t = c * CHUNK + o % (CHUNK / 8) * 8;
+            const View<E> &m = o < per ? a.Bm : a.Cm;
+            next[k].load(m.row(b, (int64_t)g * a.N + n), t, n < a.N ? length : 0);
+        }
+        const int n = n0 + tid % kNB, cc = tile * CH + tid / kNB;
+        next_h = 0.f;
+        if (n < a.N && cc < Dg)
+            next_h = a.checkpoints[(((int64_t)b * a.D + g * Dg + cc) * a.p.marks +
+                                    c * CHUNK / SEQ_SCAN_CHECKPOINT) * a.N + n];
+    };
+    prefetch(c_hi - 1, 0);
+    // Sums of a group of states over the waves are read from one half of `sums`
+    // while the next group's are written to the other.
+    int half = 0;
     for (int c = c_hi - 1; c >= c_lo; --c) {
         const int c0 = c * CHUNK, t0 = c0 + lane * T;
         float s[T], u[T], gy[T], total = 0.f;
         {
             float v[T];
-            load_steps<E>(a.dt.row(b, d), t0, len, bias, a.softplus, s);
+            load_steps<E, T>(a.dt.row(b, d), t0, len, bias, a.softplus, s);
             load_row<E, T>(a.x.row(b, d), t0, len, v);
             load_row<E, T>(a.gout.row(b, d), t0, len, gy);
 #pragma unroll
@@ -210,91 +243,107 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
         for (int n0 = 0; n0 < a.N; n0 += kNB) {
             const int nb = std::min(kNB, a.N - n0);
             __syncthreads();
-            stage<E>(a.Bm, b, (int64_t)g * a.N + n0, nb, c0, length, sB, tid, kThreads);
-            stage<E>(a.Cm, b, (int64_t)g * a.N + n0, nb, c0, length, sC, tid, kThreads);
-            for (int i = tid; i < nb * CH; i += kThreads) {
-                const int n = i % nb, cc = i / nb;
-                const int64_t row = (int64_t)b * a.D + g * Dg + tile * CH + cc;
-                sH[n * CH + cc] = tile * CH + cc < Dg
-                                      ? a.checkpoints[(row * a.p.chunks + c) * a.N + n0 + n]
-                                      : 0.f;
-            }
+#pragma unroll
+            for (int k = 0; k < PRE; ++k) stage_octet<E, LANES, T>(sBC, k * kThreads + tid, next[k]);
+            sH[tid % kNB * CH + tid / kNB] = next_h;
             __syncthreads();
-            for (int n1 = 0; n1 < nb; n1 += kNR) {
-                const int nr = std::min(kNR, nb - n1);
-                for (int r = 0; r < nr; ++r) {
+            const bool more = n0 + kNB < a.N;
+            if (more || c > c_lo) prefetch(more ? c : c - 1, more ? n0 + kNB : 0);
+            for (int n1 = 0; n1 < nb; n1 += a.p.joined) {
+                const int nr = std::min(a.p.joined, nb - n1);
+                for (int r = 0; r < nr; r += NI) {
+                    // (States past N have A, B, C and h 0 and change nothing.)
                     const int n = n1 + r, at = (n0 + n) * CH + ch;
-                    const float A2 = sA[at], carry = sG[at], h0 = sH[n * CH + ch];
-                    float da[T], in[T], Bv[T], cg[T], pB[T], pC[T], ah[T];
-                    fetch(sB, n, lane, Bv);
-                    fetch(sC, n, lane, cg);
-                    float hq = 0.f;
+                    float A2[NI], carry[NI], h0[NI], h[NI], q[NI], P[NI], P1[NI], turned[NI];
+                    float da[NI][T], in[NI][T], Bv[NI][T], cg[NI][T], ah[NI][T];
 #pragma unroll
-                    for (int i = 0; i < T; ++i) {
-                        da[i] = exp2_fast(s[i] * A2);
-                        in[i] = u[i] * Bv[i];
-                        hq = __builtin_fmaf(da[i], hq, in[i]);
+                    for (int k = 0; k < NI; ++k) {
+                        A2[k] = sA[at + k * CH];
+                        carry[k] = sG[at + k * CH];
+                        h0[k] = sH[(n + k) * CH + ch];
+                        fetch<T>(sBC + (n + k) * CHUNK, lane, Bv[k]);
+                        h[k] = lane == 0 ? h0[k] : 0.f;
+                        P[k] = exp2_fast(total * A2[k]);
+                        P1[k] = P[k];
                     }
-                    const float P = exp2_fast(total * A2);
-                    const float hs = scan_forth(P, hq, h0, lane);
-                    const float before = dpp0<kRowRor + 1>(hs);
-                    float h = lane == 0 ? h0 : before;
 #pragma unroll
-                    for (int i = 0; i < T; ++i) {
-                        ah[i] = da[i] * h;
-                        h = ah[i] + in[i];
-                        y[i] = __builtin_fmaf(cg[i], h, y[i]);
-                        pC[i] = h * gy[i];
-                        cg[i] *= gy[i];
+                    for (int i = 0; i < T; ++i)
+#pragma unroll
+                        for (int k = 0; k < NI; ++k) {
+                            da[k][i] = exp2_fast(s[i] * A2[k]);
+                            in[k][i] = u[i] * Bv[k][i];
+                            h[k] = __builtin_fmaf(da[k][i], h[k], in[k][i]);
+                        }
+                    scan_lanes<LANES>(h, P1, turned);
+                    float *to = sums + ((half * a.p.joined + r) * 2 * kWaves + wave) * CHUNK +
+                                tid % 64 * F;
+#pragma unroll
+                    for (int k = 0; k < NI; ++k) {
+                        h[k] = lane == 0 ? h0[k] : turned[k];
+                        fetch<T>(sBC + (kNB + n + k) * CHUNK, lane, cg[k]);
+                        float p[T];
+#pragma unroll
+                        for (int i = 0; i < T; ++i) {
+                            ah[k][i] = da[k][i] * h[k];
+                            h[k] = ah[k][i] + in[k][i];
+                            y[i] = __builtin_fmaf(cg[k][i], h[k], y[i]);
+                            p[i] = h[k] * gy[i];
+                            cg[k][i] *= gy[i];
+                        }
+                        *reinterpret_cast<Whole<F> *>(to + (k * 2 + 1) * kWaves * CHUNK) =
+                            meet_rows<T>(p);
+                        // q, the gradient of h; lane 15 starts from what comes from behind.
+                        q[k] = cg[k][T - 1] + (lane == LANES - 1 ? carry[k] : 0.f);
+                        P1[k] = P[k];
                     }
-                    float q = cg[T - 1];
 #pragma unroll
-                    for (int i = T - 2; i >= 0; --i) q = __builtin_fmaf(da[i + 1], q, cg[i]);
-                    const float qs = scan_back(P, da[0] * q, carry, lane);
-                    const float behind = dpp0<kRowRor + 15>(qs);
-                    if (lane == LANES - 1) sG[at] = behind;
-                    q = cg[T - 1] + (lane == LANES - 1 ? carry : behind);
-                    float dA = 0.f;
+                    for (int i = T - 2; i >= 0; --i)
 #pragma unroll
-                    for (int i = T - 1; i >= 0; --i) {
-                        if (i < T - 1) q = __builtin_fmaf(da[i + 1], q, cg[i]);
-                        const float through = q * ah[i];
-                        ds[i] = __builtin_fmaf(A2, through, ds[i]);
-                        dA = __builtin_fmaf(s[i], through, dA);
-                        gB[i] = __builtin_fmaf(q, Bv[i], gB[i]);
-                        pB[i] = q * u[i];
+                        for (int k = 0; k < NI; ++k)
+                            q[k] = __builtin_fmaf(da[k][i + 1], q[k], cg[k][i]);
+#pragma unroll
+                    for (int k = 0; k < NI; ++k) q[k] *= da[k][0];
+                    scan_lanes_back<NI>(q, P1, turned);
+#pragma unroll
+                    for (int k = 0; k < NI; ++k) {
+                        if (lane == LANES - 1) sG[at + k * CH] = turned[k];
+                        q[k] = cg[k][T - 1] + (lane == LANES - 1 ? carry[k] : turned[k]);
+                        if constexpr (T == 16) fetch<T>(sBC + (n + k) * CHUNK, lane, Bv[k]);
+                        float dA = 0.f, p[T];
+#pragma unroll
+                        for (int i = T - 1; i >= 0; --i) {
+                            if (i < T - 1) q[k] = __builtin_fmaf(da[k][i + 1], q[k], cg[k][i]);
+                            p[i] = q[k] * u[i];
+                            const float through = q[k] * ah[k][i];
+                            ds[i] = __builtin_fmaf(A2[k], through, ds[i]);
+                            dA = __builtin_fmaf(s[i], through, dA);
+                            gB[i] = __builtin_fmaf(q[k], Bv[k][i], gB[i]);
+                        }
+                        dA = row_sum(dA);
+                        if (lane == 0) sD[at + k * CH] += dA;
+                        *reinterpret_cast<Whole<F> *>(to + k * 2 * kWaves * CHUNK) =
+                            meet_rows<T>(p);
                     }
-                    dA = row_sum(dA);
-                    if (lane == 0) sD[at] += dA;
-                    // Channels meet: row k of the wave ends with positions 2k, 2k+1 of each lane.
-                    float *to = sums + ((r * 2) * kWaves + wave) * CHUNK + lane * T +
-                                tid % 64 / LANES * 2;
-                    float2 o;
-                    o.x = meet16(meet32(pB[0], pB[4]), meet32(pB[2], pB[6]));
-                    o.y = meet16(meet32(pB[1], pB[5]), meet32(pB[3], pB[7]));
-                    *reinterpret_cast<float2 *>(to) = o;
-                    o.x = meet16(meet32(pC[0], pC[4]), meet32(pC[2], pC[6]));
-                    o.y = meet16(meet32(pC[1], pC[5]), meet32(pC[3], pC[7]));
-                    *reinterpret_cast<float2 *>(to + kWaves * CHUNK) = o;
                 }
                 __syncthreads();
-                for (int i = tid; i < nr * 2 * (CHUNK / 2); i += kThreads) {
-                    const int t = i % (CHUNK / 2) * 2, which = i / (CHUNK / 2);  // [r][B or C]
-                    const float *from = sums + which * kWaves * CHUNK + t;
-                    float2 v = *reinterpret_cast<const float2 *>(from);
+                for (int i = tid; i < nr * 2 * 64; i += kThreads) {
+                    const int f = i % 64, which = i / 64 % 2, r = i / 128;
+                    const float *from =
+                        sums + ((half * a.p.joined + r) * 2 + which) * kWaves * CHUNK + f * F;
+                    Whole<F> v = *reinterpret_cast<const Whole<F> *>(from);
 #pragma unroll
                     for (int w = 1; w < kWaves; ++w) {
-                        const float2 m = *reinterpret_cast<const float2 *>(from + w * CHUNK);
-                        v.x += m.x;
-                        v.y += m.y;
+                        const Whole<F> o = *reinterpret_cast<const Whole<F> *>(from + w * CHUNK);
+#pragma unroll
+                        for (int k = 0; k < F; ++k) v.v[k] += o.v[k];
                     }
                     const int64_t rows = (int64_t)a.B * a.G * a.N;
-                    const int64_t row = ((int64_t)b * a.G + g) * a.N + n0 + n1 + which / 2;
-                    *reinterpret_cast<float2 *>(
-                        a.ws + a.p.sums +
-                        (((int64_t)tile * 2 + which % 2) * rows + row) * a.p.pitch + c0 + t) = v;
+                    const int64_t row = ((int64_t)b * a.G + g) * a.N + n0 + n1 + r;
+                    *reinterpret_cast<Whole<F> *>(
+                        a.ws + a.p.sums + (((int64_t)tile * 2 + which) * rows + row) * a.p.pitch +
+                        c0 + f % 16 * T + f / 16 * F) = v;
                 }
-                if (n1 + kNR < nb) __syncthreads();
+                half ^= 1;
             }
         }
         if (live && t0 < a.L) {
@@ -314,7 +363,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
             }
 #pragma unroll
             for (int i = 0; i < T; ++i) {
-                ds[i] = t0 + i < len ? ds[i] : 0.f;
+                ds[i] = len - t0 > i ? ds[i] : 0.f;
                 sum_bias += ds[i];
             }
             store_row<E, T>(a.ddt.row(b, d), t0, a.L, ds);
@@ -327,7 +376,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
                     const float sg = sigmoid(v[i]);
                     o[i] = go[i] * __builtin_fmaf(skip, x[i], y[i]) *
                            (sg * __builtin_fmaf(v[i], 1.f - sg, 1.f));
-                    o[i] = t0 + i < len ? o[i] : 0.f;
+                    o[i] = len - t0 > i ? o[i] : 0.f;
                 }
                 store_row<E, T>(a.dz.row(b, d), t0, a.L, o);
             }
@@ -355,6 +404,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
 // behind: tails[b][segment][d][n], and its summed steps [b][segment][d].
 template <class E>
 __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tiles) {
+    constexpr int T = kTailT, CHUNK = LANES * T;
     extern __shared__ float lds[];
     float *sC = lds;
     const int NP = (a.N + kNB - 1) / kNB * kNB;
@@ -373,12 +423,12 @@ __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tile
     }
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
     float steps = 0.f;
-    const int c_lo = (int)((int64_t)a.p.chunks * seg / a.p.segments);
-    const int c_hi = (int)((int64_t)a.p.chunks * (seg + 1) / a.p.segments);
-    for (int c = c_hi - 1; c >= c_lo; --c) {
-        const int c0 = c * CHUNK, t0 = c0 + lane * T;
+    const int lo = (int)((int64_t)a.p.chunks * seg / a.p.segments) * a.p.chunk;
+    const int hi = (int)((int64_t)a.p.chunks * (seg + 1) / a.p.segments) * a.p.chunk;
+    for (int c0 = hi - CHUNK; c0 >= lo; c0 -= CHUNK) {
+        const int t0 = c0 + lane * T;
         float s[T], gy[T], total = 0.f;
-        load_steps<E>(a.dt.row(b, d), t0, len, bias, a.softplus, s);
+        load_steps<E, T>(a.dt.row(b, d), t0, len, bias, a.softplus, s);
         load_row<E, T>(a.gout.row(b, d), t0, len, gy);
 #pragma unroll
         for (int i = 0; i < T; ++i) total += s[i];
@@ -392,19 +442,25 @@ __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tile
         for (int n0 = 0; n0 < a.N; n0 += kNB) {
             const int nb = std::min(kNB, a.N - n0);
             __syncthreads();
-            stage<E>(a.Cm, b, (int64_t)g * a.N + n0, nb, c0, len, sC, tid, kTailThreads);
+            for (int o = tid; o < nb * (CHUNK / 8); o += kTailThreads) {
+                Octet<E> v;
+                v.load(a.Cm.row(b, (int64_t)g * a.N + n0 + o / (CHUNK / 8)),
+                       c0 + o % (CHUNK / 8) * 8, len);
+                stage_octet<E, LANES, T>(sC, o, v);
+            }
             __syncthreads();
             for (int n = 0; n < nb; ++n) {
                 const int at = (n0 + n) * kTailCH + ch;
                 const float A2 = sA[at], carry = sG[at];
                 float Cv[T];
-                fetch(sC, n, lane, Cv);
-                float q = 0.f;
+                fetch<T>(sC + n * CHUNK, lane, Cv);
+                float q = lane == LANES - 1 ? carry : 0.f;
 #pragma unroll
                 for (int i = T - 1; i >= 0; --i)
                     q = exp2_fast(s[i] * A2) * __builtin_fmaf(Cv[i], gy[i], q);
-                const float qs = scan_back(exp2_fast(total * A2), q, carry, lane);
-                if (lane == 0) sG[at] = qs;
+                float P = exp2_fast(total * A2), turned;
+                scan_chain_back(q, P, turned);
+                if (lane == 0) sG[at] = q;
             }
         }
     }
@@ -446,26 +502,38 @@ __global__ __launch_bounds__(256) void scan_join(const float *ws, Plan p, int64_
                                                  const int32_t *lengths, int64_t matrix_blocks) {
     const int64_t rows = B * G * N;
     if (blockIdx.x < matrix_blocks) {
-        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        // 64 runs of 4 positions a work-group, its waves over every fourth tile each.
+        __shared__ float4 part[4][64];
+        const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+        const int wave = threadIdx.x / 64;
         const int64_t per_row = p.pitch / 4;
         const int64_t r = i / per_row, t = i % per_row * 4;
-        if (r >= 2 * rows || t >= L) return;
+        const bool here = r < 2 * rows && t < L;
         const float *from = ws + p.sums + r * p.pitch + t;
         float4 v = {0.f, 0.f, 0.f, 0.f};
-        for (int tile = 0; tile < p.tiles; ++tile) {
+        for (int tile = wave; here && tile < p.tiles; tile += 4) {
             const float4 m = *reinterpret_cast<const float4 *>(from + tile * 2 * rows * p.pitch);
             v.x += m.x;
             v.y += m.y;
             v.z += m.z;
             v.w += m.w;
         }
+        part[wave][threadIdx.x % 64] = v;
+        __syncthreads();
+        if (wave || !here) return;
         float out[4] = {v.x, v.y, v.z, v.w};
+        for (int w = 1; w < 4; ++w) {
+            const float4 m = part[w][threadIdx.x];
+            out[0] += m.x;
+            out[1] += m.y;
+            out[2] += m.z;
+            out[3] += m.w;
+        }
         const int64_t br = r < rows ? r : r - rows;
         const int len = length_of(lengths, br / (G * N), (int)L);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = t + i < len ? out[i] : 0.f;
-        typename E::type *to = (r < rows ? dB : dC) + br * L;
-        store_row<E, 4>(to, t, L, out);
+        for (int k = 0; k < 4; ++k) out[k] = t + k < len ? out[k] : 0.f;
+        store_row<E, 4>((r < rows ? dB : dC) + br * L, (int)t, (int)L, out);
         return;
     }
     const int64_t i = (blockIdx.x - matrix_blocks) * 256 + threadIdx.x;
@@ -494,7 +562,7 @@ hipError_t backward(const state_scan_backward_args &a, hipStream_t s) {
     hipError_t e;
     if (p.segments > 1) {
         const int tiles = (a.D / a.G + kTailCH - 1) / kTailCH;
-        const size_t bytes = (kNB * CHUNK + 2 * (size_t)NP * kTailCH) * sizeof(float);
+        const size_t bytes = (kNB * LANES * kTailT + 2 * (size_t)NP * kTailCH) * sizeof(float);
         scan_tail<E><<<dim3((unsigned)(a.G * tiles), (unsigned)a.B, (unsigned)p.segments),
                        kTailThreads, bytes, s>>>(k, tiles);
         if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -503,17 +571,16 @@ hipError_t backward(const state_scan_backward_args &a, hipStream_t s) {
                                                                     a.D, a.N);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    const size_t bytes = (2 * kNB * CHUNK + kNR * 2 * kWaves * CHUNK + kNB * CH +
-                          3 * (size_t)NP * CH) * sizeof(float);
-    if (bytes > 64 * 1024) {
-        e = hipFuncSetAttribute((const void *)scan_backward<E>,
-                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const auto kernel = p.T == 16 ? scan_backward<E, 16, 1> : scan_backward<E, 8, 2>;
+    if (p.lds > 64 * 1024) {
+        e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)p.lds);
         if (e != hipSuccess) return e;
     }
-    scan_backward<E><<<dim3((unsigned)(a.G * p.tiles), (unsigned)a.B, (unsigned)p.segments),
-                       kThreads, bytes, s>>>(k);
+    kernel<<<dim3((unsigned)(a.G * p.tiles), (unsigned)a.B, (unsigned)p.segments), kThreads, p.lds,
+             s>>>(k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t matrix = (2 * (int64_t)a.B * a.G * a.N * (p.pitch / 4) + 255) / 256;
+    const int64_t matrix = (2 * (int64_t)a.B * a.G * a.N * (p.pitch / 4) + 63) / 64;
     const int64_t params = ((int64_t)a.D * (a.N + 2) + 255) / 256;
     scan_join<E><<<dim3((unsigned)(matrix + params)), 256, 0, s>>>(
         k.ws, p, a.B, a.D, a.L, a.N, a.G, static_cast<typename E::type *>(a.dBm),

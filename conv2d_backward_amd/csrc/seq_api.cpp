@@ -32,8 +32,9 @@ int check_taps(int32_t K) {
 int check_states(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
     if (N < 1 || G < 1 || D % G != 0) return CONV2D_GI_EINVAL;
     if (N > SEQ_MAX_STATES) return CONV2D_GI_EUNSUPPORTED;
-    // The join of dB and dC walks every padded position of [2, B, G, N, L] in one grid.
-    if (B * G * N > ((int64_t)1 << 40) / (L + 128)) return CONV2D_GI_EUNSUPPORTED;
+    // The join of dB and dC is one grid over 4-position runs of [2, B, G, N, L], 64 to
+    // a work-group of 256, and a grid has less than 2^32 work-items.
+    if (B * G * N > ((int64_t)1 << 30) / (L + 256)) return CONV2D_GI_EUNSUPPORTED;
     return CONV2D_GI_OK;
 }
 

@@ -236,6 +236,35 @@ __device__ __forceinline__ void scan_chains(float &h0, float &h1, float &P0, flo
     }
 }
 
+// The same from the right over 16 lanes: h becomes the composition of lanes
+// 15 .. l, turned lane l+1's result, in lane 15 lane 0's.
+__device__ __forceinline__ void scan_chain_back(float &h, float &P, float &turned) {
+    asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP1, "shl")
+        "v_fmac_f32_dpp %0, %0, %1 row_shl:8" SEQ_ALL "\n\ts_nop 1\n\t"
+        "v_mov_b32_dpp %2, %0 row_ror:15" SEQ_ALL
+        : "+v"(h), "+v"(P), "=&v"(turned));
+}
+__device__ __forceinline__ void scan_chains_back(float &h0, float &h1, float &P0, float &P1,
+                                                 float &turned0, float &turned1) {
+    asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP2, "shl")
+        "v_fmac_f32_dpp %0, %0, %2 row_shl:8" SEQ_ALL "\n\t"
+        "v_fmac_f32_dpp %1, %1, %3 row_shl:8" SEQ_ALL "\n\ts_nop 0\n\t"
+        "v_mov_b32_dpp %4, %0 row_ror:15" SEQ_ALL "\n\t"
+        "v_mov_b32_dpp %5, %1 row_ror:15" SEQ_ALL
+        : "+v"(h0), "+v"(h1), "+v"(P0), "+v"(P1), "=&v"(turned0), "=&v"(turned1));
+}
+template <int NI>
+__device__ __forceinline__ void scan_lanes_back(float (&h)[NI], float (&P)[NI],
+                                                float (&turned)[NI]) {
+    if constexpr (NI == 1) {
+        scan_chain_back(h[0], P[0], turned[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < NI; k += 2)
+            scan_chains_back(h[k], h[k + 1], P[k], P[k + 1], turned[k], turned[k + 1]);
+    }
+}
+
 template <int LANES, int NI>
 __device__ __forceinline__ void scan_lanes(float (&h)[NI], float (&P)[NI], float (&turned)[NI]) {
     if constexpr (NI == 1) {
@@ -249,5 +278,19 @@ __device__ __forceinline__ void scan_lanes(float (&h)[NI], float (&P)[NI], float
 
 // v of lane ^ M.
 __device__ __forceinline__ float lane_xor(float v, int m) { return __shfl_xor(v, m, 64); }
+
+// Octet o of a group of states goes where its lanes read it: [state][T/4][LANES][4].
+template <class E, int LANES, int T>
+__device__ __forceinline__ void stage_octet(float *to, int o, const Octet<E> &v) {
+    constexpr int PER = LANES * T / 8;  // octets of a state
+    const int n = o / PER, t = o % PER * 8;
+    float4 *p = reinterpret_cast<float4 *>(to + n * (LANES * T));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int lane = (t + 4 * h) / T, q = (t + 4 * h) % T / 4;
+        p[q * LANES + lane] =
+            float4{v.at(4 * h), v.at(4 * h + 1), v.at(4 * h + 2), v.at(4 * h + 3)};
+    }
+}
 
 }  // namespace seq
