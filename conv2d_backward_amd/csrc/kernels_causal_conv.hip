@@ -175,7 +175,12 @@ __global__ __launch_bounds__(kThreads) void conv_backward(ConvBwd<E> a) {
                 load_row<E, kV>(x, t0, len, own);
 #pragma unroll
                 for (int j = 0; j < kV; ++j) xs[K - 1 + j] = own[j];
-                load_row<E, kV>(x, t0 - kV, len, own);
+                if (t0 > 0) {
+                    load_row<E, kV>(x, t0 - kV, len, own);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) own[j] = 0.f;
+                }
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) xs[j] = own[kV - (K - 1) + j];
                 load_row<E, kV>(x, t0 + kV, len, own);

@@ -82,10 +82,11 @@ __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
 #pragma unroll
         for (int k = 0; k < PRE; ++k) {
             const int o = k * kThreads + tid, n = n0 + o / (CHUNK / 8);
-            const int t = c + o % (CHUNK / 8) * 8, end_n = n < a.N ? len : 0;  // past N: zeros
+            const int t = c + o % (CHUNK / 8) * 8;
+            const int left = n < a.N ? len - t : 0;  // past N: zeros
             const int64_t state = (int64_t)g * a.N + n;
-            next[k].load(a.Bm.row(b, state), t, end_n);
-            next[PRE + k].load(a.Cm.row(b, state), t, end_n);
+            next[k].load(a.Bm.row(b, state) + t, left);
+            next[PRE + k].load(a.Cm.row(b, state) + t, left);
         }
     };
     if (end > 0) prefetch(0, 0);

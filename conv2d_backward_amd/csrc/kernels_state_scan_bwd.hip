@@ -121,38 +121,6 @@ __device__ __forceinline__ void fetch(const float *from, int lane, float (&v)[T]
     }
 }
 
-// x summed over the half waves in lanes 0..31, y in lanes 32..63.
-__device__ __forceinline__ float meet32(float x, float y) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x),
-                                                    __builtin_bit_cast(unsigned, y), false, false);
-    const unsigned p = r[0], q = r[1];
-    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
-}
-// x summed over the two rows of 16 lanes of each half in its first row, y in its second.
-__device__ __forceinline__ float meet16(float x, float y) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
-                                                    __builtin_bit_cast(unsigned, y), false, false);
-    const unsigned p = r[0], q = r[1];
-    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
-}
-
-// F floats at an address that is a multiple of their size.
-template <int F>
-struct alignas(4 * F) Whole {
-    float v[F];
-};
-
-// A wave's four channels meet: row k of 16 lanes ends with the sums of positions
-// k T/4 .. (k+1) T/4 - 1 of each lane.
-template <int T>
-__device__ __forceinline__ Whole<T / 4> meet_rows(const float (&v)[T]) {
-    Whole<T / 4> sum;
-#pragma unroll
-    for (int i = 0; i < T / 4; ++i)
-        sum.v[i] = meet16(meet32(v[i], v[T / 2 + i]), meet32(v[T / 4 + i], v[3 * T / 4 + i]));
-    return sum;
-}
-
 // A work-group: 8 waves of 4 channels, 16 lanes a channel, T positions a lane,
 // NI states at a time.
 template <class E, int T, int NI>
@@ -206,7 +174,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
             const int o = k * kThreads + tid, per = kNB * CHUNK / 8;
             const int n = n0 + o % per / (CHUNK / 8), t = c * CHUNK + o % (CHUNK / 8) * 8;
             const View<E> &m = o < per ? a.Bm : a.Cm;
-            next[k].load(m.row(b, (int64_t)g * a.N + n), t, n < a.N ? length : 0);
+            next[k].load(m.row(b, (int64_t)g * a.N + n) + t, n < a.N ? length - t : 0);
         }
         const int n = n0 + tid % kNB, cc = tile * CH + tid / kNB;
         next_h = 0.f;
@@ -444,8 +412,8 @@ __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tile
             __syncthreads();
             for (int o = tid; o < nb * (CHUNK / 8); o += kTailThreads) {
                 Octet<E> v;
-                v.load(a.Cm.row(b, (int64_t)g * a.N + n0 + o / (CHUNK / 8)),
-                       c0 + o % (CHUNK / 8) * 8, len);
+                const int t = c0 + o % (CHUNK / 8) * 8;
+                v.load(a.Cm.row(b, (int64_t)g * a.N + n0 + o / (CHUNK / 8)) + t, len - t);
                 stage_octet<E, LANES, T>(sC, o, v);
             }
             __syncthreads();

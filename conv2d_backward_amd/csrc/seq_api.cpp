@@ -185,8 +185,7 @@ int block_norm_backward(const block_norm_backward_args *a, hipStream_t stream) {
     if (!is_apart(a->dy, a->B, a->D, a->L) || !is_apart(a->dr, a->B, a->D, a->L) ||
         (a->dgate.data && !is_apart(a->dgate, a->B, a->D, a->L)))
         return CONV2D_GI_EINVAL;
-    if ((a->dscale || a->dw_post || a->dw_pre) &&
-        !is_workspace(a->workspace, a->workspace_bytes,
+    if (!is_workspace(a->workspace, a->workspace_bytes,
                       seq::norm_workspace(a->B, a->D, a->L, 1)))
         return CONV2D_GI_EINVAL;
     return status(seq::launch_norm_backward(*a, stream));

@@ -75,38 +75,42 @@ __device__ __forceinline__ void store_vec(typename E::type *p, const float (&in)
     }
 }
 
-// Positions t .. t+V-1 of a row; those outside [0, end) are 0 and not read.
+// Positions t .. t+V-1 of a row (t >= 0); those from `end` on are 0 and not read.
 template <class E, int V>
 __device__ __forceinline__ void load_row(const typename E::type *row, int t, int end,
                                          float (&out)[V]) {
     const typename E::type *p = row + t;
-    if (t >= 0 && end - t >= V) {
+    const int left = end - t;
+    if (left >= V) {
         load_vec<E, V>(p, out);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             out[i] = 0.f;
-            if (t >= -i && end - t > i) out[i] = E::up(p[i]);
+            if (left > i) out[i] = E::up(p[i]);
         }
     }
 }
 
 // Eight positions as they are stored, for a load whose use comes later; those
-// outside [0, end) are 0 and not read.
+// from the left-th on are 0 and not read.
 template <class E>
 struct Octet {
     typename Vec<typename E::type, 8>::type v;
-    __device__ __forceinline__ void load(const typename E::type *row, int t, int end) {
-        const typename E::type *p = row + t;
-        if (end - t >= 8) {
+    __device__ __forceinline__ void load(const typename E::type *p, int left) {
+        if (left >= 8) {
             v = *reinterpret_cast<const typename Vec<typename E::type, 8>::type *>(p);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[i] = 0;
-                if (end - t > i) v[i] = p[i];
+                if (left > i) v[i] = p[i];
             }
         }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0;
     }
     __device__ __forceinline__ float at(int i) const {
         const typename E::type e = v[i];
@@ -274,6 +278,38 @@ __device__ __forceinline__ void scan_lanes(float (&h)[NI], float (&P)[NI], float
         for (int k = 0; k < NI; k += 2)
             scan_chains<LANES>(h[k], h[k + 1], P[k], P[k + 1], turned[k], turned[k + 1]);
     }
+}
+
+// x summed over the half waves in lanes 0..31, y in lanes 32..63.
+__device__ __forceinline__ float meet32(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x),
+                                                    __builtin_bit_cast(unsigned, y), false, false);
+    const unsigned p = r[0], q = r[1];
+    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
+}
+// x summed over the two rows of 16 lanes of each half in its first row, y in its second.
+__device__ __forceinline__ float meet16(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x),
+                                                    __builtin_bit_cast(unsigned, y), false, false);
+    const unsigned p = r[0], q = r[1];
+    return __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q);
+}
+
+// F floats at an address that is a multiple of their size.
+template <int F>
+struct alignas(4 * F) Whole {
+    float v[F];
+};
+
+// Sums over the four rows of 16 lanes: row k ends with those of values k T/4 ..
+// (k+1) T/4 - 1 of each of its lanes.
+template <int T>
+__device__ __forceinline__ Whole<T / 4> meet_rows(const float (&v)[T]) {
+    Whole<T / 4> sum;
+#pragma unroll
+    for (int i = 0; i < T / 4; ++i)
+        sum.v[i] = meet16(meet32(v[i], v[T / 2 + i]), meet32(v[T / 4 + i], v[3 * T / 4 + i]));
+    return sum;
 }
 
 // v of lane ^ M.
