@@ -3,6 +3,7 @@
 Usage: ``python -m conv2d_backward_amd.build`` (or ``build()`` from Python).
 Each source compiles to an object under ``_build/`` at the repository root,
 in parallel; the objects link into ``conv2d_backward_amd/libconv2d_gi.so``.
+Beside it ``_sequence.so`` is built, the extension module behind sequence.py.
 """
 from __future__ import annotations
 
@@ -48,6 +49,33 @@ DEVICE = ["-x", "hip", "--offload-arch=" + ARCH,
           "-Wno-unused-command-line-argument"]
 
 
+# The extension module behind sequence.py: host code against torch's C++ API.
+BINDING = "seq_binding.cpp"
+BINDING_PATH = os.path.join(PKG, "_sequence.so")
+
+
+def _build_binding() -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-Wall", "-Werror", "-Wno-sign-compare",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, BINDING), "-o", tmp, "-L", lib, "-Wl,-rpath," + lib,
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (BINDING, " ".join(cmd), r.stderr))
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def _compile(src: str) -> str:
     path = os.path.join(CSRC, src)
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
@@ -67,7 +95,9 @@ def build(verbose: bool = False) -> str:
     """Compile every source for gfx950 and link the shared library (always rebuilds)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

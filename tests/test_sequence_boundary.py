@@ -2,8 +2,10 @@
 is refused before any HIP call (the fake pointers are never touched).  No test
 here launches a kernel, so they run without a GPU.
 """
+import ctypes
 import os
 import re
+import struct
 
 import pytest
 
@@ -39,10 +41,18 @@ def fields_of(name):
     return out
 
 
-STRUCTS = {"causal_conv": sequence._CONV, "causal_conv_backward": sequence._CONV_BACKWARD,
-           "causal_conv_step": sequence._CONV_STEP, "state_scan": sequence._SCAN,
-           "state_scan_backward": sequence._SCAN_BACKWARD, "state_scan_step": sequence._SCAN_STEP,
-           "block_norm": sequence._NORM, "block_norm_backward": sequence._NORM_BACKWARD}
+def format_of(name):
+    """The struct format of an argument struct: its int32 and float fields, then 8-byte ones."""
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    body = re.search(r"typedef struct %s_args \{(.*?)\}" % name, text, re.S).group(1)
+    small = re.findall(r"\b(int32_t|float) ([^;*]*);", body)
+    kinds = "".join(("i" if t == "int32_t" else "f") * len(names.split(",")) for t, names in small)
+    return struct.Struct(kinds + "%dq" % (len(fields_of(name)) - len(kinds)))
+
+
+STRUCTS = {n: format_of(n) for n in ("causal_conv", "causal_conv_backward", "causal_conv_step", "state_scan",
+                                     "state_scan_backward", "state_scan_step", "block_norm",
+                                     "block_norm_backward")}
 ENTRIES = {"causal_conv": "causal_conv_forward", "state_scan": "state_scan_forward",
            "block_norm": "block_norm_forward"}
 SIZES = {"B": 2, "D": 4, "L": 10, "K": 4, "N": 3, "G": 2, "lines": 2, "dtype": 0, "eps": 1e-6,
@@ -58,7 +68,27 @@ def call(name, **change):
         if f.endswith(".channel"):
             v = 10
         values.append(change.get(f, v))
-    return sequence._entry(ENTRIES.get(name, name))(STRUCTS[name].pack(*values), None)
+    return getattr(gi.load_library(), ENTRIES.get(name, name))(STRUCTS[name].pack(*values), None)
+
+
+def workspace(name, *sizes):
+    fn = getattr(gi.load_library(), name)
+    fn.restype = ctypes.c_int64
+    return fn(*sizes)
+
+
+def test_binding_describes_the_structs(lib):
+    """The binding's operands are the fields of the header's structs, in order."""
+    for name in STRUCTS:
+        header, _, scratch, operands = sequence._ENTRIES[ENTRIES.get(name, name)]
+        fields = [f for f in fields_of(name) if "." not in f]
+        sizes = header.split()
+        assert len(fields) == 1 + len(sizes) + len(operands) + (2 if scratch else 0), name
+        for f, s in zip(fields[1:], sizes):
+            assert f == s, name
+        wide = {f.split(".")[0] for f in fields_of(name) if "." in f}
+        for f, o in zip(fields[1 + len(sizes):], operands):
+            assert (f in wide) == (o[1] in (sequence._ACT, sequence._ACT32, sequence._STATES)), (name, f)
 
 
 NEEDED = {
@@ -127,13 +157,13 @@ def test_refuses_workspaces(lib, name):
 
 
 def test_workspace_sizes(lib):
-    assert sequence._entry("causal_conv_workspace")(2, 4, 10, 4) >= 0
-    assert sequence._entry("state_scan_workspace")(2, 4, 10, 3, 2) > 0
-    assert sequence._entry("block_norm_workspace")(2, 4, 10, 1) > 0
+    assert workspace("causal_conv_workspace", 2, 4, 10, 4) >= 0
+    assert workspace("state_scan_workspace", 2, 4, 10, 3, 2) > 0
+    assert workspace("block_norm_workspace", 2, 4, 10, 1) > 0
     # invalid sizes
-    assert sequence._entry("causal_conv_workspace")(2, 4, 10, 9) == -1
-    assert sequence._entry("state_scan_workspace")(2, 4, 10, 3, 3) == -1
-    assert sequence._entry("block_norm_workspace")(2, 0, 10, 1) == -1
+    assert workspace("causal_conv_workspace", 2, 4, 10, 9) == -1
+    assert workspace("state_scan_workspace", 2, 4, 10, 3, 3) == -1
+    assert workspace("block_norm_workspace", 2, 0, 10, 1) == -1
 
 
 def test_gate_and_gradient_come_together(lib):
