@@ -37,21 +37,32 @@ struct ConvFwd {
     int silu;
 };
 
-// Threads [row][position octet]; grid.x over rows, grid.y over the row's rest.
-template <class E, int K>
+// Threads [row][position octet]; grid.x over rows, grid.y over the row's rest.  A
+// thread has R octets, `row_threads` octets apart, all on their way together.
+template <class E, int K, int R>
 __global__ __launch_bounds__(kThreads) void conv_forward(ConvFwd<E> a) {
-    const int rows = kThreads / a.row_threads;
+    const int rows = kThreads / a.row_threads, lane = threadIdx.x % a.row_threads;
     const int64_t r = (int64_t)blockIdx.x * rows + threadIdx.x / a.row_threads;
     if (r >= (int64_t)a.B * a.D) return;
     const int b = (int)(r / a.D), d = (int)(r - (int64_t)b * a.D);
-    const int t0 = (int)(blockIdx.y * a.row_threads + threadIdx.x % a.row_threads) * kV;
+    const int start = (int)(blockIdx.y * R) * a.row_threads * kV;
     const int len = length_of(a.lengths, b, a.L);
     const auto *x = a.x.row(b, d);
-    float past[K];  // K-1 used
-    if (t0 == 0) {
+    Octet<E> own[R];
+#pragma unroll
+    for (int c = 0; c < R; ++c) {
+        // (All of the row: what lies beyond the length reaches no output before it, and
+        // the length need not be there yet.)
+        const int t = start + (c * a.row_threads + lane) * kV;
+        own[c].load(x + t, a.L - t);
+    }
+    float past[K], w[K];  // K-1 of past used
+#pragma unroll
+    for (int j = 0; j < K; ++j) past[j] = 0.f;
+    if (start == 0 && lane == 0) {
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
-            past[j] = a.state_in ? E::up(a.state_in[r * (K - 1) + j]) : 0.f;
+            if (a.state_in) past[j] = E::up(a.state_in[r * (K - 1) + j]);
         if (a.state_out) {
             // The last K-1 positions of the sequence; of the given state where it is shorter.
 #pragma unroll
@@ -69,42 +80,45 @@ __global__ __launch_bounds__(kThreads) void conv_forward(ConvFwd<E> a) {
             }
         }
     }
-    if (t0 >= a.L) return;
-    float out[kV];
-    if (t0 >= len) {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) out[i] = 0.f;
-        store_row<E, kV>(a.y.row(b, d), t0, a.L, out);
-        return;
-    }
-    float v[kV + K];
-    {
-        float own[kV];
-        load_row<E, kV>(x, t0, len, own);
-        if (t0 > 0) {
-            float before[kV];
-            load_vec<E, kV>(x + t0 - kV, before);
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) past[j] = before[kV - (K - 1) + j];
-        }
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) v[j] = past[j];
-#pragma unroll
-        for (int i = 0; i < kV; ++i) v[K - 1 + i] = own[i];
-    }
-    float w[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) w[k] = a.w[(int64_t)d * K + k];
     const float bias = a.bias ? a.bias[d] : 0.f;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        float p = bias;
+    for (int c = 0; c < R; ++c) {
+        const int t0 = start + (c * a.row_threads + lane) * kV, left = len - t0;
+        float v[kV + K], out[kV];
 #pragma unroll
-        for (int k = 0; k < K; ++k) p = __builtin_fmaf(w[k], v[i + k], p);
-        const float q = a.silu ? p * sigmoid(p) : p;
-        out[i] = t0 + i < len ? q : 0.f;
+        for (int i = 0; i < kV; ++i) v[K - 1 + i] = own[c].at(i);
+        // The positions before: the lane before's last; for a wave's first lane its last
+        // lane's of the octet before, or a read of them.
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            v[j] = dpp0<kWaveShr>(v[kV + j]);
+            if (c > 0) {
+                const float turned = dpp0<kWaveRor>(own[c > 0 ? c - 1 : 0].at(kV - (K - 1) + j));
+                if (lane == 0) v[j] = turned;
+            }
+        }
+        if (c == 0 && threadIdx.x % 64 == 0 && t0 > 0 && left > 0) {
+            Octet<E> o;
+            o.load(x + t0 - kV, 8);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) v[j] = o.at(kV - (K - 1) + j);
+        }
+        if (t0 == 0) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) v[j] = past[j];
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            float p = bias;
+#pragma unroll
+            for (int k = 0; k < K; ++k) p = __builtin_fmaf(w[k], v[i + k], p);
+            const float q = a.silu ? p * sigmoid(p) : p;
+            out[i] = left > i ? q : 0.f;
+        }
+        if (t0 < a.L) store_row<E, kV>(a.y.row(b, d), t0, a.L, out);
     }
-    store_row<E, kV>(a.y.row(b, d), t0, a.L, out);
 }
 
 // How the threads of a backward work-group are dealt: `along` along a row,
@@ -129,6 +143,11 @@ BwdShape bwd_shape(int B, int D, int L) {
     const int64_t want = (2048 + tiles - 1) / tiles;
     s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(list, want), 65535));
     return s;
+}
+
+__device__ __forceinline__ float silu_slope(float p) {
+    const float s = sigmoid(p);
+    return s * (1.f + p * (1.f - s));
 }
 
 template <class E>
@@ -156,72 +175,99 @@ __global__ __launch_bounds__(kThreads) void conv_backward(ConvBwd<E> a) {
     float sums[K + 1];
 #pragma unroll
     for (int k = 0; k <= K; ++k) sums[k] = 0.f;
-    if (d < a.D) {
-        float w[K];
+    const bool channel = d < a.D;
+    float w[K], bias = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = a.w[(int64_t)d * K + k];
-        const float bias = a.bias ? a.bias[d] : 0.f;
-        for (int i = first; i < last; ++i) {
-            const int b = i / a.s.segments * a.s.batch + bb;
-            const int t0 = (i % a.s.segments * along + lane) * kV;
-            if (b >= a.B || t0 >= a.L) continue;
-            const int len = length_of(a.lengths, b, a.L);
-            const auto *x = a.x.row(b, d);
-            const auto *gy = a.gy.row(b, d);
-            // Positions t0-(K-1) .. t0+V-1+(K-1) of x, from t0 of gy.
-            float xs[kV + 2 * (K - 1) + 1], dp[kV + K];
-            {
-                float own[kV];
-                load_row<E, kV>(x, t0, len, own);
+    for (int k = 0; k < K; ++k) w[k] = channel ? a.w[(int64_t)d * K + k] : 0.f;
+    if (channel && a.bias) bias = a.bias[d];
+    // Each wave's first dp, for the lane before it.
+    __shared__ float edge[2][kThreads / 64 + 1][K];
+    const int wave = threadIdx.x / 64;
+    for (int i = first; i < last; ++i) {
+        const int b = i / a.s.segments * a.s.batch + bb;
+        const int t0 = (i % a.s.segments * along + lane) * kV;
+        const bool here = channel && b < a.B && t0 < a.L;
+        const int len = here ? length_of(a.lengths, b, a.L) : 0, left = len - t0;
+        const auto *x = a.x.row(here ? b : 0, here ? d : 0);
+        const auto *gy = a.gy.row(here ? b : 0, here ? d : 0);
+        // x of positions t0-(K-1) .. t0+V-1, dp of t0 .. t0+V-1+(K-1).
+        float xs[kV + K], dp[kV + K], own[kV], g[kV];
+        load_row<E, kV>(x, t0, len, own);
+        load_row<E, kV>(gy, t0, len, g);
 #pragma unroll
-                for (int j = 0; j < kV; ++j) xs[K - 1 + j] = own[j];
-                if (t0 > 0) {
-                    load_row<E, kV>(x, t0 - kV, len, own);
-                } else {
+        for (int j = 0; j < kV; ++j) {
+            xs[K - 1 + j] = own[j];
+            dp[j] = g[j];
+        }
 #pragma unroll
-                    for (int j = 0; j < kV; ++j) own[j] = 0.f;
-                }
+        for (int j = 0; j < K - 1; ++j) xs[j] = dpp0<kWaveShr>(own[kV - (K - 1) + j]);
+        if (threadIdx.x % 64 == 0 && t0 > 0) {
+            load_row<E, kV>(x, t0 - kV, len, own);
 #pragma unroll
-                for (int j = 0; j < K - 1; ++j) xs[j] = own[kV - (K - 1) + j];
-                load_row<E, kV>(x, t0 + kV, len, own);
+            for (int j = 0; j < K - 1; ++j) xs[j] = own[kV - (K - 1) + j];
+        }
+        if (t0 == 0) {
 #pragma unroll
-                for (int j = 0; j < K - 1; ++j) xs[K - 1 + kV + j] = own[j];
-                load_row<E, kV>(gy, t0, len, own);
-#pragma unroll
-                for (int j = 0; j < kV; ++j) dp[j] = own[j];
-                load_row<E, kV>(gy, t0 + kV, len, own);
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) dp[kV + j] = own[j];
-            }
-            if (a.silu) {
-#pragma unroll
-                for (int j = 0; j < kV + K - 1; ++j) {
-                    float p = bias;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) p = __builtin_fmaf(w[k], xs[j + k], p);
-                    const float sg = sigmoid(p);
-                    // (Beyond the length p may come from NaN inside it.)
-                    dp[j] = t0 + j < len ? dp[j] * (sg * (1.f + p * (1.f - sg))) : 0.f;
-                }
-            }
-            if (a.dx.p) {
-                float out[kV];
-#pragma unroll
-                for (int j = 0; j < kV; ++j) {
-                    out[j] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        out[j] = __builtin_fmaf(w[K - 1 - k], dp[j + k], out[j]);
-                }
-                store_row<E, kV>(a.dx.row(b, d), t0, a.L, out);
-            }
+            for (int j = 0; j < K - 1; ++j) xs[j] = 0.f;
+        }
+        if (a.silu) {
 #pragma unroll
             for (int j = 0; j < kV; ++j) {
+                float p = bias;
 #pragma unroll
-                for (int k = 0; k < K; ++k) sums[k] = __builtin_fmaf(dp[j], xs[j + k], sums[k]);
-                sums[K] += dp[j];
+                for (int k = 0; k < K; ++k) p = __builtin_fmaf(w[k], xs[j + k], p);
+                // (Beyond the length p may come from NaN inside it.)
+                dp[j] = left > j ? dp[j] * silu_slope(p) : 0.f;
             }
         }
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) sums[k] = __builtin_fmaf(dp[j], xs[j + k], sums[k]);
+            sums[K] += dp[j];
+        }
+        if (!a.dx.p) continue;
+        // The next positions' dp: the lane after's first, or the wave after's; the last
+        // lane of a piece of a longer row works them out.
+        if (K > 1 && along > 64) {
+            if (threadIdx.x % 64 == 0) {
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) edge[i & 1][wave][j] = dp[j];
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            dp[kV + j] = dpp0<kWaveShl>(dp[j]);
+            if (along > 64 && threadIdx.x % 64 == 63) dp[kV + j] = edge[i & 1][wave + 1][j];
+            if (left <= kV) dp[kV + j] = 0.f;
+        }
+        if (left > kV && lane == along - 1) {
+            float xn[kV], gn[kV], tail[2 * K];
+            load_row<E, kV>(x, t0 + kV, len, xn);
+            load_row<E, kV>(gy, t0 + kV, len, gn);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                tail[j] = xs[kV + j];
+                tail[K - 1 + j] = xn[j];
+            }
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                float p = bias;
+#pragma unroll
+                for (int k = 0; k < K; ++k) p = __builtin_fmaf(w[k], tail[j + k], p);
+                dp[kV + j] = left > kV + j ? (a.silu ? gn[j] * silu_slope(p) : gn[j]) : 0.f;
+            }
+        }
+        if (!here) continue;
+        float out[kV];
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            out[j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) out[j] = __builtin_fmaf(w[K - 1 - k], dp[j + k], out[j]);
+        }
+        store_row<E, kV>(a.dx.row(b, d), t0, a.L, out);
     }
     if (!a.dw && !a.db) return;
     // Sum over the threads of a channel: within waves, then over its waves in order.
@@ -325,13 +371,18 @@ hipError_t forward(const causal_conv_args &a, hipStream_t s) {
                  static_cast<const typename E::type *>(a.state_in),
                  static_cast<typename E::type *>(a.state_out), a.lengths, a.B, a.D, a.L, 0,
                  a.silu};
+    // Rows of more than two waves' octets go to one wave, four octets a lane: fewer
+    // waves to start and no reads at their borders.
     const int64_t octets = ((int64_t)a.L + kV - 1) / kV;
-    k.row_threads = pow2_at_least(octets, kThreads);
-    const int64_t rows = kThreads / k.row_threads;
+    const int R = octets > 128 ? 4 : 1;
+    k.row_threads = R == 4 ? 64 : pow2_at_least(octets, kThreads);
+    const int64_t rows = kThreads / k.row_threads, span = (int64_t)k.row_threads * R;
     const dim3 grid((unsigned)(((int64_t)a.B * a.D + rows - 1) / rows),
-                    (unsigned)((octets + k.row_threads - 1) / k.row_threads));
+                    (unsigned)((octets + span - 1) / span));
     with_taps(a.K, [&](auto taps) {
-        conv_forward<E, decltype(taps)::value><<<grid, kThreads, 0, s>>>(k);
+        constexpr int K = decltype(taps)::value;
+        const auto kernel = R == 4 ? conv_forward<E, K, 4> : conv_forward<E, K, 1>;
+        kernel<<<grid, kThreads, 0, s>>>(k);
     });
     return hipGetLastError();
 }

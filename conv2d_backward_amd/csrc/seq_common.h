@@ -188,6 +188,7 @@ __device__ __forceinline__ float dpp0(float v) {
         0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 constexpr int kRowShl = 0x100, kRowShr = 0x110, kRowRor = 0x120;  // + distance 1..15
+constexpr int kWaveShl = 0x130, kWaveShr = 0x138, kWaveRor = 0x13c;  // by a lane of the wave
 
 // Maps h -> P h + Q compose along the lanes of a row of LANES (16 or 64): with Q
 // in h, h[k] becomes the composition of lanes 0 .. l applied to 0, and turned[k]
