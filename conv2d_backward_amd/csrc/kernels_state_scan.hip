@@ -37,18 +37,21 @@ struct ScanFwd {
 
 // A work-group: W waves, each 64/LANES rows (channels) of LANES lanes, each lane
 // T consecutive positions of a chunk of LANES * T; NI states at a time, whose
-// chains have nothing to do with each other.  LDS: B and C of NB states over the
+// chains have nothing to do with each other.  NS waves share their rows, each
+// with every NS-th group of NI states; their outputs meet in LDS.  LDS: B and C of NB states over the
 // chunk (fp32, in the order the lanes read them), then A log2(e) and the
 // running state of every (state, channel).
-template <class E, int W, int LANES, int T, int NI, int OCC>
+template <class E, int W, int LANES, int T, int NI, int NS, int OCC>
 __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
-    constexpr int kThreads = 64 * W, CH = W * 64 / LANES, CHUNK = LANES * T, NB = kStaged / CHUNK;
-    constexpr int Q = T / 4;
-    static_assert(NB % NI == 0, "whole groups of states");
+    constexpr int kThreads = 64 * W, CH = W / NS * 64 / LANES, CHUNK = LANES * T;
+    constexpr int NB = kStaged / CHUNK, Q = T / 4;
+    static_assert(NB % (NI * NS) == 0, "whole groups of states");
+    static_assert(NS == 1 || (W - W / NS) * 64 * T <= 2 * kStaged, "outputs fit where B and C were");
     extern __shared__ float lds[];
     float *sB = lds, *sC = lds + kStaged;
     float2 *sAh = reinterpret_cast<float2 *>(lds + 2 * kStaged);  // [N][CH]
-    const int tid = threadIdx.x, lane = tid % LANES, ch = tid / LANES;
+    const int tid = threadIdx.x, lane = tid % LANES, ch = tid / LANES % CH;
+    const int share = tid / LANES / CH;
     const int Dg = a.D / a.G;
     const int g = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles, b = blockIdx.y;
     const int in_group = tile * CH + ch;
@@ -113,7 +116,7 @@ __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 u[i] = s[i] * xv[i];
-                acc[i] = skip * xv[i];
+                acc[i] = share == 0 ? skip * xv[i] : 0.f;
                 total += s[i];
             }
         }
@@ -130,7 +133,7 @@ __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
             if (more || c0 + CHUNK < end)
                 prefetch(more ? c0 : c0 + CHUNK, more ? n0 + NB : 0);
             const int nb = std::min(NB, a.N - n0);
-            for (int n = 0; n < nb; n += NI) {
+            for (int n = share * NI; n < nb; n += NS * NI) {
                 float2 *ah = sAh + (n0 + n) * CH + ch;
                 const float *pB = sB + n * CHUNK + lane * 4, *pC = sC + n * CHUNK + lane * 4;
                 float da[NI][T], in[NI][T], h[NI], P[NI], carry[NI];
@@ -185,7 +188,32 @@ __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
                     }
             }
         }
-        if (live && t0 < a.L) {
+        if constexpr (NS > 1) {
+            __syncthreads();
+            float4 *meet = reinterpret_cast<float4 *>(lds) + (share - 1) * Q * (CH * LANES) +
+                           tid % (CH * LANES);
+            if (share > 0) {
+#pragma unroll
+                for (int j = 0; j < Q; ++j)
+                    meet[j * CH * LANES] =
+                        float4{acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]};
+            }
+            __syncthreads();
+            if (share == 0) {
+                for (int k = 1; k < NS; ++k) {
+                    const float4 *from = meet + k * Q * (CH * LANES);
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) {
+                        const float4 v = from[j * CH * LANES];
+                        acc[4 * j] += v.x;
+                        acc[4 * j + 1] += v.y;
+                        acc[4 * j + 2] += v.z;
+                        acc[4 * j + 3] += v.w;
+                    }
+                }
+            }
+        }
+        if (live && t0 < a.L && share == 0) {
             if (z) {
                 float zv[T];
                 load_row<E, T>(z, t0, len, zv);
@@ -199,7 +227,7 @@ __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
             store_row<E, T>(y, t0, a.L, acc);
         }
     }
-    if (live) {
+    if (live && share == 0) {
         float zero[T];
 #pragma unroll
         for (int i = 0; i < T; ++i) zero[i] = 0.f;
@@ -305,9 +333,9 @@ __global__ __launch_bounds__(kThreads) void scan_step(ScanStep<E> a) {
     }
 }
 
-template <class E, int W, int LANES, int T, int NI, int OCC>
+template <class E, int W, int LANES, int T, int NI, int NS, int OCC>
 hipError_t forward(const state_scan_args &a, hipStream_t s) {
-    constexpr int CH = W * 64 / LANES, NB = kStaged / (LANES * T);
+    constexpr int CH = W / NS * 64 / LANES, NB = kStaged / (LANES * T);
     ScanFwd<E> k{view<E>(a.x), view<E>(a.dt), view<E>(a.z), view<E>(a.Bm), view<E>(a.Cm),
                  view<E>(a.y), a.A, a.skip, a.dt_bias, a.state_in, a.state_out, a.checkpoints,
                  a.lengths, a.B, a.D, a.L, a.N, a.G, (a.D / a.G + CH - 1) / CH, a.softplus};
@@ -315,45 +343,64 @@ hipError_t forward(const state_scan_args &a, hipStream_t s) {
     const size_t bytes = (2 * kStaged + 2 * (size_t)NP * CH) * sizeof(float);
     if (bytes > 64 * 1024) {
         hipError_t e =
-            hipFuncSetAttribute((const void *)scan_forward<E, W, LANES, T, NI, OCC>,
+            hipFuncSetAttribute((const void *)scan_forward<E, W, LANES, T, NI, NS, OCC>,
                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != hipSuccess) return e;
     }
-    scan_forward<E, W, LANES, T, NI, OCC>
+    scan_forward<E, W, LANES, T, NI, NS, OCC>
         <<<dim3((unsigned)(a.G * k.tiles), (unsigned)a.B), 64 * W, bytes, s>>>(k);
     return hipGetLastError();
 }
 
-// The widths LANES x T of a row's chunk.  A lane's T positions share the 18 (16
-// lanes: 15) instructions of the lane scan beside their 7 (v_exp_f32 takes the
-// time of two); rows of 64 lanes add 0.6 for B and C, which fewer channels
-// share.  A SIMD works on 4 waves at a time and leaves none idle: fewer waves
-// than 4 a SIMD make nothing faster, more take their turns.  So of
-//   chunks * T * (8 + 18 / T) * max(1, waves / 4096)
-// the least.  Measured (bf16, N = 16, us, 64 x 16 / 64 x 8 / 16 x 16 / 16 x 8):
-// [1, 4096, 8192] 203 / 218 / 277 / 444, [8, 4096, 1024] 182 / 190 / 166 / 204,
-// [5, 1000, 301] 47 / 26 / 29 / 28, [1, 1024, 8192] 97 / 104 / 255 / 420.
-template <class E>
-hipError_t forward_any(const state_scan_args &a, hipStream_t s) {
-    static const int kLanes[] = {64, 64, 64, 16, 16, 16}, kT[] = {16, 8, 4, 16, 8, 4};
+// How the work is dealt: waves of a work-group, lanes of a row, positions of a
+// lane, waves that share a row's states.
+struct Deal {
+    int W, lanes, T, shares;
+};
+constexpr Deal kDeals[] = {{8, 64, 16, 1}, {8, 64, 16, 2}, {8, 64, 16, 4},
+                           {8, 64, 8, 2},  {4, 16, 16, 1}, {4, 16, 8, 1},
+                           {4, 16, 4, 1},  {8, 16, 8, 4},  {8, 16, 8, 2}};
+constexpr int kDealCount = sizeof(kDeals) / sizeof(kDeals[0]);
+
+// The deal with the least time by a count of issue slots.  Per chunk a wave has
+//   N / shares * (7.6 T + 15 (64 lanes: 18 for the lane scan))   its chains
+//   + N T lanes / (16 W)                                         its part of B and C
+//   + 20 T                                                       steps, gates, stores
+// and 2560 waves, 2.5 a SIMD, run as fast as one: more take their turns.  The
+// constants are fitted to 17 deals at 12 shapes, where this choice is within 2%
+// of the fastest on average and 8% at worst.  Measured (bf16, us, in the order
+// above): [1, 4096, 8192] N 16 196 / 233 / 296 / 255 / 280 / 427 / 684 / 308 / 316,
+// [1, 1024, 8192] 109 / 74 / 74 / 81 / 257 / 393 / 640 / 211 / 289,
+// [5, 1000, 301] 46 / 55 / 82 / 31 / 28 / 26 / 31 / 28 / 24,
+// [16, 1024, 60] 101 / 148 / 234 / 80 / 33 / 18 / 13 / 30 / 21.
+int pick_deal(const state_scan_args &a) {
     int best = 0;
     double least = 0;
-    for (int v = 0; v < 6; ++v) {
-        const int channels = (v < 3 ? 8 : 4) * 64 / kLanes[v], chunk = kLanes[v] * kT[v];
-        const int64_t rows = (int64_t)a.B * a.G * ((a.D / a.G + channels - 1) / channels) * channels;
-        const double waves = (double)rows * kLanes[v] / 64;
-        const double cost = ((a.L + chunk - 1) / chunk) *
-                            (v < 3 ? kT[v] * 8.6 + 18 : kT[v] * 8. + 15) *
-                            std::max(1., waves / 4096);
-        if (v == 0 || cost < least) best = v, least = cost;
+    for (int i = 0; i < kDealCount; ++i) {
+        const Deal &v = kDeals[i];
+        const int channels = v.W / v.shares * 64 / v.lanes, chunk = v.lanes * v.T;
+        const int64_t tiles = (a.D / a.G + channels - 1) / channels;
+        const double waves = (double)a.B * a.G * tiles * v.W;
+        const double work = (double)a.N / v.shares * (7.6 * v.T + (v.lanes == 64 ? 18 : 15)) +
+                            (double)a.N * v.T * v.lanes / (16 * v.W) + 20. * v.T;
+        const double cost = ((a.L + chunk - 1) / chunk) * work * std::max(1., waves / 2560);
+        if (i == 0 || cost < least) best = i, least = cost;
     }
-    switch (best) {
-        case 0: return forward<E, 8, 64, 16, 1, 4>(a, s);
-        case 1: return forward<E, 8, 64, 8, 1, 4>(a, s);
-        case 2: return forward<E, 8, 64, 4, 2, 4>(a, s);
-        case 3: return forward<E, 4, 16, 16, 1, 3>(a, s);
-        case 4: return forward<E, 4, 16, 8, 1, 4>(a, s);
-        default: return forward<E, 4, 16, 4, 2, 4>(a, s);
+    return best;
+}
+
+template <class E>
+hipError_t forward_any(const state_scan_args &a, hipStream_t s) {
+    switch (pick_deal(a)) {
+        case 0: return forward<E, 8, 64, 16, 1, 1, 4>(a, s);
+        case 1: return forward<E, 8, 64, 16, 1, 2, 4>(a, s);
+        case 2: return forward<E, 8, 64, 16, 1, 4, 4>(a, s);
+        case 3: return forward<E, 8, 64, 8, 1, 2, 4>(a, s);
+        case 4: return forward<E, 4, 16, 16, 1, 1, 3>(a, s);
+        case 5: return forward<E, 4, 16, 8, 1, 1, 4>(a, s);
+        case 6: return forward<E, 4, 16, 4, 2, 1, 4>(a, s);
+        case 7: return forward<E, 8, 16, 8, 1, 4, 4>(a, s);
+        default: return forward<E, 8, 16, 8, 1, 2, 4>(a, s);
     }
 }
 

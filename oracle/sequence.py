@@ -154,7 +154,8 @@ def state_scan_grads(gout, x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, so
             if z is not None:
                 sg = sigmoid(z[b, :, t])
                 slope = sg * (1 + z[b, :, t] * (1 - sg))
-                put("dz", (b, slice(None), t), gy * y * slope, np.abs(gy * slope) * Y)
+                put("dz", (b, slice(None), t), gy * y * slope,
+                    np.abs(gy) * sg * (1 + np.abs(z[b, :, t]) * (1 - sg)) * Y)
                 gy *= z[b, :, t] * sg
             q = back + Cm[b, of, :, t] * gy[:, None]
             Q = Back + np.abs(Cm[b, of, :, t] * gy[:, None])

@@ -302,6 +302,22 @@ def test_scan_backward(case, dtype):
     s.check_backward(s.forward(want_checkpoints=True)[2])
 
 
+@pytest.mark.parametrize("case", [
+    # Sizes for which the work is dealt to waves in every way there is (two chunks at least).
+    (1, 4096, 1030, 16, 1), (1, 1024, 1030, 16, 1), (1, 256, 1030, 16, 1), (1, 1024, 600, 16, 1),
+    (8, 4096, 260, 16, 1), (8, 2048, 150, 16, 1), (16, 1024, 70, 16, 1), (1, 1536, 140, 16, 1), (5, 1000, 301, 16, 1),
+    (3, 700, 150, 18, 2)], ids=str)
+def test_scan_sizes(case):
+    Scan((*case, None, "dense"), "bf16").check_forward()
+
+
+@pytest.mark.parametrize("case", [(8, 1040, 300, 16, 1), (260, 2, 140, 3, 2), (2, 600, 777, 24, 2)], ids=str)
+def test_scan_backward_sizes(case):
+    """Whole rows a work-group and cut ones, lanes of 16 and of 8 positions."""
+    s = Scan((*case, None, "dense"), "f32")
+    s.check_backward(s.forward(want_checkpoints=True)[2])
+
+
 @pytest.mark.parametrize("soft,gate,extras", [(True, False, True), (False, True, False), (True, True, False)])
 def test_scan_options(soft, gate, extras):
     s = Scan((2, 18, 150, 16, 1, None, "dense"), "f32", soft, gate, extras)
