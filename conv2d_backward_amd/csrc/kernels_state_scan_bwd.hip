@@ -4,7 +4,7 @@
 // chunk) and its gradient q backwards, q_t = C_t gy_t + a_{t+1} q_{t+1}; both go
 // over a chunk with the lane scan of kernels_state_scan.hip and share its
 // exponentials.  dB and dC sum over channels: 4 channels meet in a wave through
-// lane swaps, 8 waves through LDS, and the work-groups of a group through the
+// lane swaps, a work-group's waves through LDS, and the work-groups of a group through the
 // workspace, in a fixed order.
 //
 // A work-group walks its chunks from the last to the first.  Where there are
@@ -22,13 +22,12 @@ namespace seq {
 namespace {
 
 constexpr int LANES = 16, RPW = 64 / LANES;
-constexpr int kWaves = 8, kThreads = 64 * kWaves, CH = kWaves * RPW;
 constexpr int kNB = 16;  // states whose B and C are in LDS at once
 constexpr int kTailT = 8, kTailWaves = 4, kTailThreads = 64 * kTailWaves,
               kTailCH = kTailWaves * RPW;
 
 struct Plan {
-    int T, chunk;        // positions of a lane and of a chunk
+    int W, T, chunk;     // waves of a work-group, positions of a lane and of a chunk
     int tiles, chunks;   // channel tiles of a group, chunks of a row
     int segments;
     int marks;           // checkpoints of a row
@@ -42,9 +41,9 @@ struct Plan {
 constexpr size_t kLdsBytes = 160 * 1024;
 
 // LDS of a work-group: B and C, two halves of sums, states before, and A, q and dA.
-size_t lds_bytes(int T, int joined, int64_t N) {
-    const size_t NP = (N + kNB - 1) / kNB * kNB, chunk = LANES * T;
-    return (2 * kNB * chunk + 2 * joined * 2 * kWaves * chunk + kNB * CH + 3 * NP * CH) *
+size_t lds_bytes(int W, int T, int joined, int64_t N) {
+    const size_t NP = (N + kNB - 1) / kNB * kNB, chunk = LANES * T, CH = W * RPW;
+    return (2 * kNB * chunk + 2 * joined * 2 * W * chunk + kNB * CH + 3 * NP * CH) *
            sizeof(float);
 }
 
@@ -53,19 +52,41 @@ Plan make_plan(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
     // A lane of 16 positions spends half as much on the lane scans as one of 8
     // (30 instructions for both chains, beside some 24 a position): 288 us for
     // 311 at [4, 2048, 2048], N = 16.  Not where padding the row to whole chunks
-    // costs more (78 us for 116 at [5, 1000, 301]) nor where its sums do not fit.
-    const int64_t c16 = (L + 255) / 256 * (16 * 24 + 30), c8 = (L + 127) / 128 * (8 * 24 + 30);
-    p.T = c16 <= c8 && lds_bytes(16, 1, N) <= kLdsBytes ? 16 : 8;
-    p.joined = p.T == 16 ? 2 : 4;
-    while (lds_bytes(p.T, p.joined, N) > kLdsBytes) p.joined /= 2;
-    p.lds = lds_bytes(p.T, p.joined, N);
+    // costs more (78 us for 116 at [5, 1000, 301]), where there are too few chunks
+    // to give every compute unit one (33 us for 52 at [1, 256, 1000]), nor where its
+    // sums do not fit.
+    const int64_t c16 = (L + 255) / 256, c8 = (L + 127) / 128;
+    const int64_t items = B * G * ((D / G + 8 * RPW - 1) / (8 * RPW));
+    p.T = c16 * (16 * 24 + 30) <= c8 * (8 * 24 + 30) && items * c16 >= 256 &&
+                  lds_bytes(8, 16, 1, N) <= kLdsBytes
+              ? 16
+              : 8;
     p.chunk = LANES * p.T;
-    p.tiles = (int)((D / G + CH - 1) / CH);
     p.chunks = (int)((L + p.chunk - 1) / p.chunk);
+    // Work-groups of 8 waves, one on a compute unit; rows are cut until there are
+    // two for each.  Where their number leaves the last round of compute units
+    // mostly empty, work-groups of 4 waves, two on a compute unit, deal it finer
+    // though they share less (us, 8 / 4 waves: [2, 602, 777] N 24 G 2 82 / 74,
+    // [3, 333, 555] N 64 105 / 104, [1, 256, 1000] N 16 37 / 33; even ones
+    // [4, 2048, 2048] 281 / 304, [1, 1024, 2048] 63 / 67), and where even those come
+    // out uneven, cut rows do ([8, 1040, 2048] 457 whole, 391 cut in 8).
+    for (p.W = 8;; p.W = 4) {
+        p.tiles = (int)((D / G + p.W * RPW - 1) / (p.W * RPW));
+        const int64_t groups = B * G * p.tiles, units = 256 * (8 / p.W);
+        p.segments =
+            groups >= units ? 1 : (int)std::min<int64_t>(p.chunks, (2 * units + groups - 1) / groups);
+        const int64_t all = groups * p.segments, rounds = (all + units - 1) / units;
+        if (all >= rounds * units * 7 / 10) break;
+        if (p.W == 4) {
+            if (p.segments == 1) p.segments = std::min(p.chunks, 8);
+            break;
+        }
+    }
+    p.joined = p.T == 16 ? 2 : 4;
+    while (lds_bytes(p.W, p.T, p.joined, N) > kLdsBytes) p.joined /= 2;
+    p.lds = lds_bytes(p.W, p.T, p.joined, N);
     p.marks = (int)((L + SEQ_SCAN_CHECKPOINT - 1) / SEQ_SCAN_CHECKPOINT);
     p.pitch = p.chunks * p.chunk;
-    const int64_t groups = B * G * p.tiles;
-    p.segments = groups >= 256 ? 1 : (int)std::min<int64_t>(p.chunks, (512 + groups - 1) / groups);
     p.sums = 0;
     p.params = p.sums + p.tiles * 2 * B * G * N * (int64_t)p.pitch;
     p.tails = p.params + B * p.segments * D * (N + 2);
@@ -121,10 +142,11 @@ __device__ __forceinline__ void fetch(const float *from, int lane, float (&v)[T]
     }
 }
 
-// A work-group: 8 waves of 4 channels, 16 lanes a channel, T positions a lane,
+// A work-group: waves of 4 channels, 16 lanes a channel, T positions a lane,
 // NI states at a time.
-template <class E, int T, int NI>
-__global__ __launch_bounds__(kThreads, 2) void scan_backward(ScanBwd<E> a) {
+template <class E, int kWaves, int T, int NI>
+__global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
+    constexpr int kThreads = 64 * kWaves, CH = kWaves * RPW;
     constexpr int CHUNK = LANES * T, F = T / 4;  // F: sums of a lane
     constexpr int OCTETS = 2 * kNB * CHUNK / 8, PRE = OCTETS / kThreads;
     static_assert(OCTETS % kThreads == 0 && kNB * CH == kThreads, "whole rounds of threads");
@@ -539,13 +561,14 @@ hipError_t backward(const state_scan_backward_args &a, hipStream_t s) {
                                                                     a.D, a.N);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    const auto kernel = p.T == 16 ? scan_backward<E, 16, 1> : scan_backward<E, 8, 2>;
+    const auto kernel = p.W == 8 ? (p.T == 16 ? scan_backward<E, 8, 16, 1> : scan_backward<E, 8, 8, 2>)
+                                 : (p.T == 16 ? scan_backward<E, 4, 16, 1> : scan_backward<E, 4, 8, 2>);
     if (p.lds > 64 * 1024) {
         e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)p.lds);
         if (e != hipSuccess) return e;
     }
-    kernel<<<dim3((unsigned)(a.G * p.tiles), (unsigned)a.B, (unsigned)p.segments), kThreads, p.lds,
+    kernel<<<dim3((unsigned)(a.G * p.tiles), (unsigned)a.B, (unsigned)p.segments), 64 * p.W, p.lds,
              s>>>(k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t matrix = (2 * (int64_t)a.B * a.G * a.N * (p.pitch / 4) + 63) / 64;
