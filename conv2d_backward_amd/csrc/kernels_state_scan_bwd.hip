@@ -118,8 +118,10 @@ __device__ __forceinline__ void load_steps(const typename E::type *dt, int t0, i
 #pragma unroll
         for (int i = 0; i < T; ++i) s[i] = softplus(s[i]);
     }
+    if (len - t0 < T) {
 #pragma unroll
-    for (int i = 0; i < T; ++i) s[i] = len - t0 > i ? s[i] : 0.f;
+        for (int i = 0; i < T; ++i) s[i] = len - t0 > i ? s[i] : 0.f;
+    }
 }
 
 // Sum over the 16 lanes of a row, in every lane.
@@ -205,6 +207,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
                                     c * CHUNK / SEQ_SCAN_CHECKPOINT) * a.N + n];
     };
     prefetch(c_hi - 1, 0);
+    // This tile's part of dB, and how far from it dC's is.
+    const int64_t to_C = (int64_t)a.B * a.G * a.N * a.p.pitch;
+    float *out = a.ws + a.p.sums + tile * 2 * to_C + ((int64_t)b * a.G + g) * a.N * a.p.pitch;
     // Sums of a group of states over the waves are read from one half of `sums`
     // while the next group's are written to the other.
     int half = 0;
@@ -317,9 +322,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
                 }
                 __syncthreads();
                 for (int i = tid; i < nr * 2 * 64; i += kThreads) {
-                    const int f = i % 64, which = i / 64 % 2, r = i / 128;
+                    const int f = i % 64, rw = i / 64;  // [r][B or C]
                     const float *from =
-                        sums + ((half * a.p.joined + r) * 2 + which) * kWaves * CHUNK + f * F;
+                        sums + (half * a.p.joined * 2 + rw) * kWaves * CHUNK + f * F;
                     Whole<F> v = *reinterpret_cast<const Whole<F> *>(from);
 #pragma unroll
                     for (int w = 1; w < kWaves; ++w) {
@@ -327,11 +332,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
 #pragma unroll
                         for (int k = 0; k < F; ++k) v.v[k] += o.v[k];
                     }
-                    const int64_t rows = (int64_t)a.B * a.G * a.N;
-                    const int64_t row = ((int64_t)b * a.G + g) * a.N + n0 + n1 + r;
-                    *reinterpret_cast<Whole<F> *>(
-                        a.ws + a.p.sums + (((int64_t)tile * 2 + which) * rows + row) * a.p.pitch +
-                        c0 + f % 16 * T + f / 16 * F) = v;
+                    *reinterpret_cast<Whole<F> *>(out + (rw & 1 ? to_C : 0) +
+                                                  (int64_t)(n0 + n1 + rw / 2) * a.p.pitch + c0 +
+                                                  f % 16 * T + f / 16 * F) = v;
                 }
                 half ^= 1;
             }
@@ -351,11 +354,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
 #pragma unroll
                 for (int i = 0; i < T; ++i) ds[i] *= sigmoid(v[i] + bias);
             }
+            if (len - t0 < T) {
 #pragma unroll
-            for (int i = 0; i < T; ++i) {
-                ds[i] = len - t0 > i ? ds[i] : 0.f;
-                sum_bias += ds[i];
+                for (int i = 0; i < T; ++i) ds[i] = len - t0 > i ? ds[i] : 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < T; ++i) sum_bias += ds[i];
             store_row<E, T>(a.ddt.row(b, d), t0, a.L, ds);
             if (a.z.p) {
                 float go[T];
@@ -366,7 +370,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
                     const float sg = sigmoid(v[i]);
                     o[i] = go[i] * __builtin_fmaf(skip, x[i], y[i]) *
                            (sg * __builtin_fmaf(v[i], 1.f - sg, 1.f));
-                    o[i] = len - t0 > i ? o[i] : 0.f;
+                }
+                if (len - t0 < T) {
+#pragma unroll
+                    for (int i = 0; i < T; ++i) o[i] = len - t0 > i ? o[i] : 0.f;
                 }
                 store_row<E, T>(a.dz.row(b, d), t0, a.L, o);
             }
