@@ -111,7 +111,35 @@ bool take(const Operand &o, const at::Tensor &t, const int64_t *shape, size_t n,
     }
 }
 
-// call(entry, stream, sizes, operands) -> status, or the outputs in order.
+// Sizes that the caller leaves to the operands: the first needed one that has each.
+bool bind(const Entry &e, PyObject *given, int64_t *size, bool *known) {
+    for (size_t i = 0; i < e.operands.size(); ++i) {
+        const Operand &o = e.operands[i];
+        bool all = true;
+        for (const auto &d : o.dims) all = all && known[d.first];
+        if (all || o.use != kNeeded) continue;
+        PyObject *v = PyTuple_GET_ITEM(given, i);
+        if (!THPVariable_Check(v)) return refuse("%s must be a tensor%s", o.name.c_str());
+        const at::Tensor &t = THPVariable_Unpack(v);
+        const int64_t n = o.dims.size();
+        const bool ungrouped = o.kind == kStates && t.dim() == n - 1;
+        if (!ungrouped && t.dim() != n) {
+            const std::string more = std::to_string(n) + " dimensions, has " + std::to_string(t.dim());
+            return refuse("%s must have %s", o.name.c_str(), more.c_str());
+        }
+        for (int64_t k = 0, at = 0; k < n; ++k) {
+            const auto &d = o.dims[k];
+            const int64_t here = ungrouped && k == 1 ? 1 : t.size(at++) - d.second;
+            if (known[d.first]) continue;
+            size[d.first] = here;
+            known[d.first] = true;
+        }
+    }
+    return true;
+}
+
+// call(entry, stream, sizes, operands) -> status, or the outputs in order.  A size
+// that is None comes from the operands.
 // An operand is a tensor, or None: an optional one is missing, an output is
 // allocated; False: an output is not wanted.
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t count) {
@@ -146,24 +174,31 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t count) {
         }
         // The header: the type, then the first sizes (a float goes as it is stored).
         int64_t size[kMaxSizes];
-        std::vector<int32_t> words{code};
+        int32_t word[kMaxSizes];
+        bool known[kMaxSizes], whole = true;
         for (Py_ssize_t i = 0; i < n_sizes; ++i) {
             PyObject *v = PyTuple_GET_ITEM(sizes, i);
-            size[i] = 0;
-            int32_t word;
+            size[i] = word[i] = 0;
+            known[i] = v != Py_None;
+            whole = whole && known[i];
             if (PyFloat_Check(v)) {
                 const float f = (float)PyFloat_AS_DOUBLE(v);
-                std::memcpy(&word, &f, 4);
-            } else {
+                std::memcpy(&word[i], &f, 4);
+            } else if (known[i]) {
                 size[i] = PyLong_AsLongLong(v);
                 if (PyErr_Occurred()) return nullptr;
-                if (size[i] != (int32_t)size[i]) {
-                    PyErr_SetString(PyExc_ValueError, "a size is beyond 32 bits");
-                    return nullptr;
-                }
-                word = (int32_t)size[i];
             }
-            if (i < e->header) words.push_back(word);
+        }
+        if (!whole && !bind(*e, given, size, known)) return nullptr;
+        std::vector<int32_t> words{code};
+        words.reserve(16);
+        for (Py_ssize_t i = 0; i < n_sizes; ++i) {
+            if (size[i] != (int32_t)size[i]) {
+                PyErr_SetString(PyExc_ValueError, "a size is beyond 32 bits");
+                return nullptr;
+            }
+            if (size[i]) word[i] = (int32_t)size[i];
+            if (i < e->header) words.push_back(word[i]);
         }
         if (words.size() % 2) words.push_back(0);
         std::vector<int64_t> fields(words.size() / 2);

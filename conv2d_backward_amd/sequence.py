@@ -124,9 +124,10 @@ def _make(name):
 
 
 def _call(name, lead, stream, sizes, operands):
-    """Runs an entry: its outputs in order (an operand False: an output not wanted)."""
+    """Runs an entry: its outputs in order (a size None: the operands have it; an
+    operand False: an output not wanted)."""
     entry = _made.get(name) or _make(name)
-    index = lead.get_device()
+    index = lead.get_device() if isinstance(lead, torch.Tensor) else -1
     if stream is None or index < 0:
         if index < 0:  # refused by name
             out = _sequence.call(entry, 0, sizes, operands)
@@ -170,9 +171,7 @@ def causal_conv(x, weight, bias=None, *, silu=True, state=None, lengths=None, wa
     of each sequence (y is 0 beyond).  new_state, for the next call or
     ``causal_conv_step``, is None unless want_state.
     """
-    B, D, L = _shape(x, "x", 3)
-    K = _shape(weight, "weight", 2)[1]
-    return _call("causal_conv_forward", x, stream, (B, D, L, K, bool(silu)),
+    return _call("causal_conv_forward", x, stream, (None, None, None, None, bool(silu)),
                  (x, out, weight, bias, state, None if want_state else False, lengths))
 
 
@@ -180,11 +179,9 @@ def causal_conv_backward(grad_out, x, weight, bias=None, *, silu=True, lengths=N
                          want_dw=True, want_db=None, dx=None, stream=None):
     """The gradients of ``causal_conv`` from a zero state: (dx, dweight, dbias),
     each None when not wanted (dbias by default where there is a bias)."""
-    B, D, L = _shape(x, "x", 3)
-    K = _shape(weight, "weight", 2)[1]
     if want_db is None:
         want_db = bias is not None
-    return _call("causal_conv_backward", x, stream, (B, D, L, K, bool(silu)),
+    return _call("causal_conv_backward", x, stream, (None, None, None, None, bool(silu)),
                  (grad_out, x, dx if want_dx else False, weight, bias, None if want_dw else False,
                   None if want_db else False, lengths))
 
@@ -196,19 +193,13 @@ def causal_conv_step(x, state, weight, bias=None, *, silu=True, slots=None, out=
     int32 [B]: the line of each row (row b uses line b without); a slot outside
     the lines marks a padding row, whose y is 0 and which changes no line.
     """
-    B, D = _shape(x, "x", 2)
-    K = _shape(weight, "weight", 2)[1]
-    return _call("causal_conv_step", x, stream, (B, D, K, bool(silu), _shape(state, "state", 3)[0]),
+    return _call("causal_conv_step", x, stream, (None, None, None, bool(silu), None),
                  (x, out, weight, bias, state, slots))[0]
 
 
-def _groups(B, C, dims):
-    """The groups of B and C; [B, N, ...] has one."""
-    if not isinstance(B, torch.Tensor) or not isinstance(C, torch.Tensor):
-        raise ValueError("B and C must be tensors")
-    if B.dim() != C.dim():
-        raise ValueError("B and C must have the same dimensions")
-    return B.shape[1] if B.dim() == dims else 1
+def _marks(x):
+    """Checkpoints of a row."""
+    return -(-_shape(x, "x", 3)[2] // SCAN_CHECKPOINT)
 
 
 def state_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, softplus=True, state=None,
@@ -221,10 +212,8 @@ def state_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, softplus=True, s
     dt_bias).  state [B, D, N] float32: h before position 0.  new_state and the
     checkpoints that ``state_scan_backward`` takes are None unless wanted.
     """
-    nB, nD, L = _shape(x, "x", 3)
-    N = _shape(A, "A", 2)[1]
     return _call("state_scan_forward", x, stream,
-                 (nB, nD, L, N, _groups(B, C, 4), bool(softplus), 0, -(-L // SCAN_CHECKPOINT)),
+                 (None, None, None, None, None, bool(softplus), 0, _marks(x)),
                  (x, dt, z, B, C, out, A, D, dt_bias, state, None if want_state else False,
                   None if want_checkpoints else False, lengths))
 
@@ -238,15 +227,13 @@ def state_scan_backward(grad_out, x, dt, A, B, C, checkpoints, D=None, z=None, d
     the gradient of new_state (zeros by default); dstate, that of state, is None
     unless wanted.  dB and dC have B's shape.  dx, ddt, dz: optional outputs.
     """
-    nB, nD, L = _shape(x, "x", 3)
-    N = _shape(A, "A", 2)[1]
     if z is None:
         if dz is not None:
             raise ValueError("dz needs z")
         dz = False
     dx, ddt, dz, dB, dC, dA, dD, dbias, dstate = _call(
         "state_scan_backward", x, stream,
-        (nB, nD, L, N, _groups(B, C, 4), bool(softplus), 0, -(-L // SCAN_CHECKPOINT)),
+        (None, None, None, None, None, bool(softplus), 0, _marks(x)),
         (grad_out, x, dt, z, B, C, dx, ddt, dz, A, D, dt_bias, checkpoints, grad_state, None, None, None,
          False if D is None else None, False if dt_bias is None else None,
          None if want_dstate else False, lengths))
@@ -262,10 +249,7 @@ def state_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, soft
     x, dt, z [B, D]; B, C [B, G, N] or [B, N]; state [lines, D, N] float32
     (contiguous) is updated in place; slots as in ``causal_conv_step``.
     """
-    nB, nD = _shape(x, "x", 2)
-    N = _shape(A, "A", 2)[1]
-    return _call("state_scan_step", x, stream,
-                 (nB, nD, N, _groups(B, C, 3), bool(softplus), _shape(state, "state", 3)[0], 0),
+    return _call("state_scan_step", x, stream, (None, None, None, None, bool(softplus), None, 0),
                  (x, dt, z, B, C, out, A, D, dt_bias, state, slots))[0]
 
 
@@ -279,12 +263,11 @@ def block_norm(y, residual, weight_post=None, weight_pre=None, *, gate=None, sca
     is the RMS norm of the sum (weight_pre; None without it).  residual_out may be
     the residual itself.
     """
-    B, D, L = _shape(y, "y", 3)
     if weight_pre is None:
         if out is not None:
             raise ValueError("out needs weight_pre")
         out = False
-    return _call("block_norm_forward", y, stream, (B, D, L, float(eps), 0, 0),
+    return _call("block_norm_forward", y, stream, (None, None, None, float(eps), 0, 0),
                  (y, gate, residual, residual_out, out, scale, weight_post, weight_pre, lengths))
 
 
@@ -296,13 +279,12 @@ def block_norm_backward(grad_residual, grad_out, y, residual_out, weight_post=No
     grad_residual (float32) is the gradient of new_residual, grad_out that of u;
     either may be None.  residual_out: the forward call's new_residual.
     """
-    B, D, L = _shape(y, "y", 3)
     if gate is None:
         if dgate is not None:
             raise ValueError("dgate needs the gate")
         dgate = False
     return NormGrads(*_call(
-        "block_norm_backward", y, stream, (B, D, L, float(eps), 0, 1),
+        "block_norm_backward", y, stream, (None, None, None, float(eps), 0, 1),
         (grad_residual, grad_out, y, gate, residual_out, dy, dresidual, dgate, scale, weight_post,
          weight_pre, False if scale is None else None, False if weight_post is None else None,
          False if weight_pre is None else None, lengths)))
