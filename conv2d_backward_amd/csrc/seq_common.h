@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sequence_ops.h"
 
@@ -75,20 +76,36 @@ __device__ __forceinline__ void store_vec(typename E::type *p, const float (&in)
     }
 }
 
+// The first `left` of V positions as they are stored, 0 for the others.  The reads
+// go out one by one under their conditions; the empty statements keep what uses
+// them from moving up there, where it would cost the end of a row V latencies.
+template <class T, int V>
+__device__ __forceinline__ void load_end(const T *p, int left, T (&out)[V]) {
+    using Word = std::conditional_t<sizeof(T) == 4, T, uint32_t>;
+    Word u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        u[i] = 0;
+        if (i < left) u[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm volatile("" : "+v"(u[i]));
+#pragma unroll
+    for (int i = 0; i < V; ++i) out[i] = (T)u[i];
+}
+
 // Positions t .. t+V-1 of a row (t >= 0); those from `end` on are 0 and not read.
 template <class E, int V>
 __device__ __forceinline__ void load_row(const typename E::type *row, int t, int end,
                                          float (&out)[V]) {
-    const typename E::type *p = row + t;
     const int left = end - t;
     if (left >= V) {
-        load_vec<E, V>(p, out);
+        load_vec<E, V>(row + t, out);
     } else {
+        typename E::type u[V];
+        load_end(row + t, left, u);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            out[i] = 0.f;
-            if (left > i) out[i] = E::up(p[i]);
-        }
+        for (int i = 0; i < V; ++i) out[i] = E::up(u[i]);
     }
 }
 
@@ -101,11 +118,10 @@ struct Octet {
         if (left >= 8) {
             v = *reinterpret_cast<const typename Vec<typename E::type, 8>::type *>(p);
         } else {
+            typename E::type u[8];
+            load_end(p, left, u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = 0;
-                if (left > i) v[i] = p[i];
-            }
+            for (int i = 0; i < 8; ++i) v[i] = u[i];
         }
     }
     __device__ __forceinline__ void zero() {
