@@ -342,7 +342,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_sums(NormBwd<E> a) 
     constexpr int COLS = kV * kBwdCV;
     __shared__ float waves[kBwdThreads / 64][6][COLS];
     const int cv = threadIdx.x % kBwdCV, tid = threadIdx.x;
-    const int bt = blockIdx.x, b = bt / a.s.tiles, split = blockIdx.y;
+    const int all = a.B * a.s.tiles, wg = tile_of(blockIdx.x, gridDim.x);
+    const int bt = wg % all, b = bt / a.s.tiles, split = wg / all;
     const int t0 = bt % a.s.tiles * COLS + cv * kV;
     const int left = length_of(a.lengths, b, a.L) - t0;
     const int lo = (int)((int64_t)a.D * split / a.s.splits);
@@ -401,8 +402,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a)
     __shared__ float coef[4][COLS];  // i_post, i_pre, c_pre, c_post
     const int cv = threadIdx.x % kBwdCV, tid = threadIdx.x;
     // From the last tile back: the caches hold what the first pass read last.
-    const int bt = gridDim.x - 1 - blockIdx.x, b = bt / a.s.tiles;
-    const int split = gridDim.y - 1 - blockIdx.y;
+    const int all = a.B * a.s.tiles, wg = tile_of(gridDim.x - 1 - blockIdx.x, gridDim.x);
+    const int bt = wg % all, b = bt / a.s.tiles, split = wg / all;
     const int t0 = bt % a.s.tiles * COLS + cv * kV;
     const int left = length_of(a.lengths, b, a.L) - t0;
     const int lo = (int)((int64_t)a.D * split / a.s.splits);
@@ -531,7 +532,7 @@ hipError_t backward(const block_norm_backward_args &a, hipStream_t s) {
                  view<F32>(a.gr), view<F32>(a.r_out), view<F32>(a.dr), a.scale, a.w_post, a.w_pre,
                  a.lengths, static_cast<float *>(a.workspace), a.B, a.D, a.L,
                  bwd_shape(a.B, a.D, a.L), params, a.eps};
-    const dim3 grid((unsigned)(a.B * k.s.tiles), (unsigned)k.s.splits);
+    const dim3 grid((unsigned)(a.B * k.s.tiles * k.s.splits));
     norm_backward_sums<E><<<grid, kBwdThreads, 0, s>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -131,7 +131,12 @@ struct BwdShape {
 
 BwdShape bwd_shape(int B, int D, int L) {
     BwdShape s;
-    s.along = pow2_at_least(((int64_t)L + kV - 1) / kV, kThreads);
+    // A row beyond 256 octets in pieces of 256, 128 or 64 lanes, whichever leave the
+    // fewest idle (shorter rows lose more to the borders of pieces than to idle lanes).
+    const int64_t octets = ((int64_t)L + kV - 1) / kV;
+    s.along = pow2_at_least(octets, kThreads);
+    for (int n = s.along / 2; octets > kThreads && n >= 64; n /= 2)
+        if ((octets + n - 1) / n * n < (octets + s.along - 1) / s.along * s.along) s.along = n;
     s.batch = pow2_at_least(B, kThreads / s.along);
     s.channels = kThreads / (s.along * s.batch);
     s.segments = (int)(((int64_t)L + (int64_t)s.along * kV - 1) / ((int64_t)s.along * kV));

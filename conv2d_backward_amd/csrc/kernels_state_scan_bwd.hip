@@ -9,8 +9,8 @@
 //
 // A work-group walks its chunks from the last to the first.  Where there are
 // too few (batch, channel tile) pairs to fill the chip, the positions are cut
-// into segments: scan_tail finds what each segment sends back on its own,
-// scan_carry chains those, and the segments then run side by side.
+// into segments: scan_tail finds what each segment sends back on its own, and
+// the segments then run side by side, each chaining what is behind it.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -175,10 +175,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
         if (n < a.N && c < Dg) {
             const int64_t at = (int64_t)(g * Dg + c) * a.N + n;
             A2 = a.A[at] * kLog2e;
-            if (a.p.segments > 1)
-                q = a.ws[a.p.tails + bs * a.D * a.N + at];
-            else if (a.gstate)
-                q = a.gstate[(int64_t)b * a.D * a.N + at];
+            if (a.gstate) q = a.gstate[(int64_t)b * a.D * a.N + at];
+            // Through the segments behind this one.
+            for (int later = a.p.segments - 1; later > seg; --later) {
+                const int64_t ls = (int64_t)b * a.p.segments + later;
+                q = __builtin_fmaf(exp2_fast(a.ws[a.p.steps + ls * a.D + g * Dg + c] * A2), q,
+                                   a.ws[a.p.tails + ls * a.D * a.N + at]);
+            }
         }
         sA[i] = A2;
         sG[i] = q;
@@ -397,8 +400,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
     }
 }
 
-// What a segment sends back to the state before it when nothing comes from
-// behind: tails[b][segment][d][n], and its summed steps [b][segment][d].
+// What a segment (but the first, behind nothing) sends back to the state before it
+// when nothing comes from behind: tails[b][segment][d][n], and its summed steps
+// [b][segment][d].
 template <class E>
 __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tiles) {
     constexpr int T = kTailT, CHUNK = LANES * T;
@@ -409,7 +413,7 @@ __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tile
     const int tid = threadIdx.x, lane = tid % LANES, ch = tid / LANES;
     const int Dg = a.D / a.G;
     const int g = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-    const int b = blockIdx.y, seg = blockIdx.z;
+    const int b = blockIdx.y, seg = blockIdx.z + 1;
     const bool live = tile * kTailCH + ch < Dg;
     const int d = g * Dg + std::min(tile * kTailCH + ch, Dg - 1);
     const int len = length_of(a.lengths, b, a.L);
@@ -469,24 +473,6 @@ __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tile
     }
     steps = row_sum(steps);
     if (live && lane == 0) a.ws[a.p.steps + bs * a.D + d] = steps;
-}
-
-// Chains the segments of a (batch, channel, state): tails become what comes
-// from behind each segment.
-__global__ void scan_carry(float *ws, Plan p, const float *A, const float *gstate, int64_t B,
-                           int64_t D, int64_t N) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= B * D * N) return;
-    const int64_t b = i / (D * N), dn = i - b * D * N, d = dn / N;
-    const float A2 = A[dn] * kLog2e;
-    float carry = gstate ? gstate[i] : 0.f;
-    for (int seg = p.segments - 1; seg >= 0; --seg) {
-        const int64_t bs = b * p.segments + seg;
-        float *tail = ws + p.tails + bs * D * N + dn;
-        const float own = *tail;
-        *tail = carry;
-        carry = __builtin_fmaf(exp2_fast(ws[p.steps + bs * D + d] * A2), carry, own);
-    }
 }
 
 // The last sums: dB and dC over channel tiles, dA, dskip and ddt_bias over the
@@ -560,12 +546,8 @@ hipError_t backward(const state_scan_backward_args &a, hipStream_t s) {
     if (p.segments > 1) {
         const int tiles = (a.D / a.G + kTailCH - 1) / kTailCH;
         const size_t bytes = (kNB * LANES * kTailT + 2 * (size_t)NP * kTailCH) * sizeof(float);
-        scan_tail<E><<<dim3((unsigned)(a.G * tiles), (unsigned)a.B, (unsigned)p.segments),
+        scan_tail<E><<<dim3((unsigned)(a.G * tiles), (unsigned)a.B, (unsigned)(p.segments - 1)),
                        kTailThreads, bytes, s>>>(k, tiles);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        const int64_t n = (int64_t)a.B * a.D * a.N;
-        scan_carry<<<dim3((unsigned)((n + 255) / 256)), 256, 0, s>>>(k.ws, p, a.A, a.gstate, a.B,
-                                                                    a.D, a.N);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const auto kernel = p.W == 8 ? (p.T == 16 ? scan_backward<E, 8, 16, 1> : scan_backward<E, 8, 8, 2>)
