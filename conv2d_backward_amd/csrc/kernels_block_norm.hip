@@ -290,7 +290,7 @@ BwdShape bwd_shape(int64_t B, int64_t D, int64_t L) {
     BwdShape s;
     s.tiles = (int)((L + kV * kBwdCV - 1) / (kV * kBwdCV));
     // Four work-groups a compute unit; a share has a round of rows at least.
-    const int64_t most = std::min<int64_t>(16, (D + kBwdRows - 1) / kBwdRows);
+    const int64_t most = std::min<int64_t>(64, (D + kBwdRows - 1) / kBwdRows);
     s.splits = (int)std::max<int64_t>(1, std::min(most, 1024 / (B * s.tiles)));
     s.sums = 0;
     s.params = s.sums + s.splits * 6 * B * s.tiles * kV * kBwdCV;
@@ -410,6 +410,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a)
     const int hi = (int)((int64_t)a.D * (split + 1) / a.s.splits);
     for (int i = tid; i < 6 * COLS; i += kBwdThreads) {
         float v = 0.f;
+#pragma unroll 8
         for (int s = 0; s < a.s.splits; ++s)
             v += a.ws[a.s.sums + (((int64_t)s * 6 + i / COLS) * a.B * a.s.tiles + bt) * COLS +
                       i % COLS];
@@ -510,17 +511,31 @@ hipError_t forward(const block_norm_args &a, hipStream_t s) {
         kernel<<<dim3((unsigned)a.B), kTokenThreads, 0, s>>>(k);
         return hipGetLastError();
     }
-    // Up to 1024 channels a tile stays in registers, with 32 columns where those
-    // tiles fill half the chip, else 16; more channels are read again, with 32
-    // columns where those tiles fill the chip.  Measured (us, 32 kept / 16 kept /
-    // 32 again / 16 again): [8, 1024, 2001] bf16 56 / 80 / 74 / 95,
-    // [3, 1000, 1025] f32 24 / 22 / 29 / 22, [4, 2048, 2048] bf16 - / 69 / 67 / 90,
-    // [2, 4096, 2048] bf16 - / - / 102 / 89 (8 columns kept: 94).
-    const int64_t wide = a.B * tiles_of(a.L, 4);
-    const int CV = wide >= (a.D <= 1024 ? 128 : 256) ? 4 : 2;
+    // A tile stays in registers where its channels fit: 32 columns of up to 1024, 16
+    // of 2048 or 8 of 4096.  Pieces of rows should be long and tiles enough for the
+    // chip: 32 columns where those make 128 tiles, 8 where 16 make fewer than 96 (or
+    // none fit, up to 512 tiles of 8).  Else it is read again, with 32 columns where
+    // those make 256 tiles.  Measured (us, 32 / 16 / 8 columns kept, 32 / 16 again):
+    // [8, 1024, 2001] bf16 50 / 69 / 75, again 74 / 95; [3, 1000, 1025] f32 24 / 21 / 24;
+    // [1, 600, 1500] bf16 - / 12 / 10; [3, 1800, 2805] f16 - / 77 / 96, again 110;
+    // [64, 1500, 16] bf16 - / 13 / 10; [1, 4000, 1000] bf16 - / - / 31, again 52;
+    // [2, 4096, 2048] bf16 - / - / 67, again 59.
+    const int64_t t32 = a.B * tiles_of(a.L, 4), t16 = a.B * tiles_of(a.L, 2),
+                  t8 = a.B * tiles_of(a.L, 1);
+    int CV;
+    void (*kernel)(NormFwd<E>);
+    if (a.D <= 1024 && t32 >= 128)
+        CV = 4, kernel = norm_forward<E, 1024, 4, 4>;
+    else if (a.D <= 2048 && t16 >= 96)
+        CV = 2, kernel = a.D <= 1024 ? norm_forward<E, 1024, 2, 2> : norm_forward<E, 1024, 2, 4>;
+    else if (a.D <= 4096 && t8 < 512)
+        CV = 1, kernel = a.D <= 1024 ? norm_forward<E, 1024, 1, 1>
+                         : a.D <= 2048 ? norm_forward<E, 1024, 1, 2> : norm_forward<E, 1024, 1, 4>;
+    else if (t32 >= 256)
+        CV = 4, kernel = norm_forward<E, 1024, 4, 0>;
+    else
+        CV = 2, kernel = norm_forward<E, 1024, 2, 0>;
     k.tiles = (int)tiles_of(a.L, CV);
-    const auto kernel = a.D <= 1024 ? (CV == 4 ? norm_forward<E, 1024, 4, 4> : norm_forward<E, 1024, 2, 2>)
-                                    : (CV == 4 ? norm_forward<E, 1024, 4, 0> : norm_forward<E, 1024, 2, 0>);
     kernel<<<dim3((unsigned)(a.B * k.tiles)), 1024, 0, s>>>(k);
     return hipGetLastError();
 }
