@@ -313,6 +313,7 @@ __global__ void conv_backward_join(const float *part, float *dw, float *db, int 
     const int64_t n = (int64_t)D * (K + 1);
     if (i >= n) return;
     float sum = 0.f;
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) sum += part[s * n + i];
     const int64_t d = i / (K + 1);
     const int k = (int)(i - d * (K + 1));

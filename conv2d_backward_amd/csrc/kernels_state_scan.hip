@@ -22,7 +22,10 @@
 namespace seq {
 namespace {
 
-constexpr int kStaged = 4096;  // floats of B, and as many of C, in LDS at once
+// Floats of B, and as many of C, in LDS at once.  Rows of 64 lanes come through so
+// many states between two waits only with more of them; with T = 16 the registers
+// to carry them are not there (spilled, [2, 340, 3307] f32, N = 64, takes 166 us for 127).
+constexpr int staged_floats(int lanes, int T) { return lanes == 64 && T == 8 ? 8192 : 4096; }
 
 template <class E>
 struct ScanFwd {
@@ -44,7 +47,7 @@ struct ScanFwd {
 template <class E, int W, int LANES, int T, int NI, int NS, int OCC>
 __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
     constexpr int kThreads = 64 * W, CH = W / NS * 64 / LANES, CHUNK = LANES * T;
-    constexpr int NB = kStaged / CHUNK, Q = T / 4;
+    constexpr int kStaged = staged_floats(LANES, T), NB = kStaged / CHUNK, Q = T / 4;
     static_assert(NB % (NI * NS) == 0, "whole groups of states");
     static_assert(NS == 1 || (W - W / NS) * 64 * T <= 2 * kStaged, "outputs fit where B and C were");
     extern __shared__ float lds[];
@@ -335,6 +338,7 @@ __global__ __launch_bounds__(kThreads) void scan_step(ScanStep<E> a) {
 
 template <class E, int W, int LANES, int T, int NI, int NS, int OCC>
 hipError_t forward(const state_scan_args &a, hipStream_t s) {
+    constexpr int kStaged = staged_floats(LANES, T);
     constexpr int CH = W / NS * 64 / LANES, NB = kStaged / (LANES * T);
     ScanFwd<E> k{view<E>(a.x), view<E>(a.dt), view<E>(a.z), view<E>(a.Bm), view<E>(a.Cm),
                  view<E>(a.y), a.A, a.skip, a.dt_bias, a.state_in, a.state_out, a.checkpoints,
@@ -357,33 +361,37 @@ hipError_t forward(const state_scan_args &a, hipStream_t s) {
 struct Deal {
     int W, lanes, T, shares;
 };
-constexpr Deal kDeals[] = {{8, 64, 16, 1}, {8, 64, 16, 2}, {8, 64, 16, 4},
-                           {8, 64, 8, 2},  {4, 16, 16, 1}, {4, 16, 8, 1},
-                           {4, 16, 4, 1},  {8, 16, 8, 4},  {8, 16, 8, 2}};
+constexpr Deal kDeals[] = {{8, 64, 16, 1}, {8, 64, 16, 2}, {8, 64, 16, 4}, {8, 64, 8, 1},
+                           {8, 64, 8, 2},  {8, 64, 8, 4},  {4, 16, 16, 1}, {4, 16, 4, 1},
+                           {8, 16, 8, 2},  {8, 16, 8, 4}};
 constexpr int kDealCount = sizeof(kDeals) / sizeof(kDeals[0]);
 
 // The deal with the least time by a count of issue slots.  Per chunk a wave has
 //   N / shares * (7.6 T + 15 (64 lanes: 18 for the lane scan))   its chains
-//   + N T lanes / (16 W)                                         its part of B and C
-//   + 20 T                                                       steps, gates, stores
-// and 2560 waves, 2.5 a SIMD, run as fast as one: more take their turns.  The
-// constants are fitted to 17 deals at 12 shapes, where this choice is within 2%
-// of the fastest on average and 8% at worst.  Measured (bf16, us, in the order
-// above): [1, 4096, 8192] N 16 196 / 233 / 296 / 255 / 280 / 427 / 684 / 308 / 316,
-// [1, 1024, 8192] 109 / 74 / 74 / 81 / 257 / 393 / 640 / 211 / 289,
-// [5, 1000, 301] 46 / 55 / 82 / 31 / 28 / 26 / 31 / 28 / 24,
-// [16, 1024, 60] 101 / 148 / 234 / 80 / 33 / 18 / 13 / 30 / 21.
+//   + N' T lanes / (16 W)   its part of B and C, of N' states: N in whole stages
+//   + 20 T                  steps, gates, stores
+// and 2560 waves, 2.5 a SIMD, run as fast as one: more take their turns; a stage
+// costs 100 more for its waits.  At 29 shapes the choice is within 3% of the
+// fastest on average and 19% at worst.  Measured (us, in the order above):
+// [1, 4096, 8192] bf16 N 16 180 / 214 / 284 / 200 / 230 / 313 / 277 / 681 / 328 / 311,
+// [1, 1024, 8192] bf16 N 16 107 / 78 / 76 / 122 / 79 / 85 / 252 / 628 / 299 / 221,
+// [2, 340, 3307] f32 N 64 199 / 131 / 127 / 185 / 114 / 114 / 345 / 623 / 310 / 187,
+// [5, 1825, 3409] f32 N 8 186 / 219 / 296 / 162 / 188 / 280 / 193 / 268 / 237 / 285,
+// [5, 1000, 301] bf16 N 16 39 / 43 / 62 / 23 / 26 / 37 / 26 / 30 / 24 / 27,
+// [16, 1024, 60] bf16 N 16 88 / 119 / 179 / 49 / 66 / 103 / 26 / 12 / 18 / 25.
 int pick_deal(const state_scan_args &a) {
     int best = 0;
     double least = 0;
     for (int i = 0; i < kDealCount; ++i) {
         const Deal &v = kDeals[i];
         const int channels = v.W / v.shares * 64 / v.lanes, chunk = v.lanes * v.T;
+        const int NB = staged_floats(v.lanes, v.T) / chunk, stages = (a.N + NB - 1) / NB;
         const int64_t tiles = (a.D / a.G + channels - 1) / channels;
         const double waves = (double)a.B * a.G * tiles * v.W;
         const double work = (double)a.N / v.shares * (7.6 * v.T + (v.lanes == 64 ? 18 : 15)) +
-                            (double)a.N * v.T * v.lanes / (16 * v.W) + 20. * v.T;
-        const double cost = ((a.L + chunk - 1) / chunk) * work * std::max(1., waves / 2560);
+                            (double)stages * NB * v.T * v.lanes / (16 * v.W) + 20. * v.T;
+        const double cost = ((a.L + chunk - 1) / chunk) *
+                            (work * std::max(1., waves / 2560) + 100. * stages);
         if (i == 0 || cost < least) best = i, least = cost;
     }
     return best;
@@ -395,12 +403,13 @@ hipError_t forward_any(const state_scan_args &a, hipStream_t s) {
         case 0: return forward<E, 8, 64, 16, 1, 1, 4>(a, s);
         case 1: return forward<E, 8, 64, 16, 1, 2, 4>(a, s);
         case 2: return forward<E, 8, 64, 16, 1, 4, 4>(a, s);
-        case 3: return forward<E, 8, 64, 8, 1, 2, 4>(a, s);
-        case 4: return forward<E, 4, 16, 16, 1, 1, 3>(a, s);
-        case 5: return forward<E, 4, 16, 8, 1, 1, 4>(a, s);
-        case 6: return forward<E, 4, 16, 4, 2, 1, 4>(a, s);
-        case 7: return forward<E, 8, 16, 8, 1, 4, 4>(a, s);
-        default: return forward<E, 8, 16, 8, 1, 2, 4>(a, s);
+        case 3: return forward<E, 8, 64, 8, 1, 1, 4>(a, s);
+        case 4: return forward<E, 8, 64, 8, 1, 2, 4>(a, s);
+        case 5: return forward<E, 8, 64, 8, 1, 4, 4>(a, s);
+        case 6: return forward<E, 4, 16, 16, 1, 1, 3>(a, s);
+        case 7: return forward<E, 4, 16, 4, 2, 1, 4>(a, s);
+        case 8: return forward<E, 8, 16, 8, 1, 2, 4>(a, s);
+        default: return forward<E, 8, 16, 8, 1, 4, 4>(a, s);
     }
 }
 

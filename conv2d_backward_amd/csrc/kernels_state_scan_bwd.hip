@@ -49,39 +49,35 @@ size_t lds_bytes(int W, int T, int joined, int64_t N) {
 
 Plan make_plan(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
     Plan p;
-    // A lane of 16 positions spends half as much on the lane scans as one of 8
-    // (30 instructions for both chains, beside some 24 a position): 288 us for
-    // 311 at [4, 2048, 2048], N = 16.  Not where padding the row to whole chunks
-    // costs more (78 us for 116 at [5, 1000, 301]), where there are too few chunks
-    // to give every compute unit one (33 us for 52 at [1, 256, 1000]), nor where its
-    // sums do not fit.
+    // Work-groups of 8 waves, one on a compute unit, lanes of 16 positions (which
+    // spend half as much on the lane scans as lanes of 8: 30 instructions for both
+    // chains, beside some 24 a position) unless padding the row to whole chunks costs
+    // more, there are too few chunks to give every compute unit one, or their sums do
+    // not fit.  Where that leaves the last round of compute units mostly empty,
+    // work-groups of 4 waves and lanes of 8, more of them cut finer, though they share
+    // less.  Measured (us, first / second way): [4, 2048, 2048] N 16 268 / 315,
+    // [1, 1024, 2048] N 16 60 / 65, [2, 547, 1364] N 64 174 / 174, but
+    // [5, 1825, 3409] N 8 686 / 498, [2, 1834, 640] N 64 239 / 207,
+    // [2, 340, 3307] N 64 304 / 249.
     const int64_t c16 = (L + 255) / 256, c8 = (L + 127) / 128;
-    const int64_t items = B * G * ((D / G + 8 * RPW - 1) / (8 * RPW));
-    p.T = c16 * (16 * 24 + 30) <= c8 * (8 * 24 + 30) && items * c16 >= 256 &&
-                  lds_bytes(8, 16, 1, N) <= kLdsBytes
-              ? 16
-              : 8;
-    p.chunk = LANES * p.T;
-    p.chunks = (int)((L + p.chunk - 1) / p.chunk);
-    // Work-groups of 8 waves, one on a compute unit; rows are cut until there are
-    // two for each.  Where their number leaves the last round of compute units
-    // mostly empty, work-groups of 4 waves, two on a compute unit, deal it finer
-    // though they share less (us, 8 / 4 waves: [2, 602, 777] N 24 G 2 82 / 74,
-    // [3, 333, 555] N 64 105 / 104, [1, 256, 1000] N 16 37 / 33; even ones
-    // [4, 2048, 2048] 281 / 304, [1, 1024, 2048] 63 / 67), and where even those come
-    // out uneven, cut rows do ([8, 1040, 2048] 457 whole, 391 cut in 8).
-    for (p.W = 8;; p.W = 4) {
-        p.tiles = (int)((D / G + p.W * RPW - 1) / (p.W * RPW));
-        const int64_t groups = B * G * p.tiles, units = 256 * (8 / p.W);
-        p.segments =
-            groups >= units ? 1 : (int)std::min<int64_t>(p.chunks, (2 * units + groups - 1) / groups);
-        const int64_t all = groups * p.segments, rounds = (all + units - 1) / units;
-        if (all >= rounds * units * 7 / 10) break;
-        if (p.W == 4) {
-            if (p.segments == 1) p.segments = std::min(p.chunks, 8);
-            break;
-        }
-    }
+    const int64_t wide = B * G * ((D / G + 8 * RPW - 1) / (8 * RPW));
+    const auto deal = [&](int W, int T, int64_t want) {
+        p.W = W;
+        p.T = T;
+        p.chunk = LANES * T;
+        p.chunks = (int)((L + p.chunk - 1) / p.chunk);
+        p.tiles = (int)((D / G + W * RPW - 1) / (W * RPW));
+        // As many segments as `want` work-groups need, evened out.
+        const int64_t groups = B * G * p.tiles;
+        const int most = (int)std::min<int64_t>(p.chunks, (want + groups - 1) / groups);
+        const int longest = (p.chunks + most - 1) / most;
+        p.segments = (p.chunks + longest - 1) / longest;
+        const int64_t rounds = (groups * p.segments + 255) / 256;
+        return (double)(groups * p.chunks) / (double)(rounds * 256 * longest);
+    };
+    const bool longer = c16 * (16 * 24 + 30) <= c8 * (8 * 24 + 30) && wide * c16 >= 256 &&
+                        lds_bytes(8, 16, 1, N) <= kLdsBytes;
+    if (deal(8, longer ? 16 : 8, 256) < 0.7) deal(4, 8, 1536);
     p.joined = p.T == 16 ? 2 : 4;
     while (lds_bytes(p.W, p.T, p.joined, N) > kLdsBytes) p.joined /= 2;
     p.lds = lds_bytes(p.W, p.T, p.joined, N);
@@ -177,6 +173,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
             A2 = a.A[at] * kLog2e;
             if (a.gstate) q = a.gstate[(int64_t)b * a.D * a.N + at];
             // Through the segments behind this one.
+#pragma unroll 4
             for (int later = a.p.segments - 1; later > seg; --later) {
                 const int64_t ls = (int64_t)b * a.p.segments + later;
                 q = __builtin_fmaf(exp2_fast(a.ws[a.p.steps + ls * a.D + g * Dg + c] * A2), q,
@@ -494,6 +491,7 @@ __global__ __launch_bounds__(256) void scan_join(const float *ws, Plan p, int64_
         const bool here = r < 2 * rows && t < L;
         const float *from = ws + p.sums + r * p.pitch + t;
         float4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
         for (int tile = wave; here && tile < p.tiles; tile += 4) {
             const float4 m = *reinterpret_cast<const float4 *>(from + tile * 2 * rows * p.pitch);
             v.x += m.x;
@@ -522,6 +520,7 @@ __global__ __launch_bounds__(256) void scan_join(const float *ws, Plan p, int64_
     const int64_t i = (blockIdx.x - matrix_blocks) * 256 + threadIdx.x;
     if (i >= D * (N + 2)) return;
     float v = 0.f;
+#pragma unroll 8
     for (int64_t s = 0; s < B * p.segments; ++s) v += ws[p.params + s * D * (N + 2) + i];
     const int64_t d = i / (N + 2), n = i % (N + 2);
     if (n < N) {
@@ -550,8 +549,8 @@ hipError_t backward(const state_scan_backward_args &a, hipStream_t s) {
                        kTailThreads, bytes, s>>>(k, tiles);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    const auto kernel = p.W == 8 ? (p.T == 16 ? scan_backward<E, 8, 16, 1> : scan_backward<E, 8, 8, 2>)
-                                 : (p.T == 16 ? scan_backward<E, 4, 16, 1> : scan_backward<E, 4, 8, 2>);
+    const auto kernel = p.W == 4 ? scan_backward<E, 4, 8, 2>
+                        : p.T == 16 ? scan_backward<E, 8, 16, 1> : scan_backward<E, 8, 8, 2>;
     if (p.lds > 64 * 1024) {
         e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)p.lds);
