@@ -318,6 +318,14 @@ def test_scan_backward_sizes(case):
     s.check_backward(s.forward(want_checkpoints=True)[2])
 
 
+@pytest.mark.parametrize("case", [(1, 2000, 2045, 4, 2), (1, 1030, 2045, 5, 1), (1, 260, 2050, 4, 2), (2, 1024, 1030, 4, 1),
+                                  (2, 4096, 250, 4, 1), (1, 1024, 2040, 4, 1)], ids=str)
+def test_scan_sizes_of_few_states(case):
+    """Rows of 64 lanes dealt in every way; backward by work-groups of 8 waves, whole rows and cut ones."""
+    s = Scan((*case, None, "dense"), "bf16")
+    s.check_backward(s.check_forward())
+
+
 @pytest.mark.parametrize("soft,gate,extras", [(True, False, True), (False, True, False), (True, True, False)])
 def test_scan_options(soft, gate, extras):
     s = Scan((2, 18, 150, 16, 1, None, "dense"), "f32", soft, gate, extras)
@@ -452,6 +460,16 @@ class Norm:
 @pytest.mark.parametrize("case", NORM, ids=str)
 @pytest.mark.parametrize("dtype", TYPES)
 def test_norm(case, dtype):
+    Norm(case, dtype).check()
+
+
+@pytest.mark.parametrize("case", [
+    # Tiles of 32, 16 and 8 columns, kept and read again.
+    (16, 33, 250, None, "dense"), (6, 70, 250, "ragged", "dense"), (6, 1030, 250, None, "padded"),
+    (1, 1100, 30, None, "dense"), (3, 2060, 100, "ragged", "slice"), (1, 4100, 20, None, "dense"),
+    (32, 2060, 250, None, "dense")], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_sizes(case, dtype):
     Norm(case, dtype).check()
 
 
