@@ -188,32 +188,36 @@ __global__ __launch_bounds__(kThreads) void conv_backward(ConvBwd<E> a) {
     // Each wave's first dp, for the lane before it.
     __shared__ float edge[2][kThreads / 64 + 1][K];
     const int wave = threadIdx.x / 64;
+    // This thread's channel in the first batch item, and its place in the list.
+    const auto *x0 = a.x.row(0, d), *gy0 = a.gy.row(0, d);
+    auto *dx0 = a.dx.row(0, d);
+    int b = first / a.s.segments * a.s.batch + bb, segment = first % a.s.segments;
     for (int i = first; i < last; ++i) {
-        const int b = i / a.s.segments * a.s.batch + bb;
-        const int t0 = (i % a.s.segments * along + lane) * kV;
+        const int t0 = (segment * along + lane) * kV;
         const bool here = channel && b < a.B && t0 < a.L;
         const int len = here ? length_of(a.lengths, b, a.L) : 0, left = len - t0;
-        const auto *x = a.x.row(here ? b : 0, here ? d : 0);
-        const auto *gy = a.gy.row(here ? b : 0, here ? d : 0);
+        const auto *x = x0 + b * a.x.batch, *gy = gy0 + b * a.gy.batch;
+        auto *dx = dx0 + b * a.dx.batch;
+        if (++segment == a.s.segments) segment = 0, b += a.s.batch;
         // x of positions t0-(K-1) .. t0+V-1, dp of t0 .. t0+V-1+(K-1).
-        float xs[kV + K], dp[kV + K], own[kV], g[kV];
-        load_row<E, kV>(x, t0, len, own);
-        load_row<E, kV>(gy, t0, len, g);
+        float xs[kV + K], dp[kV + K];
+        Octet<E> own, g, before;
+        own.load(x + t0, left);
+        g.load(gy + t0, left);
+        // A wave's first lane reads the positions before its own, others have their
+        // neighbour's.
+        const bool border = threadIdx.x % 64 == 0 && t0 > 0;
+        if (border) before.load(x + t0 - kV, left + kV);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-            xs[K - 1 + j] = own[j];
-            dp[j] = g[j];
+            xs[K - 1 + j] = own.at(j);
+            dp[j] = g.at(j);
         }
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) xs[j] = dpp0<kWaveShr>(own[kV - (K - 1) + j]);
-        if (threadIdx.x % 64 == 0 && t0 > 0) {
-            load_row<E, kV>(x, t0 - kV, len, own);
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) xs[j] = own[kV - (K - 1) + j];
-        }
-        if (t0 == 0) {
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) xs[j] = 0.f;
+        for (int j = 0; j < K - 1; ++j) {
+            xs[j] = dpp0<kWaveShr>(xs[kV + j]);
+            if (border) xs[j] = before.at(kV - (K - 1) + j);
+            if (t0 == 0) xs[j] = 0.f;
         }
         if (a.silu) {
 #pragma unroll
@@ -272,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void conv_backward(ConvBwd<E> a) {
 #pragma unroll
             for (int k = 0; k < K; ++k) out[j] = __builtin_fmaf(w[K - 1 - k], dp[j + k], out[j]);
         }
-        store_row<E, kV>(a.dx.row(b, d), t0, a.L, out);
+        store_row<E, kV>(dx, t0, a.L, out);
     }
     if (!a.dw && !a.db) return;
     // Sum over the threads of a channel: within waves, then over its waves in order.
