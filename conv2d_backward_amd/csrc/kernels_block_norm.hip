@@ -7,7 +7,9 @@
 // gate, r in, r_out, u out): a tile of few channels is read once, into
 // registers, one of many again, which finds much of it in the caches.  A tile's
 // rows are pieces of a cache line; the tiles that share the line run at the same
-// time on the same die (tile_of), whose L2 has it.
+// time on the same die (tile_of), whose L2 has it.  [4, 2048, 2048] bf16: 76 us
+// forward (235 MB, 3.1 TB/s): its work-groups, one a compute unit, read and write in
+// turn, with the sums between.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -275,9 +277,9 @@ __global__ __launch_bounds__(kTokenThreads) void norm_token(NormFwd<E> a) {
 // Backward: two passes over tiles of 64 columns by a share of the rows, so that
 // rows are read in whole cache lines and any shape fills the chip: the first
 // sums over channels, the second has every gradient of its elements.
-// [4, 2048, 2048] bf16: 38 + 75 us, the second at the rate of a large copy, the
-// first partly out of the memory-side cache.  A single pass with a work-group
-// per 32 columns and all channels, reading its tile twice, took 150 us.
+// [4, 2048, 2048] bf16: 40 + 66 us, the second at 5.6 TB/s, partly out of the
+// memory-side cache.  A single pass with a work-group per 32 columns and all
+// channels, reading its tile twice, took 150 us.
 constexpr int kBwdThreads = 256, kBwdCV = 8, kBwdRows = kBwdThreads / kBwdCV;
 
 struct BwdShape {

@@ -8,10 +8,11 @@
 // log2(lanes) steps, and each lane runs its chain again from the state it then
 // knows, adding C_t h_t to its outputs.  Every exponential is taken once.
 //
-// What bounds it: for each (channel, state, position) one v_exp_f32 (a quarter
-// rate instruction) and five full-rate ones, about 10 issue slots of 4 cycles
-// for 64 elements with the lane scan; the bytes (x, dt, z, y) are 1/N of that
-// many elements.
+// What bounds it: for each (channel, state, position) one v_exp_f32 (8 cycles of
+// its SIMD for 64 lanes) and five full-rate instructions (4 cycles); the bytes (x,
+// dt, z, y) are 1/N of that many elements.  [1, 4096, 8192] bf16, N = 16: 178 us,
+// the vector ALUs busy for 89% of it; the instructions named would take 103 us, and
+// the lane scan, the steps and gates and the staging of B and C add 3.8 to their 6.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -41,9 +42,9 @@ struct ScanFwd {
 // A work-group: W waves, each 64/LANES rows (channels) of LANES lanes, each lane
 // T consecutive positions of a chunk of LANES * T; NI states at a time, whose
 // chains have nothing to do with each other.  NS waves share their rows, each
-// with every NS-th group of NI states; their outputs meet in LDS.  LDS: B and C of NB states over the
-// chunk (fp32, in the order the lanes read them), then A log2(e) and the
-// running state of every (state, channel).
+// with every NS-th group of NI states; their outputs meet in LDS.  LDS: B and C of
+// NB states over the chunk (fp32, in the order the lanes read them), then A log2(e)
+// and the running state of every (state, channel).
 template <class E, int W, int LANES, int T, int NI, int NS, int OCC>
 __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
     constexpr int kThreads = 64 * W, CH = W / NS * 64 / LANES, CHUNK = LANES * T;
@@ -421,7 +422,7 @@ hipError_t step(const state_scan_step_args &a, hipStream_t s) {
     const int V = a.N % 4 == 0 ? 4 : 1;
     while (k.row_lanes < 16 && k.row_lanes * V < a.N) k.row_lanes *= 2;
     // Two channels a lane where half the work-groups still fill the chip many times
-    // over ([256, 4096], N = 16: 32.7 us, 4.1 TB/s; one 36.6, four 37.6), one where
+    // over ([256, 4096], N = 16: 32.3 us, 4.4 TB/s; one 36.6, four 37.6), one where
     // latency counts.
     const int64_t rows = kThreads / k.row_lanes, groups = (a.D + rows - 1) / rows * a.B;
     const int R = groups >= 8192 ? 2 : 1;
