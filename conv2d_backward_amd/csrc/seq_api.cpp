@@ -16,12 +16,22 @@ namespace {
 constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
 constexpr int64_t kMaxPositions = (int64_t)1 << 26;
+constexpr int64_t kMaxBatchPositions = (int64_t)1 << 31;  // of all batch items; counted in 32 bits
+// A norm's work-groups of 1024 own 32 positions, and a grid has less than 2^32 work-items.
+constexpr int64_t kMaxNormTiles = (int64_t)1 << 22;
 
 int check_sizes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
     if (dtype != SEQ_F32 && dtype != SEQ_BF16 && dtype != SEQ_F16) return CONV2D_GI_EINVAL;
     if (B < 1 || D < 1 || L < 1) return CONV2D_GI_EINVAL;
-    if (B > kMaxBatch || B * D >= kMaxRows || L > kMaxPositions) return CONV2D_GI_EUNSUPPORTED;
+    if (B > kMaxBatch || B * D >= kMaxRows || L > kMaxPositions || B * L >= kMaxBatchPositions)
+        return CONV2D_GI_EUNSUPPORTED;
     return CONV2D_GI_OK;
+}
+
+int check_norm(int64_t B, int64_t D, int64_t L, float eps) {
+    if (D > SEQ_MAX_NORM_CHANNELS || B * ((L + 31) / 32) >= kMaxNormTiles)
+        return CONV2D_GI_EUNSUPPORTED;
+    return eps >= 0.f ? CONV2D_GI_OK : CONV2D_GI_EINVAL;
 }
 
 int check_taps(int32_t K) {
@@ -153,9 +163,8 @@ int state_scan_step(const state_scan_step_args *a, hipStream_t stream) {
 int block_norm_forward(const block_norm_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc == CONV2D_GI_OK) rc = check_norm(a->B, a->D, a->L, a->eps);
     if (rc != CONV2D_GI_OK) return rc;
-    if (a->D > SEQ_MAX_NORM_CHANNELS) return CONV2D_GI_EUNSUPPORTED;
-    if (!(a->eps >= 0.f)) return CONV2D_GI_EINVAL;
     if (!a->y.data || !a->r.data || !a->r_out.data) return CONV2D_GI_EINVAL;
     if (!a->w_pre != !a->u.data) return CONV2D_GI_EINVAL;
     if (!is_apart(a->r_out, a->B, a->D, a->L) ||
@@ -168,16 +177,16 @@ int block_norm_forward(const block_norm_args *a, hipStream_t stream) {
 }
 
 int64_t block_norm_workspace(int32_t B, int32_t D, int32_t L, int32_t backward) {
-    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK || D > SEQ_MAX_NORM_CHANNELS) return -1;
+    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK || check_norm(B, D, L, 0.f) != CONV2D_GI_OK)
+        return -1;
     return seq::norm_workspace(B, D, L, backward != 0);
 }
 
 int block_norm_backward(const block_norm_backward_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc == CONV2D_GI_OK) rc = check_norm(a->B, a->D, a->L, a->eps);
     if (rc != CONV2D_GI_OK) return rc;
-    if (a->D > SEQ_MAX_NORM_CHANNELS) return CONV2D_GI_EUNSUPPORTED;
-    if (!(a->eps >= 0.f)) return CONV2D_GI_EINVAL;
     if (!a->y.data || !a->r_out.data || !a->dy.data || !a->dr.data) return CONV2D_GI_EINVAL;
     if ((a->gu.data && !a->w_pre) || !a->gate.data != !a->dgate.data) return CONV2D_GI_EINVAL;
     if ((a->dscale && !a->scale) || (a->dw_post && !a->w_post) || (a->dw_pre && !a->w_pre))

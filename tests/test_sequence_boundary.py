@@ -135,6 +135,14 @@ def test_refuses_sizes_and_types(lib, name):
         assert call(name, slots=0, lines=1) == gi.EINVAL   # fewer lines than rows
 
 
+@pytest.mark.parametrize("name", sorted(n for n in STRUCTS if "L" in fields_of(n)))
+def test_refuses_more_positions_than_a_grid_has(lib, name):
+    assert call(name, B=32, L=1 << 26) == gi.EUNSUPPORTED
+    if name.startswith("block_norm"):
+        assert call(name, B=8, L=1 << 24) == gi.EUNSUPPORTED
+        assert lib.block_norm_workspace(8, 4, 1 << 24, 1) == -1 < lib.block_norm_workspace(8, 4, 1 << 23, 1)
+
+
 OUTPUTS = {"causal_conv": ("y",), "causal_conv_backward": ("dx",), "causal_conv_step": ("y",),
            "state_scan": ("y",), "state_scan_backward": ("dx", "ddt", "dz"), "state_scan_step": ("y",),
            "block_norm": ("r_out", "u"), "block_norm_backward": ("dy", "dr", "dgate")}
