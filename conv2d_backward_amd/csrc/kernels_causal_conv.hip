@@ -52,10 +52,10 @@ __global__ __launch_bounds__(kThreads) void conv_forward(ConvFwd<E> a) {
     Octet<E> own[R];
 #pragma unroll
     for (int c = 0; c < R; ++c) {
-        // (All of the row: what lies beyond the length reaches no output before it, and
-        // the length need not be there yet.)
+        // (What lies beyond the length is not read: 9.5 us for 10.7 at [5, 1000, 1237] fp16
+        // with half of the positions there, though the length must arrive first.)
         const int t = start + (c * a.row_threads + lane) * kV;
-        own[c].load(x + t, a.L - t);
+        own[c].load(x + t, len - t);
     }
     float past[K], w[K];  // K-1 of past used
 #pragma unroll
