@@ -30,7 +30,7 @@ namespace {
 
 constexpr int LANES = 16, RPW = 64 / LANES;
 constexpr int kNB = 16;  // states whose B and C are in LDS at once
-constexpr int kTailT = 8, kTailWaves = 4, kTailThreads = 64 * kTailWaves,
+constexpr int kTailT = 8, kTailNI = 4, kTailWaves = 4, kTailThreads = 64 * kTailWaves,
               kTailCH = kTailWaves * RPW;
 
 struct Plan {
@@ -447,25 +447,35 @@ __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tile
         for (int n0 = 0; n0 < a.N; n0 += kNB) {
             const int nb = std::min(kNB, a.N - n0);
             __syncthreads();
-            for (int o = tid; o < nb * (CHUNK / 8); o += kTailThreads) {
+            for (int o = tid; o < kNB * (CHUNK / 8); o += kTailThreads) {
                 Octet<E> v;
-                const int t = c0 + o % (CHUNK / 8) * 8;
-                v.load(a.Cm.row(b, (int64_t)g * a.N + n0 + o / (CHUNK / 8)) + t, len - t);
+                const int t = c0 + o % (CHUNK / 8) * 8, n = n0 + o / (CHUNK / 8);
+                v.load(a.Cm.row(b, (int64_t)g * a.N + n) + t, n < a.N ? len - t : 0);
                 stage_octet<E, LANES, T>(sC, o, v);
             }
             __syncthreads();
-            for (int n = 0; n < nb; ++n) {
+            // kTailNI states at once: there are few waves, and one chain waits for itself
+            // (67 us for 61 at [4, 420, 3640] f32, N = 24).  States past N have A and C 0 and
+            // change nothing.
+            for (int n = 0; n < nb; n += kTailNI) {
                 const int at = (n0 + n) * kTailCH + ch;
-                const float A2 = sA[at], carry = sG[at];
-                float Cv[T];
-                fetch<T>(sC + n * CHUNK, lane, Cv);
-                float q = lane == LANES - 1 ? carry : 0.f;
+                float A2[kTailNI], q[kTailNI], P[kTailNI], turned[kTailNI], Cv[kTailNI][T];
+#pragma unroll
+                for (int k = 0; k < kTailNI; ++k) {
+                    A2[k] = sA[at + k * kTailCH];
+                    q[k] = lane == LANES - 1 ? sG[at + k * kTailCH] : 0.f;
+                    fetch<T>(sC + (n + k) * CHUNK, lane, Cv[k]);
+                    P[k] = exp2_fast(total * A2[k]);
+                }
 #pragma unroll
                 for (int i = T - 1; i >= 0; --i)
-                    q = exp2_fast(s[i] * A2) * __builtin_fmaf(Cv[i], gy[i], q);
-                float P = exp2_fast(total * A2), turned;
-                scan_chain_back(q, P, turned);
-                if (lane == 0) sG[at] = q;
+#pragma unroll
+                    for (int k = 0; k < kTailNI; ++k)
+                        q[k] = exp2_fast(s[i] * A2[k]) * __builtin_fmaf(Cv[k][i], gy[i], q[k]);
+                scan_lanes_back<kTailNI>(q, P, turned);
+#pragma unroll
+                for (int k = 0; k < kTailNI; ++k)
+                    if (lane == 0) sG[at + k * kTailCH] = q[k];
             }
         }
     }
