@@ -165,6 +165,11 @@ __global__ __launch_bounds__(NT) void norm_forward(NormFwd<E> a) {
         float u[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) u[i] = r[q][i] * (sum[0][i] * w);
+        if (left < kV) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)  // 0 beyond the length also where eps or w leave 0 * inf
+                u[i] = left > i ? u[i] : 0.f;
+        }
         store_row<E, kV>(a.u.row(b, d), t0, a.L, u);
     }
 }
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(kTokenThreads) void norm_token(NormFwd<E> a) {
         float w[V];
         load_channels<F32, V>(a.w_pre, 1, d, D, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) w[i] *= r[q][i] * i_pre;
+        for (int i = 0; i < V; ++i) w[i] = in ? w[i] * (r[q][i] * i_pre) : 0.f;
         store_channels<E, V>(a.u.row(b, 0), a.u.channel, d, D, w);
     }
 }

@@ -1,0 +1,104 @@
+"""The sequence kernels where a position, a length or a part is missing, and where
+values are infinite, zero or tiny, against the float64 oracle.
+
+Tolerances and their counts are those of test_gpu_sequence.py.  The oracle sees
+each sequence cut to its length, so that nothing beyond one enters a sum.
+"""
+import pytest
+
+from oracle import sequence as oracle
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+from test_gpu_sequence import TYPES, Inputs, check, num, poison  # noqa: E402
+
+import conv2d_backward_amd as gi  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    gi.load_library()
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def ends(lengths, B, L):
+    return [L] * B if lengths is None else [min(max(n, 0), L) for n in lengths.tolist()]
+
+
+def beyond(t, lengths):
+    """The values of t [B, D, L] beyond the lengths, in one row."""
+    return torch.cat([t[b, :, n:].flatten() for b, n in enumerate(ends(lengths, t.shape[0], t.shape[-1]))])
+
+
+# ---- block_norm ----------------------------------------------------------------------------------
+
+
+class Norm:
+    def __init__(self, B, D, L, dtype, lengths=None, parts="post pre gate scale", eps=0.0, size=1.0):
+        i = Inputs(B + D + L, dtype)
+        self.eps, self.n = eps, None if lengths is None else ints(*lengths)
+
+        def act(dtype=None, scale=1.0):
+            return poison(i.normal(B, D, L, dtype=dtype, scale=scale), self.n)
+
+        parts = parts.split()
+        self.y, self.r, self.gr = act(scale=size), act(torch.float32, size), act(torch.float32)
+        self.post = i.params(D) if "post" in parts else None
+        self.pre = i.params(D) if "pre" in parts else None
+        self.gate = act() if "gate" in parts else None
+        self.scale = i.params(D) if "scale" in parts else None
+        self.gu = act() if "pre" in parts else None
+
+    def forward(self):
+        return gi.block_norm(self.y, self.r, self.post, self.pre, gate=self.gate, scale=self.scale, eps=self.eps,
+                             lengths=self.n)
+
+    def by_sequence(self, function, acts):
+        """function(activations of one sequence, weights) of each sequence that has positions: [(b, length, result)]."""
+        B, _, L = self.y.shape
+        weights = num(self.post, self.pre)
+        out = []
+        for b, n in enumerate(ends(self.n, B, L)):
+            if n:
+                cut = [None if v is None else v[b:b + 1, :, :n] for v in num(*acts, self.gate)]
+                out.append((b, n, function(*cut[:-1], *weights, cut[-1], *num(self.scale), self.eps)))
+        return out
+
+    def check_forward(self):
+        B, D, L = self.y.shape
+        r, u = self.forward()
+        for b, n, (rr, ru, Sr, Su) in self.by_sequence(oracle.block_norm, (self.y, self.r)):
+            check(r[b:b + 1, :, :n], rr, Sr, D + 32, "residual")
+            if u is not None:
+                check(u[b:b + 1, :, :n], ru, Su, 2 * D + 64, "u")
+        for v in (r, u):
+            assert v is None or bool((beyond(v, self.n) == 0).all())
+        return r
+
+
+AT_ZERO = [  # B, D, L, lengths
+    (1, 20, 9, None), (4, 20, 9, (9, 0, 3, 8)), (3, 70, 1, (1, 0, 1)), (2, 4200, 1, (0, 1)), (3, 130, 70, (70, 64, 1)),
+    (2, 2060, 33, (0, 20)), (1, 4200, 21, None), (130, 33, 40, tuple(range(130))),
+]
+
+
+@pytest.mark.parametrize("case", AT_ZERO, ids=lambda c: "x".join(map(str, c[:3])))
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_without_eps(case, dtype):
+    """Positions that nothing is added to have no root of zero in them: 0 where the contract says 0."""
+    B, D, L, lengths = case
+    Norm(B, D, L, dtype, lengths).check_forward()
+
+
+@pytest.mark.parametrize("D,L", [(20, 9), (20, 1), (4200, 12)])
+def test_norm_is_zero_beyond_lengths_whatever_the_weight(D, L):
+    s = Norm(2, D, L, "bf16", (L // 2, 0), eps=1e-6)
+    s.pre[3], s.pre[4] = float("inf"), float("nan")
+    for v in s.forward():
+        assert bool((beyond(v, s.n) == 0).all())
