@@ -426,9 +426,12 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a)
     __syncthreads();
     if (tid < COLS) {
         const float D = (float)a.D;
-        const float i_pre = inverse_rms(sums[1][tid], a.D, a.eps);
+        // Columns without a position get 0 for both roots (1/0 at eps = 0): their zeros
+        // go through the same sums as the others' values and add nothing.
+        const bool here = bt % a.s.tiles * COLS + tid < length_of(a.lengths, b, a.L);
+        const float i_pre = here ? inverse_rms(sums[1][tid], a.D, a.eps) : 0.f;
         const float c_pre = i_pre * i_pre * i_pre * (sums[2][tid] / D);
-        const float i_post = a.w_post ? inverse_rms(sums[0][tid], a.D, a.eps) : 1.f;
+        const float i_post = !here ? 0.f : a.w_post ? inverse_rms(sums[0][tid], a.D, a.eps) : 1.f;
         const float m = sums[3][tid] + i_pre * sums[4][tid] - c_pre * sums[5][tid];
         coef[0][tid] = i_post;
         coef[1][tid] = i_pre;

@@ -59,6 +59,10 @@ class Norm:
         return gi.block_norm(self.y, self.r, self.post, self.pre, gate=self.gate, scale=self.scale, eps=self.eps,
                              lengths=self.n)
 
+    def backward(self, r):
+        return gi.block_norm_backward(self.gr, self.gu, self.y, r, self.post, self.pre, gate=self.gate,
+                                      scale=self.scale, eps=self.eps, lengths=self.n)
+
     def by_sequence(self, function, acts):
         """function(activations of one sequence, weights) of each sequence that has positions: [(b, length, result)]."""
         B, _, L = self.y.shape
@@ -81,6 +85,22 @@ class Norm:
             assert v is None or bool((beyond(v, self.n) == 0).all())
         return r
 
+    def check_backward(self, r):
+        B, D, L = self.y.shape
+        g = self.backward(r)._asdict()
+        whole = {}
+        for b, n, ref in self.by_sequence(oracle.block_norm_grads, (self.gr, self.gu, self.y, r)):
+            for name, v in ref.items():
+                if v.ndim == 1:
+                    whole[name] = whole.get(name, 0) + v
+                elif not name.startswith("S"):
+                    check(g[name][b:b + 1, :, :n], v, ref["S" + name], 4 * D + 128, name)
+        for name, got in g.items():
+            if got is not None and got.dim() == 1:
+                check(got, whole[name], whole["S" + name], 4 * D + 128 + B * L, name)
+            elif got is not None:
+                assert bool((beyond(got, self.n) == 0).all()), name
+
 
 AT_ZERO = [  # B, D, L, lengths
     (1, 20, 9, None), (4, 20, 9, (9, 0, 3, 8)), (3, 70, 1, (1, 0, 1)), (2, 4200, 1, (0, 1)), (3, 130, 70, (70, 64, 1)),
@@ -102,3 +122,12 @@ def test_norm_is_zero_beyond_lengths_whatever_the_weight(D, L):
     s.pre[3], s.pre[4] = float("inf"), float("nan")
     for v in s.forward():
         assert bool((beyond(v, s.n) == 0).all())
+
+
+@pytest.mark.parametrize("case", AT_ZERO, ids=lambda c: "x".join(map(str, c[:3])))
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_gradients_without_eps(case, dtype):
+    """Columns without a position add nothing to the parameters' gradients."""
+    B, D, L, lengths = case
+    s = Norm(B, D, L, dtype, lengths)
+    s.check_backward(s.forward()[0])
