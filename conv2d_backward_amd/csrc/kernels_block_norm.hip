@@ -341,9 +341,11 @@ struct NormIn {
     }
 };
 
-// With q = scale sigmoid(gate) w_post y the mean that dy's norm needs,
-// sum_d q dr, splits over dr = gr + i (gu w_pre) - r i^3 c into sums of the
-// inputs, so that one pass has all six sums.
+// With v the gradient of rms(x) = x i, x's is i (v - (x i) k), k = i mean(v x): x i and
+// k are of order 1 and of v, where x i^3 mean(v x) overflows for x under 2^-42.
+// With q = scale sigmoid(gate) w_post y the mean that dy's norm needs, sum_d q dr,
+// splits over dr = gr + i (gu w_pre - (r i) k) into sums of the inputs, so that one
+// pass has all six sums.
 template <class E>
 __global__ __launch_bounds__(kBwdThreads) void norm_backward_sums(NormBwd<E> a) {
     constexpr int COLS = kV * kBwdCV;
@@ -406,7 +408,7 @@ template <class E>
 __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a) {
     constexpr int COLS = kV * kBwdCV;
     __shared__ float sums[6][COLS];
-    __shared__ float coef[4][COLS];  // i_post, i_pre, c_pre, c_post
+    __shared__ float coef[4][COLS];  // i_post, i_pre, k_pre, k_post
     const int cv = threadIdx.x % kBwdCV, tid = threadIdx.x;
     // From the last tile back: the caches hold what the first pass read last.
     const int all = a.B * a.s.tiles, wg = tile_of(gridDim.x - 1 - blockIdx.x, gridDim.x);
@@ -430,22 +432,22 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a)
         // go through the same sums as the others' values and add nothing.
         const bool here = bt % a.s.tiles * COLS + tid < length_of(a.lengths, b, a.L);
         const float i_pre = here ? inverse_rms(sums[1][tid], a.D, a.eps) : 0.f;
-        const float c_pre = i_pre * i_pre * i_pre * (sums[2][tid] / D);
+        const float k_pre = i_pre * (sums[2][tid] / D);
         const float i_post = !here ? 0.f : a.w_post ? inverse_rms(sums[0][tid], a.D, a.eps) : 1.f;
-        const float m = sums[3][tid] + i_pre * sums[4][tid] - c_pre * sums[5][tid];
+        const float m = sums[3][tid] + i_pre * (sums[4][tid] - k_pre * (i_pre * sums[5][tid]));
         coef[0][tid] = i_post;
         coef[1][tid] = i_pre;
-        coef[2][tid] = c_pre;
-        coef[3][tid] = a.w_post ? i_post * i_post * i_post * (m / D) : 0.f;
+        coef[2][tid] = k_pre;
+        coef[3][tid] = a.w_post ? i_post * (m / D) : 0.f;
     }
     __syncthreads();
-    float i_post[kV], i_pre[kV], c_pre[kV], c_post[kV];
+    float i_post[kV], i_pre[kV], k_pre[kV], k_post[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
         i_post[i] = coef[0][cv * kV + i];
         i_pre[i] = coef[1][cv * kV + i];
-        c_pre[i] = coef[2][cv * kV + i];
-        c_post[i] = coef[3][cv * kV + i];
+        k_pre[i] = coef[2][cv * kV + i];
+        k_post[i] = coef[3][cv * kV + i];
     }
     for (int d = lo + tid / kBwdCV; d < hi; d += kBwdRows) {
         float p[3] = {0.f, 0.f, 0.f};
@@ -460,15 +462,16 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a)
             for (int i = 0; i < kV; ++i) {
                 const float y = in.y.at(i), r = in.r.at(i), gu = in.gu.at(i);
                 const float open = in.open(a, i);
-                const float drv = in.gr.at(i) + i_pre[i] * (gu * w) - r * c_pre[i];
+                const float ri = r * i_pre[i];
+                const float drv = in.gr.at(i) + i_pre[i] * (gu * w - ri * k_pre[i]);
                 const float yi = y * i_post[i], n = yi * wq, dn = drv * scale * open;
                 p[0] = __builtin_fmaf(drv * open, n, p[0]);
                 p[1] = __builtin_fmaf(dn, yi, p[1]);
-                p[2] = __builtin_fmaf(gu * r, i_pre[i], p[2]);
+                p[2] = __builtin_fmaf(gu, ri, p[2]);
                 const bool inside = left > i;
                 dr[i] = inside ? drv : 0.f;
                 dgate[i] = inside ? dn * n * (1.f - open) : 0.f;
-                dy[i] = inside ? i_post[i] * (dn * wq) - y * c_post[i] : 0.f;
+                dy[i] = inside ? i_post[i] * (dn * wq - yi * k_post[i]) : 0.f;
             }
             store_row<F32, kV>(a.dr.row(b, d), t0, a.L, dr);
             store_row<E, kV>(a.dy.row(b, d), t0, a.L, dy);

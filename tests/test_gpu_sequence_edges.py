@@ -131,3 +131,12 @@ def test_norm_gradients_without_eps(case, dtype):
     B, D, L, lengths = case
     s = Norm(B, D, L, dtype, lengths)
     s.check_backward(s.forward()[0])
+
+
+@pytest.mark.parametrize("parts", ["post pre gate scale", "pre", "post"])
+@pytest.mark.parametrize("size", [2.0 ** -50, 2.0 ** -60, 2.0 ** 50])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_gradients_of_tiny_and_huge_values(parts, size, dtype):
+    """The inverse root's cube is beyond float32 for values under 2^-42, the gradients are not."""
+    s = Norm(2, 40, 13, dtype, (13, 6), parts, size=size)
+    s.check_backward(s.check_forward())
