@@ -318,14 +318,18 @@ struct NormBwd {
     float eps;
 };
 
-// An element vector of every input; missing ones are zeros.
+// An element vector of every input; missing ones are zeros, and so is the new residual
+// without a norm of it.
 template <class E>
 struct NormIn {
     Octet<E> y, gate, gu;
     Octet<F32> r, gr;
     __device__ __forceinline__ void load(const NormBwd<E> &a, int b, int d, int t0, int left) {
         y.load(a.y.row(b, d) + t0, left);
-        r.load(a.r_out.row(b, d) + t0, left);
+        if (a.w_pre)
+            r.load(a.r_out.row(b, d) + t0, left);
+        else
+            r.zero();
         if (a.gr.p)
             gr.load(a.gr.row(b, d) + t0, left);
         else
@@ -431,7 +435,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a)
         // Columns without a position get 0 for both roots (1/0 at eps = 0): their zeros
         // go through the same sums as the others' values and add nothing.
         const bool here = bt % a.s.tiles * COLS + tid < length_of(a.lengths, b, a.L);
-        const float i_pre = here ? inverse_rms(sums[1][tid], a.D, a.eps) : 0.f;
+        const float i_pre = here && a.w_pre ? inverse_rms(sums[1][tid], a.D, a.eps) : 0.f;
         const float k_pre = i_pre * (sums[2][tid] / D);
         const float i_post = !here ? 0.f : a.w_post ? inverse_rms(sums[0][tid], a.D, a.eps) : 1.f;
         const float m = sums[3][tid] + i_pre * (sums[4][tid] - k_pre * (i_pre * sums[5][tid]));
@@ -471,7 +475,9 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_apply(NormBwd<E> a)
                 const bool inside = left > i;
                 dr[i] = inside ? drv : 0.f;
                 dgate[i] = inside ? dn * n * (1.f - open) : 0.f;
-                dy[i] = inside ? i_post[i] * (dn * wq - yi * k_post[i]) : 0.f;
+                // (Without a norm of y its value has no part in dy, though it be infinite.)
+                const float part = a.w_post ? yi * k_post[i] : 0.f;
+                dy[i] = inside ? i_post[i] * (dn * wq - part) : 0.f;
             }
             store_row<F32, kV>(a.dr.row(b, d), t0, a.L, dr);
             store_row<E, kV>(a.dy.row(b, d), t0, a.L, dy);

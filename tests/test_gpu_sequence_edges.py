@@ -140,3 +140,21 @@ def test_norm_gradients_of_tiny_and_huge_values(parts, size, dtype):
     """The inverse root's cube is beyond float32 for values under 2^-42, the gradients are not."""
     s = Norm(2, 40, 13, dtype, (13, 6), parts, size=size)
     s.check_backward(s.check_forward())
+
+
+def test_norm_gradients_of_norms_that_are_not_there():
+    """Without a norm its input has no part in the gradients: no mean, no root of zero, no NaN of its own."""
+    s = Norm(2, 20, 9, "f32", parts="post gate scale")
+    r, _ = s.forward()
+    want = s.backward(r)
+    for value in (0.0, float("nan"), float("inf"), 1e30):
+        r[0, :, 4] = value
+        got = s.backward(r)
+        assert torch.equal(got.dresidual, s.gr)
+        assert all(p is q is None or torch.equal(p, q) for p, q in zip(got, want)), value
+    s = Norm(2, 20, 9, "f32", parts="pre gate scale")
+    r, _ = s.forward()
+    want = s.backward(r)
+    for value in (0.0, float("nan"), float("inf")):
+        s.y[1, 3, 7] = value
+        assert torch.equal(s.backward(r).dy, want.dy) and torch.equal(s.backward(r).dresidual, want.dresidual)
