@@ -230,11 +230,23 @@ __global__ __launch_bounds__(kThreads) void conv_backward(ConvBwd<E> a) {
                 dp[j] = left > j ? dp[j] * silu_slope(p) : 0.f;
             }
         }
+        if (left >= kV) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
+            for (int j = 0; j < kV; ++j) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) sums[k] = __builtin_fmaf(dp[j], xs[j + k], sums[k]);
-            sums[K] += dp[j];
+                for (int k = 0; k < K; ++k) sums[k] = __builtin_fmaf(dp[j], xs[j + k], sums[k]);
+                sums[K] += dp[j];
+            }
+        } else {
+            // A position beyond the length multiplies none of the values inside, which
+            // may be infinite: 0 for its dp is not enough.
+#pragma unroll
+            for (int j = 0; j < kV - 1; ++j) {
+                if (left <= j) continue;
+#pragma unroll
+                for (int k = 0; k < K; ++k) sums[k] = __builtin_fmaf(dp[j], xs[j + k], sums[k]);
+                sums[K] += dp[j];
+            }
         }
         if (!a.dx.p) continue;
         // The next positions' dp: the lane after's first, or the wave after's; the last

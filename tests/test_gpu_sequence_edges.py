@@ -158,3 +158,23 @@ def test_norm_gradients_of_norms_that_are_not_there():
     for value in (0.0, float("nan"), float("inf")):
         s.y[1, 3, 7] = value
         assert torch.equal(s.backward(r).dy, want.dy) and torch.equal(s.backward(r).dresidual, want.dresidual)
+
+
+# ---- causal_conv ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("L,lengths", [(13, None), (21, (21, 5, 18)), (700, (699, 0, 130)), (2077, (2077, 2049, 2050))])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_conv_taps_take_only_positions_they_meet(L, lengths, value):
+    """x[len-1] meets the last tap alone."""
+    i = Inputs(L, "f32")
+    n = None if lengths is None else ints(*lengths)
+    x, gy, w = i.normal(3, 5, L), i.normal(3, 5, L), i.params(5, 4)
+    at = L if n is None else ends(n, 3, L)[0]
+    x[0, 2, at - 1] = value
+    dx, dw, db = gi.causal_conv_backward(poison(gy, n), poison(x, n), w, silu=False, lengths=n, want_db=True)
+    bad = ~torch.isfinite(dw)
+    assert bad[2].tolist() == [False, False, False, True] and int(bad.sum()) == 1
+    assert bool(torch.isfinite(dx).all()) and bool(torch.isfinite(db).all())
+    if value == float("inf"):
+        assert float(dw[2, 3]) == value * float(torch.sign(gy[0, 2, at - 1]))
