@@ -289,6 +289,11 @@ __global__ __launch_bounds__(kThreads) void conv_backward(ConvBwd<E> a) {
 #pragma unroll
             for (int k = 0; k < K; ++k) out[j] = __builtin_fmaf(w[K - 1 - k], dp[j + k], out[j]);
         }
+        if (left < kV) {
+#pragma unroll
+            for (int j = 0; j < kV; ++j)  // 0 beyond the length also where a weight is infinite
+                out[j] = left > j ? out[j] : 0.f;
+        }
         store_row<E, kV>(dx, t0, a.L, out);
     }
     if (!a.dw && !a.db) return;

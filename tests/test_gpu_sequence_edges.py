@@ -178,3 +178,13 @@ def test_conv_taps_take_only_positions_they_meet(L, lengths, value):
     assert bool(torch.isfinite(dx).all()) and bool(torch.isfinite(db).all())
     if value == float("inf"):
         assert float(dw[2, 3]) == value * float(torch.sign(gy[0, 2, at - 1]))
+
+
+@pytest.mark.parametrize("silu", [True, False])
+def test_conv_gradient_is_zero_beyond_lengths_whatever_the_weight(silu):
+    i = Inputs(3, "bf16")
+    n = ints(21, 0, 5, 600)
+    x, gy, w = poison(i.normal(4, 5, 700), n), poison(i.normal(4, 5, 700), n), i.params(5, 4)
+    w[1, 0], w[2, 3], w[3, 2] = float("inf"), float("nan"), -float("inf")
+    dx = gi.causal_conv_backward(gy, x, w, silu=silu, lengths=n)[0]
+    assert bool((beyond(dx, n) == 0).all())
