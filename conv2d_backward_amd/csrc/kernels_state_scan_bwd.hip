@@ -355,6 +355,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
                 sum_skip = __builtin_fmaf(gy[i], x[i], sum_skip);
                 ds[i] = __builtin_fmaf(ds[i], kLn2, x[i] * gB[i]);
             }
+            if (len - t0 < T) {
+#pragma unroll
+                for (int i = 0; i < T; ++i) o[i] = len - t0 > i ? o[i] : 0.f;
+            }
             store_row<E, T>(a.dx.row(b, d), t0, a.L, o);
             if (a.softplus) {
                 load_row<E, T>(a.dt.row(b, d), t0, len, v);

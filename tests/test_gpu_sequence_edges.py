@@ -11,6 +11,7 @@ from oracle import sequence as oracle
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
+import test_gpu_sequence as base  # noqa: E402
 from test_gpu_sequence import TYPES, Inputs, check, num, poison  # noqa: E402
 
 import conv2d_backward_amd as gi  # noqa: E402
@@ -188,3 +189,18 @@ def test_conv_gradient_is_zero_beyond_lengths_whatever_the_weight(silu):
     w[1, 0], w[2, 3], w[3, 2] = float("inf"), float("nan"), -float("inf")
     dx = gi.causal_conv_backward(gy, x, w, silu=silu, lengths=n)[0]
     assert bool((beyond(dx, n) == 0).all())
+
+
+# ---- state_scan ----------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("case", [(4, 20, 45, 5, 1), (4, 36, 300, 16, 2), (4, 2000, 600, 4, 2)], ids=str)
+def test_scan_gradients_are_zero_beyond_lengths_whatever_the_skip(case):
+    s = base.Scan((*case, None, "dense"), "bf16")
+    s.n = ints(case[2], 0, 7, 30)
+    for v in (s.x, s.dt, s.z, s.gout, s.B, s.C):
+        poison(v, s.n)
+    s.skip[1], s.skip[2] = float("inf"), float("nan")
+    g = s.backward(s.forward(want_checkpoints=True)[2])
+    for v in (g.dx, g.ddt, g.dz):
+        assert bool((beyond(v, s.n) == 0).all())
