@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * W, OCC) void scan_forward(ScanFwd<E> a) {
         const int dc = g * Dg + std::min(tile * CH + c, Dg - 1);
         float2 v = {0.f, 0.f};
         if (n < a.N) {
-            v.x = a.A[(int64_t)dc * a.N + n] * kLog2e;
+            v.x = decay_rate(a.A[(int64_t)dc * a.N + n]);
             if (a.state_in) v.y = a.state_in[((int64_t)b * a.D + dc) * a.N + n];
         }
         sAh[i] = v;

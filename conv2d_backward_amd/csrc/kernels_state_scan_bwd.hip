@@ -177,7 +177,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void scan_backward(ScanBwd<E> a) {
         float A2 = 0.f, q = 0.f;
         if (n < a.N && c < Dg) {
             const int64_t at = (int64_t)(g * Dg + c) * a.N + n;
-            A2 = a.A[at] * kLog2e;
+            A2 = decay_rate(a.A[at]);
             if (a.gstate) q = a.gstate[(int64_t)b * a.D * a.N + at];
             // Through the segments behind this one.
 #pragma unroll 4
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(kTailThreads) void scan_tail(ScanBwd<E> a, int tile
     const int len = length_of(a.lengths, b, a.L);
     for (int i = tid; i < NP * kTailCH; i += kTailThreads) {
         const int n = i / kTailCH, c = tile * kTailCH + i % kTailCH;
-        sA[i] = n < a.N && c < Dg ? a.A[(int64_t)(g * Dg + c) * a.N + n] * kLog2e : 0.f;
+        sA[i] = n < a.N && c < Dg ? decay_rate(a.A[(int64_t)(g * Dg + c) * a.N + n]) : 0.f;
         sG[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;

@@ -179,6 +179,13 @@ __device__ __forceinline__ float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.f + exp2_fast(-v * kLog2e));
 }
 
+// A log2(e) of a scan.  -inf becomes the lowest float, whose decay is 0 for any step
+// above 1e-36 too: positions beyond a length have step 0, where exp(0 A) has to be 1.
+__device__ __forceinline__ float decay_rate(float A) {
+    const float v = A * kLog2e;
+    return v < -3.4028234664e38f ? -3.4028234664e38f : v;
+}
+
 // log(1 + e^v) = max(v, 0) + log(1 + e) with e = exp(-|v|) in (0, 1].  The sum
 // w = 1 + e loses c = e - (w - 1) <= 2^-24 of e, exactly known; log(1 + e) is
 // log(w) + c / w to second order in c, and c stands for c / w: they differ by

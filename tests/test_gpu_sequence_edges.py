@@ -4,6 +4,7 @@ values are infinite, zero or tiny, against the float64 oracle.
 Tolerances and their counts are those of test_gpu_sequence.py.  The oracle sees
 each sequence cut to its length, so that nothing beyond one enters a sum.
 """
+import numpy as np
 import pytest
 
 from oracle import sequence as oracle
@@ -204,3 +205,43 @@ def test_scan_gradients_are_zero_beyond_lengths_whatever_the_skip(case):
     g = s.backward(s.forward(want_checkpoints=True)[2])
     for v in (g.dx, g.ddt, g.dz):
         assert bool((beyond(v, s.n) == 0).all())
+
+
+SCAN_FORGETS = [(4, 20, 45, 5, 1), (4, 36, 300, 16, 2), (4, 1024, 1030, 4, 1), (4, 2000, 600, 4, 2)]
+
+
+@pytest.mark.parametrize("case", SCAN_FORGETS, ids=str)
+def test_scan_of_infinite_rates(case):
+    """A = -inf forgets the state at each position (exp(-inf) = 0); beyond a length the state still passes."""
+    B, D, L, N, G = case
+    s = base.Scan((*case, None, "dense"), "f32")
+    s.n = ints(L, 0, 7, 30)
+    for v in (s.x, s.dt, s.z, s.gout, s.B, s.C):
+        poison(v, s.n)
+    s.A[2, 0] = s.A[5, N - 1] = -float("inf")
+    y, h, marks = s.forward(want_state=True, want_checkpoints=True)
+    some = [0, 2, 5, D - 1]                          # (rows of channels do not meet: a few do for the oracle)
+    of = torch.tensor(some, device="cuda") // (D // G)
+    x, dt, z = (v[:, some] for v in (s.x, s.dt, s.z))
+    Bm, Cm = s.B[:, of], s.C[:, of]
+    args = num(x, dt, s.A[some], Bm, Cm, s.skip[some], z, s.bias[some])
+    ry, rh, S, H, rmarks = oracle.state_scan(*args, True, *num(s.state[:, some]), s.n, every=gi.SCAN_CHECKPOINT)
+    check(y[:, some], ry, S, 32 * L + 64, "y")
+    check(h[:, some], rh, H, 32 * L + 64, "state")
+    check(marks[:, some], rmarks, np.abs(rmarks) + np.abs(H)[:, :, None], 32 * L + 64, "checkpoints")
+
+
+@pytest.mark.parametrize("case", SCAN_FORGETS, ids=str)
+def test_scan_gradients_of_infinite_rates(case):
+    """The gradients at A = -inf are those at a rate whose decay is 0 in float32."""
+    B, D, L, N, G = case
+    s = base.Scan((*case, None, "dense"), "f32")
+    s.n = ints(L, 0, 7, 30)
+    for v in (s.x, s.dt, s.z, s.gout, s.B, s.C):
+        poison(v, s.n)
+    got = {}
+    for rate in (-1e30, -float("inf")):
+        s.A[2, 0] = s.A[5, N - 1] = rate
+        got[rate] = s.backward(s.forward(want_checkpoints=True)[2], want_dstate=True)
+    for name, p, q in zip(got[-1e30]._fields, *got.values()):
+        assert bool(torch.isfinite(p).all()) and torch.equal(p, q), name
