@@ -3,7 +3,8 @@
 Usage: ``python -m conv2d_backward_amd.build`` (or ``build()`` from Python).
 Each source compiles to an object under ``_build/`` at the repository root,
 in parallel; the objects link into ``conv2d_backward_amd/libconv2d_gi.so``.
-Beside it ``_sequence.so`` is built, the extension module behind sequence.py.
+Beside it ``_sequence.so`` is built, the extension module behind sequence.py, which
+needs torch and g++; without torch only the library is built.
 """
 from __future__ import annotations
 
@@ -54,11 +55,15 @@ BINDING = "seq_binding.cpp"
 BINDING_PATH = os.path.join(PKG, "_sequence.so")
 
 
-def _build_binding() -> str:
+def _build_binding() -> str | None:
     import sysconfig
 
-    import torch
-    from torch.utils import cpp_extension
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        sys.stderr.write("%s is not built: no torch (%s)\n" % (os.path.basename(BINDING_PATH), e))
+        return None
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING_PATH + ".tmp%d" % os.getpid()
@@ -92,18 +97,20 @@ def _compile(src: str) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source for gfx950 and link the shared library (always rebuilds)."""
+    """Compile every source for gfx950, link the shared library and build its torch binding
+    (always rebuilds)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        # The library is whole before what becomes of its binding counts.
+        tmp = LIB_PATH + ".tmp%d" % os.getpid()
+        cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+        os.replace(tmp, LIB_PATH)
         binding.result()
-    tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
-    os.replace(tmp, LIB_PATH)
     if verbose:
         print("built", LIB_PATH)
     return LIB_PATH
