@@ -27,19 +27,6 @@ __all__ = [
     "state_scan_step", "block_norm", "block_norm_backward", "ScanGrads", "NormGrads", "SCAN_CHECKPOINT",
 ]
 
-_SEQUENCE = __all__[__all__.index("causal_conv"):]
-
-
-def __getattr__(name):
-    # The sequence operators' module imports torch, which the rest of the binding
-    # does at a call: so it is loaded when one of them is first named.
-    if name in _SEQUENCE:
-        from . import sequence
-
-        globals().update({n: getattr(sequence, n) for n in _SEQUENCE})
-        return globals()[name]
-    raise AttributeError("module %r has no attribute %r" % (__name__, name))
-
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "libconv2d_gi.so")
 
@@ -556,3 +543,9 @@ def forward(x, weight, *, stride: int, padding, out=None, stream=None):
                                   ctypes.c_void_p(s.cuda_stream))
     _check(code)
     return out
+
+
+# (It needs the names above, and loads neither torch nor its extension module before a call.)
+from .sequence import (SCAN_CHECKPOINT, NormGrads, ScanGrads, block_norm,  # noqa: E402
+                       block_norm_backward, causal_conv, causal_conv_backward, causal_conv_step,
+                       state_scan, state_scan_backward, state_scan_step)

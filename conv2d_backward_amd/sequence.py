@@ -12,15 +12,15 @@ Like the convolutions these are plain functions, not autograd nodes: each
 gradient is a call of its own.  Calls are asynchronous on ``stream`` (a torch
 stream; default: the current one), which the caller orders after whatever
 produced the inputs.  Bad arguments raise ValueError or ``Conv2dGiError``
-before anything is launched.
+before anything is launched.  torch and the extension module are loaded at the
+first call, which raises ``LibraryNotBuilt`` where the module is missing.
 """
 from __future__ import annotations
 
 import collections
 import ctypes
+import importlib
 import os
-
-import torch
 
 from . import LibraryNotBuilt, _check, load_library
 
@@ -34,9 +34,17 @@ SCAN_CHECKPOINT = 128
 ScanGrads = collections.namedtuple("ScanGrads", "dx ddt dA dB dC dD dz ddt_bias dstate")
 NormGrads = collections.namedtuple("NormGrads", "dy dresidual dgate dscale dweight_post dweight_pre")
 
-if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_sequence.so")):
-    raise LibraryNotBuilt("_sequence.so is missing: build it with `python -m conv2d_backward_amd.build`")
-from . import _sequence  # noqa: E402
+torch = _sequence = None  # of the first call
+_binding_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_sequence.so")
+
+
+def _load():
+    global torch, _sequence
+    if not os.path.exists(_binding_path):
+        raise LibraryNotBuilt("%s is missing: build it with `python -m conv2d_backward_amd.build`" % _binding_path)
+    torch = importlib.import_module("torch")  # (the extension module links with it)
+    _sequence = importlib.import_module("._sequence", __package__)
+
 
 # Operand kinds and uses of seq_binding.cpp.
 _ACT, _ACT32, _STATES, _DENSE, _DENSE32, _INDEX = range(6)
@@ -106,6 +114,8 @@ _made = {}
 
 
 def _make(name):
+    if _sequence is None:
+        _load()
     header, others, workspace, operands = _ENTRIES[name]
     lib = load_library()
 
@@ -153,15 +163,6 @@ def _call(name, lead, stream, sizes, operands):
     return out
 
 
-def _shape(t, name, dims):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError("%s must be a tensor" % name)
-    shape = t.shape
-    if len(shape) != dims:
-        raise ValueError("%s must have %d dimensions, has %d" % (name, dims, len(shape)))
-    return shape
-
-
 def causal_conv(x, weight, bias=None, *, silu=True, state=None, lengths=None, want_state=False,
                 out=None, stream=None):
     """Depthwise causal convolution of K taps with bias and SiLU: (y, new_state).
@@ -199,7 +200,10 @@ def causal_conv_step(x, state, weight, bias=None, *, silu=True, slots=None, out=
 
 def _marks(x):
     """Checkpoints of a row."""
-    return -(-_shape(x, "x", 3)[2] // SCAN_CHECKPOINT)
+    shape = getattr(x, "shape", ())
+    if len(shape) != 3:
+        raise ValueError("x must be a tensor of 3 dimensions, has %d" % len(shape))
+    return -(-shape[2] // SCAN_CHECKPOINT)
 
 
 def state_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, softplus=True, state=None,
