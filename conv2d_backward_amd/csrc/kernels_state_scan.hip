@@ -435,6 +435,14 @@ hipError_t step(const state_scan_step_args &a, hipStream_t s) {
 
 }  // namespace
 
+int64_t scan_forward_items(const state_scan_args &a) {
+    // A work-group has two channels at least and eight waves at most.
+    const int64_t most = ((int64_t)a.D + a.G) / 2 * 512;
+    if (most >> 32 == 0) return most;
+    const Deal &v = kDeals[pick_deal(a)];
+    const int channels = v.W / v.shares * 64 / v.lanes;
+    return (int64_t)a.G * ((a.D / a.G + channels - 1) / channels) * 64 * v.W;
+}
 hipError_t launch_scan_forward(const state_scan_args &a, hipStream_t s) {
     return a.dtype == SEQ_F32 ? forward_any<F32>(a, s)
            : a.dtype == SEQ_BF16 ? forward_any<BF16>(a, s) : forward_any<F16>(a, s);

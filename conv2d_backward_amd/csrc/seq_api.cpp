@@ -19,6 +19,7 @@ constexpr int64_t kMaxPositions = (int64_t)1 << 26;
 constexpr int64_t kMaxBatchPositions = (int64_t)1 << 31;  // of all batch items; counted in 32 bits
 // A norm's work-groups of 1024 own 32 positions, and a grid has less than 2^32 work-items.
 constexpr int64_t kMaxNormTiles = (int64_t)1 << 22;
+constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;  // work-items of a grid along one axis
 
 int check_sizes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
     if (dtype != SEQ_F32 && dtype != SEQ_BF16 && dtype != SEQ_F16) return CONV2D_GI_EINVAL;
@@ -39,13 +40,22 @@ int check_taps(int32_t K) {
     return K > SEQ_MAX_TAPS ? CONV2D_GI_EUNSUPPORTED : CONV2D_GI_OK;
 }
 
-int check_states(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
+int check_states(int64_t D, int64_t N, int64_t G) {
     if (N < 1 || G < 1 || D % G != 0) return CONV2D_GI_EINVAL;
-    if (N > SEQ_MAX_STATES) return CONV2D_GI_EUNSUPPORTED;
+    return N > SEQ_MAX_STATES ? CONV2D_GI_EUNSUPPORTED : CONV2D_GI_OK;
+}
+
+int check_grid(int64_t items) {
+    return items > kMaxItems ? CONV2D_GI_EUNSUPPORTED : CONV2D_GI_OK;
+}
+
+int check_scan_backward(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
+    const int rc = check_states(D, N, G);
     // The join of dB and dC is one grid over 4-position runs of [2, B, G, N, L], 64 to
-    // a work-group of 256, and a grid has less than 2^32 work-items.
-    if (B * G * N > ((int64_t)1 << 30) / (L + 256)) return CONV2D_GI_EUNSUPPORTED;
-    return CONV2D_GI_OK;
+    // a work-group of 256.
+    if (rc == CONV2D_GI_OK && B * G * N > ((int64_t)1 << 30) / (L + 256))
+        return CONV2D_GI_EUNSUPPORTED;
+    return rc;
 }
 
 // An output's rows must not share elements: dense positions, channels and batch
@@ -114,7 +124,8 @@ int causal_conv_step(const causal_conv_step_args *a, hipStream_t stream) {
 int state_scan_forward(const state_scan_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, a->L);
-    if (rc == CONV2D_GI_OK) rc = check_states(a->B, a->D, a->L, a->N, a->G);
+    if (rc == CONV2D_GI_OK) rc = check_states(a->D, a->N, a->G);
+    if (rc == CONV2D_GI_OK) rc = check_grid(seq::scan_forward_items(*a));
     if (rc != CONV2D_GI_OK) return rc;
     if (!a->x.data || !a->dt.data || !a->Bm.data || !a->Cm.data || !a->y.data || !a->A)
         return CONV2D_GI_EINVAL;
@@ -124,7 +135,7 @@ int state_scan_forward(const state_scan_args *a, hipStream_t stream) {
 
 int64_t state_scan_workspace(int32_t B, int32_t D, int32_t L, int32_t N, int32_t G) {
     if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK ||
-        check_states(B, D, L, N, G) != CONV2D_GI_OK)
+        check_scan_backward(B, D, L, N, G) != CONV2D_GI_OK)
         return -1;
     return seq::scan_backward_workspace(B, D, L, N, G);
 }
@@ -132,7 +143,7 @@ int64_t state_scan_workspace(int32_t B, int32_t D, int32_t L, int32_t N, int32_t
 int state_scan_backward(const state_scan_backward_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, a->L);
-    if (rc == CONV2D_GI_OK) rc = check_states(a->B, a->D, a->L, a->N, a->G);
+    if (rc == CONV2D_GI_OK) rc = check_scan_backward(a->B, a->D, a->L, a->N, a->G);
     if (rc != CONV2D_GI_OK) return rc;
     if (!a->gout.data || !a->x.data || !a->dt.data || !a->Bm.data || !a->Cm.data || !a->A ||
         !a->checkpoints || !a->dx.data || !a->ddt.data || !a->dBm || !a->dCm || !a->dA)
@@ -150,7 +161,7 @@ int state_scan_backward(const state_scan_backward_args *a, hipStream_t stream) {
 int state_scan_step(const state_scan_step_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, 1);
-    if (rc == CONV2D_GI_OK) rc = check_states(a->B, a->D, 1, a->N, a->G);
+    if (rc == CONV2D_GI_OK) rc = check_states(a->D, a->N, a->G);
     if (rc != CONV2D_GI_OK) return rc;
     if (!a->x.data || !a->dt.data || !a->Bm.data || !a->Cm.data || !a->y.data || !a->A ||
         !a->state)

@@ -14,6 +14,7 @@ hipError_t launch_conv_step(const causal_conv_step_args &a, hipStream_t s);
 int64_t conv_backward_workspace(int B, int D, int L, int K);
 
 hipError_t launch_scan_forward(const state_scan_args &a, hipStream_t s);
+int64_t scan_forward_items(const state_scan_args &a);  // of the grid's x
 hipError_t launch_scan_step(const state_scan_step_args &a, hipStream_t s);
 hipError_t launch_scan_backward(const state_scan_backward_args &a, hipStream_t s);
 int64_t scan_backward_workspace(int B, int D, int L, int N, int G);

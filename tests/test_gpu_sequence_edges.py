@@ -245,3 +245,27 @@ def test_scan_gradients_of_infinite_rates(case):
         got[rate] = s.backward(s.forward(want_checkpoints=True)[2], want_dstate=True)
     for name, p, q in zip(got[-1e30]._fields, *got.values()):
         assert bool(torch.isfinite(p).all()) and torch.equal(p, q), name
+
+
+def test_scan_of_more_states_and_positions_than_gradients_have():
+    """B*G*N*(L+256) beyond 2^30: a prompt of equal rows (batch stride 0) and a large generation step."""
+    B, D, L, N, G = 64, 8, 16640, 128, 8
+    i = Inputs(8, "bf16")
+    x, dt, Bm, Cm = i.normal(1, D, L), i.normal(1, D, L, scale=0.3), i.normal(1, G, N, L), i.normal(1, G, N, L)
+    A, bias = i.params(D, N, low=-4, high=-0.05), i.params(D, low=-5, high=-3)
+    every = [v.expand(B, *v.shape[1:]) for v in (x, dt, Bm, Cm)]
+    y, h, _ = gi.state_scan(*every[:2], A, *every[2:], dt_bias=bias, want_state=True)
+    ry, rh, S, H = oracle.state_scan(*num(x, dt, A, Bm, Cm), None, None, *num(bias), True)
+    check(y[:1], ry, S, 32 * L + 64, "y")
+    check(h[:1], rh, H, 32 * L + 64, "state")
+    assert all(torch.equal(v, v[:1].expand_as(v)) for v in (y, h))
+    B = 4200
+    rows = [v[..., 5].expand(B, *v.shape[1:-1]) for v in (x, dt, Bm, Cm)]
+    state = i.params(1, D, N).repeat(B, 1, 1)
+    before = state[:1].clone()
+    y = gi.state_scan_step(*rows[:2], A, *rows[2:], state, dt_bias=bias)
+    ry, rh, S, H = oracle.state_scan(*num(*[v[..., 5:6] for v in (x, dt)], A, *[v[..., 5:6] for v in (Bm, Cm)]),
+                                     None, None, *num(bias), True, *num(before))
+    check(y[:1], ry[..., 0], S[..., 0], 96 + 8 * N, "y")
+    check(state[:1], rh, H, 96, "state")
+    assert torch.equal(y, y[:1].expand_as(y)) and torch.equal(state, state[:1].expand_as(state))

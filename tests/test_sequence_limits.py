@@ -1,0 +1,23 @@
+"""Host-side tests of the sequence operators' size limits: a call is refused for what its
+own kernels cannot do.  As in test_sequence_boundary.py nothing is launched: a call that
+is within the limits is refused for its output's strides, which are looked at later.
+"""
+import conv2d_backward_amd as gi
+from test_sequence_boundary import call, lib, workspace  # noqa: F401  (lib: a fixture)
+
+APART = {"y.channel": 0}   # EINVAL, after the sizes
+
+
+def test_scan_calls_without_gradients_have_no_limit_of_the_gradients(lib):  # noqa: F811
+    """B*G*N*(L+256) beyond 2^30, which bounds the sums of dB and dC."""
+    assert call("state_scan_step", B=4200, D=64, G=8, N=128, lines=4200, **APART) == gi.EINVAL
+    assert call("state_scan", B=64, D=64, G=8, N=128, L=16640, **APART) == gi.EINVAL
+    assert call("state_scan_backward", B=64, D=64, G=8, N=128, L=1 << 18) == gi.EUNSUPPORTED
+    assert workspace("state_scan_workspace", 64, 64, 1 << 18, 128, 8) == -1
+
+
+def test_scan_forward_is_refused_beyond_its_own_grid(lib):  # noqa: F811
+    """A work-group of 256 or 512 for each group of one channel: 2^32 work-items or more."""
+    most = (1 << 24) - 1
+    assert call("state_scan", B=1, D=most, G=most, N=256, L=1) == gi.EUNSUPPORTED
+    assert call("state_scan", B=1, D=most, G=1, N=256, L=1, **APART) == gi.EINVAL
