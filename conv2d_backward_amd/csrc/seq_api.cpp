@@ -51,9 +51,11 @@ int check_grid(int64_t items) {
 
 int check_scan_backward(int64_t B, int64_t D, int64_t L, int64_t N, int64_t G) {
     const int rc = check_states(D, N, G);
-    // The join of dB and dC is one grid over 4-position runs of [2, B, G, N, L], 64 to
-    // a work-group of 256.
-    if (rc == CONV2D_GI_OK && B * G * N > ((int64_t)1 << 30) / (L + 256))
+    // The join is one grid, the largest: over 4-position runs of dB and dC ([2, B, G, N]
+    // rows padded to whole chunks), 64 to a work-group of 256, and behind them over dA,
+    // dskip and ddt_bias, [D, N + 2].
+    const int64_t left = kMaxItems - 512 - D * (N + 2);
+    if (rc == CONV2D_GI_OK && (left < 0 || B * G * N > left / 2 / (L + 256)))
         return CONV2D_GI_EUNSUPPORTED;
     return rc;
 }

@@ -50,7 +50,7 @@ enum { SEQ_F32 = 0, SEQ_BF16 = 1, SEQ_F16 = 2 };
 
 /* Limits: taps of a causal convolution, states of a scan, channels of a norm.
    Of every entry: B <= 65535, B*D < 2^24, L <= 2^26, B*L < 2^31 (norms: 2^27);
-   of state_scan_backward also B*G*N*(L+256) <= 2^30. */
+   of state_scan_backward also 2*B*G*N*(L+256) + D*(N+2) < 2^32 - 512. */
 enum { SEQ_MAX_TAPS = 8, SEQ_MAX_STATES = 256, SEQ_MAX_NORM_CHANNELS = 65536 };
 
 /* An activation [B, D, L]: element (b, d, t) at data[b*batch + d*channel + t].

@@ -21,3 +21,16 @@ def test_scan_forward_is_refused_beyond_its_own_grid(lib):  # noqa: F811
     most = (1 << 24) - 1
     assert call("state_scan", B=1, D=most, G=most, N=256, L=1) == gi.EUNSUPPORTED
     assert call("state_scan", B=1, D=most, G=1, N=256, L=1, **APART) == gi.EINVAL
+
+
+def test_scan_gradients_are_refused_for_the_whole_of_their_last_grid(lib):  # noqa: F811
+    """The join of dB and dC has D*(N+2) work-items of its parameters behind them: counted
+    too, or the first kernels of a call run and the last one's launch fails."""
+    for sizes in (dict(B=1, D=(1 << 24) - 8, L=1, N=256, G=1),
+                  dict(B=1, D=1 << 23, L=(1 << 22) - 512, N=256, G=1)):
+        assert call("state_scan_backward", **sizes) == gi.EUNSUPPORTED
+        assert workspace("state_scan_workspace", *(sizes[k] for k in "BDLNG")) == -1
+    for sizes in (dict(B=1, D=(1 << 24) - 8, L=1, N=128, G=1),
+                  dict(B=1, D=1 << 22, L=(1 << 22) - 512, N=256, G=1)):
+        assert call("state_scan_backward", **{"dx.channel": 0}, **sizes) == gi.EINVAL
+        assert workspace("state_scan_workspace", *(sizes[k] for k in "BDLNG")) > 0
