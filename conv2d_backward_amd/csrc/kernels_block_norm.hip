@@ -514,6 +514,27 @@ __global__ __launch_bounds__(256) void norm_join(const float *part, float *dscal
 
 int64_t tiles_of(int64_t L, int CV) { return (L + kV * CV - 1) / (kV * CV); }
 
+// How the columns are dealt to work-groups, and how many rows of them a thread keeps
+// (0: none).  A tile stays in registers where its channels fit: 32 columns of up to 1024, 16
+// of 2048 or 8 of 4096.  Pieces of rows should be long and tiles enough for the
+// chip: 32 columns where those make 128 tiles, 8 where 16 make fewer than 96 (or
+// none fit, up to 512 tiles of 8).  Else it is read again, with 32 columns where
+// those make 256 tiles.  Measured (us, 32 / 16 / 8 columns kept, 32 / 16 again):
+// [8, 1024, 2001] bf16 50 / 69 / 75, again 74 / 95; [3, 1000, 1025] f32 24 / 21 / 24;
+// [1, 600, 1500] bf16 - / 12 / 10; [3, 1800, 2805] f16 - / 77 / 96, again 110;
+// [64, 1500, 16] bf16 - / 13 / 10; [1, 4000, 1000] bf16 - / - / 31, again 52;
+// [2, 4096, 2048] bf16 - / - / 67, again 59.
+struct Deal {
+    int CV, kept;
+};
+Deal pick_deal(int64_t B, int64_t D, int64_t L) {
+    const int64_t t32 = B * tiles_of(L, 4), t16 = B * tiles_of(L, 2), t8 = B * tiles_of(L, 1);
+    if (D <= 1024 && t32 >= 128) return {4, 4};
+    if (D <= 2048 && t16 >= 96) return {2, D <= 1024 ? 2 : 4};
+    if (D <= 4096 && t8 < 512) return {1, D <= 1024 ? 1 : D <= 2048 ? 2 : 4};
+    return {t32 >= 256 ? 4 : 2, 0};
+}
+
 template <class E>
 hipError_t forward(const block_norm_args &a, hipStream_t s) {
     NormFwd<E> k{view<E>(a.y), view<E>(a.gate), view<E>(a.u), view<F32>(a.r), view<F32>(a.r_out),
@@ -530,31 +551,17 @@ hipError_t forward(const block_norm_args &a, hipStream_t s) {
         kernel<<<dim3((unsigned)a.B), kTokenThreads, 0, s>>>(k);
         return hipGetLastError();
     }
-    // A tile stays in registers where its channels fit: 32 columns of up to 1024, 16
-    // of 2048 or 8 of 4096.  Pieces of rows should be long and tiles enough for the
-    // chip: 32 columns where those make 128 tiles, 8 where 16 make fewer than 96 (or
-    // none fit, up to 512 tiles of 8).  Else it is read again, with 32 columns where
-    // those make 256 tiles.  Measured (us, 32 / 16 / 8 columns kept, 32 / 16 again):
-    // [8, 1024, 2001] bf16 50 / 69 / 75, again 74 / 95; [3, 1000, 1025] f32 24 / 21 / 24;
-    // [1, 600, 1500] bf16 - / 12 / 10; [3, 1800, 2805] f16 - / 77 / 96, again 110;
-    // [64, 1500, 16] bf16 - / 13 / 10; [1, 4000, 1000] bf16 - / - / 31, again 52;
-    // [2, 4096, 2048] bf16 - / - / 67, again 59.
-    const int64_t t32 = a.B * tiles_of(a.L, 4), t16 = a.B * tiles_of(a.L, 2),
-                  t8 = a.B * tiles_of(a.L, 1);
-    int CV;
+    const Deal deal = pick_deal(a.B, a.D, a.L);
     void (*kernel)(NormFwd<E>);
-    if (a.D <= 1024 && t32 >= 128)
-        CV = 4, kernel = norm_forward<E, 1024, 4, 4>;
-    else if (a.D <= 2048 && t16 >= 96)
-        CV = 2, kernel = a.D <= 1024 ? norm_forward<E, 1024, 2, 2> : norm_forward<E, 1024, 2, 4>;
-    else if (a.D <= 4096 && t8 < 512)
-        CV = 1, kernel = a.D <= 1024 ? norm_forward<E, 1024, 1, 1>
-                         : a.D <= 2048 ? norm_forward<E, 1024, 1, 2> : norm_forward<E, 1024, 1, 4>;
-    else if (t32 >= 256)
-        CV = 4, kernel = norm_forward<E, 1024, 4, 0>;
+    if (deal.CV == 4)
+        kernel = deal.kept ? norm_forward<E, 1024, 4, 4> : norm_forward<E, 1024, 4, 0>;
+    else if (deal.CV == 2)
+        kernel = deal.kept == 2   ? norm_forward<E, 1024, 2, 2>
+                 : deal.kept == 4 ? norm_forward<E, 1024, 2, 4> : norm_forward<E, 1024, 2, 0>;
     else
-        CV = 2, kernel = norm_forward<E, 1024, 2, 0>;
-    k.tiles = (int)tiles_of(a.L, CV);
+        kernel = deal.kept == 1   ? norm_forward<E, 1024, 1, 1>
+                 : deal.kept == 2 ? norm_forward<E, 1024, 1, 2> : norm_forward<E, 1024, 1, 4>;
+    k.tiles = (int)tiles_of(a.L, deal.CV);
     kernel<<<dim3((unsigned)(a.B * k.tiles)), 1024, 0, s>>>(k);
     return hipGetLastError();
 }
@@ -588,6 +595,8 @@ hipError_t launch_norm_backward(const block_norm_backward_args &a, hipStream_t s
     return a.dtype == SEQ_F32 ? backward<F32>(a, s)
            : a.dtype == SEQ_BF16 ? backward<BF16>(a, s) : backward<F16>(a, s);
 }
+
+int norm_columns(int64_t B, int64_t D, int64_t L) { return L == 1 ? 1 : kV * pick_deal(B, D, L).CV; }
 
 int64_t norm_workspace(int B, int D, int L, int backward) {
     return backward ? bwd_shape(B, D, L).floats * 4 : 0;

@@ -4,6 +4,7 @@
 // Entry points and their contract are declared in include/sequence_ops.h.
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "api_internal.h"
@@ -17,7 +18,7 @@ constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
 constexpr int64_t kMaxPositions = (int64_t)1 << 26;
 constexpr int64_t kMaxBatchPositions = (int64_t)1 << 31;  // of all batch items; counted in 32 bits
-// A norm's work-groups of 1024 own 32 positions, and a grid has less than 2^32 work-items.
+// A norm's work-groups have 1024 work-items at most, and a grid less than 2^32.
 constexpr int64_t kMaxNormTiles = (int64_t)1 << 22;
 constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;  // work-items of a grid along one axis
 
@@ -29,9 +30,10 @@ int check_sizes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
     return CONV2D_GI_OK;
 }
 
-int check_norm(int64_t B, int64_t D, int64_t L, float eps) {
-    if (D > SEQ_MAX_NORM_CHANNELS || B * ((L + 31) / 32) >= kMaxNormTiles)
-        return CONV2D_GI_EUNSUPPORTED;
+int check_norm(int64_t B, int64_t D, int64_t L, bool backward, float eps) {
+    if (D > SEQ_MAX_NORM_CHANNELS) return CONV2D_GI_EUNSUPPORTED;
+    const int64_t columns = backward ? 32 : std::min<int64_t>(32, seq::norm_columns(B, D, L));
+    if (B * ((L + columns - 1) / columns) >= kMaxNormTiles) return CONV2D_GI_EUNSUPPORTED;
     return eps >= 0.f ? CONV2D_GI_OK : CONV2D_GI_EINVAL;
 }
 
@@ -176,7 +178,7 @@ int state_scan_step(const state_scan_step_args *a, hipStream_t stream) {
 int block_norm_forward(const block_norm_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, a->L);
-    if (rc == CONV2D_GI_OK) rc = check_norm(a->B, a->D, a->L, a->eps);
+    if (rc == CONV2D_GI_OK) rc = check_norm(a->B, a->D, a->L, false, a->eps);
     if (rc != CONV2D_GI_OK) return rc;
     if (!a->y.data || !a->r.data || !a->r_out.data) return CONV2D_GI_EINVAL;
     if (!a->w_pre != !a->u.data) return CONV2D_GI_EINVAL;
@@ -190,7 +192,7 @@ int block_norm_forward(const block_norm_args *a, hipStream_t stream) {
 }
 
 int64_t block_norm_workspace(int32_t B, int32_t D, int32_t L, int32_t backward) {
-    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK || check_norm(B, D, L, 0.f) != CONV2D_GI_OK)
+    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK || check_norm(B, D, L, backward != 0, 0.f) != CONV2D_GI_OK)
         return -1;
     return seq::norm_workspace(B, D, L, backward != 0);
 }
@@ -198,7 +200,7 @@ int64_t block_norm_workspace(int32_t B, int32_t D, int32_t L, int32_t backward) 
 int block_norm_backward(const block_norm_backward_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, a->L);
-    if (rc == CONV2D_GI_OK) rc = check_norm(a->B, a->D, a->L, a->eps);
+    if (rc == CONV2D_GI_OK) rc = check_norm(a->B, a->D, a->L, true, a->eps);
     if (rc != CONV2D_GI_OK) return rc;
     if (!a->y.data || !a->r_out.data || !a->dy.data || !a->dr.data) return CONV2D_GI_EINVAL;
     if ((a->gu.data && !a->w_pre) || !a->gate.data != !a->dgate.data) return CONV2D_GI_EINVAL;

@@ -21,6 +21,7 @@ int64_t scan_backward_workspace(int B, int D, int L, int N, int G);
 
 hipError_t launch_norm_forward(const block_norm_args &a, hipStream_t s);
 hipError_t launch_norm_backward(const block_norm_backward_args &a, hipStream_t s);
+int norm_columns(int64_t B, int64_t D, int64_t L);  // positions of a forward work-group
 int64_t norm_workspace(int B, int D, int L, int backward);
 
 }  // namespace seq

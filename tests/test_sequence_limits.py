@@ -34,3 +34,15 @@ def test_scan_gradients_are_refused_for_the_whole_of_their_last_grid(lib):  # no
                   dict(B=1, D=1 << 22, L=(1 << 22) - 512, N=256, G=1)):
         assert call("state_scan_backward", **{"dx.channel": 0}, **sizes) == gi.EINVAL
         assert workspace("state_scan_workspace", *(sizes[k] for k in "BDLNG")) > 0
+
+
+def test_norm_is_refused_by_the_columns_its_work_groups_have(lib):  # noqa: F811
+    """1024 work-items for 32 columns, for 16 of 1025 .. 2048 channels: 2^32 or more are refused."""
+    for L, D, code in ((1 << 23, 1024, gi.EINVAL), (1 << 23, 1500, gi.EUNSUPPORTED), ((1 << 23) - 8, 1500, gi.EUNSUPPORTED),
+                       ((1 << 23) - 16, 1500, gi.EINVAL), (1 << 23, 3000, gi.EINVAL), (1 << 24, 3000, gi.EUNSUPPORTED)):
+        sizes = dict(B=8, D=D, L=L)
+        if code == gi.EINVAL:
+            sizes.update({"r_out.channel": 0})
+        assert call("block_norm", **sizes) == code, (L, D)
+    assert call("block_norm_backward", B=8, D=1500, L=1 << 23, **{"dr.channel": 0}) == gi.EINVAL
+    assert call("block_norm", B=65535, D=64, L=1, **{"r_out.channel": 0, "r_out.batch": 0}) == gi.EINVAL
