@@ -10,10 +10,11 @@ points mirror these names.
 
 Like the convolutions these are plain functions, not autograd nodes: each
 gradient is a call of its own.  Calls are asynchronous on ``stream`` (a torch
-stream; default: the current one), which the caller orders after whatever
-produced the inputs.  Bad arguments raise ValueError or ``Conv2dGiError``
-before anything is launched.  torch and the extension module are loaded at the
-first call, which raises ``LibraryNotBuilt`` where the module is missing.
+stream of the tensors' device; default: the current one), which the caller
+orders after whatever produced the inputs.  Bad arguments raise ValueError or
+``Conv2dGiError`` before anything is launched.  torch and the extension module
+are loaded at the first call, which raises ``LibraryNotBuilt`` where the module
+is missing.
 """
 from __future__ import annotations
 
@@ -147,6 +148,8 @@ def _call(name, lead, stream, sizes, operands):
             with torch.cuda.device(index):
                 out = _sequence.call(entry, torch._C._cuda_getCurrentRawStream(index), sizes, operands)
     else:
+        if stream.device_index != index:
+            raise ValueError("stream is on cuda:%d, the tensors are on cuda:%d" % (stream.device_index, index))
         with torch.cuda.stream(stream):  # outputs and scratch are that stream's memory
             out = _sequence.call(entry, stream.cuda_stream, sizes, operands)
         current = torch.cuda.current_stream(index)

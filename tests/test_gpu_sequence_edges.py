@@ -269,3 +269,19 @@ def test_scan_of_more_states_and_positions_than_gradients_have():
     check(y[:1], ry[..., 0], S[..., 0], 96 + 8 * N, "y")
     check(state[:1], rh, H, 96, "state")
     assert torch.equal(y, y[:1].expand_as(y)) and torch.equal(state, state[:1].expand_as(state))
+
+
+# ---- streams -------------------------------------------------------------------------------------
+
+
+def test_stream_of_another_device_is_refused():
+    """Its kernels would run there, on memory that is here."""
+    class Elsewhere:
+        device_index, cuda_stream = 1, 0
+
+    i = Inputs(1, "bf16")
+    x = i.normal(2, 6, 10)
+    for f in (lambda: gi.causal_conv(x, i.params(6, 4), stream=Elsewhere()),
+              lambda: gi.block_norm(x, x.float(), stream=Elsewhere())):
+        with pytest.raises(ValueError, match="cuda:1"):
+            f()
