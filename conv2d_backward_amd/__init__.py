@@ -24,7 +24,7 @@ __all__ = [
     "OK", "EINVAL", "EUNSUPPORTED", "EHIP", "VARIANT_AUTO", "VARIANT_GENERIC", "VARIANT_HALO", "VARIANT_STEM",
     "VARIANT_COL2IM",
     "causal_conv", "causal_conv_backward", "causal_conv_step", "state_scan", "state_scan_backward",
-    "state_scan_step", "block_norm", "block_norm_backward", "ScanGrads", "NormGrads", "SCAN_CHECKPOINT",
+    "state_scan_step", "state_scan_plan", "block_norm", "block_norm_backward", "ScanGrads", "NormGrads", "SCAN_CHECKPOINT",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -101,6 +101,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.conv2d_grad_bias.restype = ctypes.c_int
     lib.conv2d_gw_plan.argtypes = [PP, ctypes.c_char_p, ctypes.c_size_t]
     lib.conv2d_gw_plan.restype = ctypes.c_int
+    lib.state_scan_plan.argtypes = [ctypes.c_int32] * 6 + [ctypes.c_char_p, ctypes.c_size_t]
+    lib.state_scan_plan.restype = ctypes.c_int
     lib.conv2d_gi_set_halo_tile.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]
     lib.conv2d_gi_set_halo_tile.restype = ctypes.c_int
     lib.conv2d_gi_set_halo_split.argtypes = [ctypes.c_int]
@@ -140,7 +142,7 @@ def exported_names():
             "conv2d_gi_release_workspaces", "conv2d_gi_version", "conv2d_gi_mfma_peak_probe",
             "causal_conv_forward", "causal_conv_backward", "causal_conv_step",
             "causal_conv_workspace", "state_scan_forward", "state_scan_backward",
-            "state_scan_step", "state_scan_workspace", "block_norm_forward",
+            "state_scan_step", "state_scan_workspace", "state_scan_plan", "block_norm_forward",
             "block_norm_backward", "block_norm_workspace"]
 
 
@@ -548,4 +550,4 @@ def forward(x, weight, *, stride: int, padding, out=None, stream=None):
 # (It needs the names above, and loads neither torch nor its extension module before a call.)
 from .sequence import (SCAN_CHECKPOINT, NormGrads, ScanGrads, block_norm,  # noqa: E402
                        block_norm_backward, causal_conv, causal_conv_backward, causal_conv_step,
-                       state_scan, state_scan_backward, state_scan_step)
+                       state_scan, state_scan_backward, state_scan_plan, state_scan_step)

@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdio>
 
 #include "seq_common.h"
 #include "seq_kernels.h"
@@ -442,6 +443,11 @@ int64_t scan_forward_items(const state_scan_args &a) {
     const Deal &v = kDeals[pick_deal(a)];
     const int channels = v.W / v.shares * 64 / v.lanes;
     return (int64_t)a.G * ((a.D / a.G + channels - 1) / channels) * 64 * v.W;
+}
+void scan_forward_plan(const state_scan_args &a, char *buf, size_t len) {
+    const Deal &v = kDeals[pick_deal(a)];
+    std::snprintf(buf, len, "waves=%d lanes=%d positions=%d shares=%d staged=%d", v.W, v.lanes, v.T,
+                  v.shares, staged_floats(v.lanes, v.T) / (v.lanes * v.T));
 }
 hipError_t launch_scan_forward(const state_scan_args &a, hipStream_t s) {
     return a.dtype == SEQ_F32 ? forward_any<F32>(a, s)

@@ -21,6 +21,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdio>
 
 #include "seq_common.h"
 #include "seq_kernels.h"
@@ -594,6 +595,12 @@ hipError_t backward(const state_scan_backward_args &a, hipStream_t s) {
 hipError_t launch_scan_backward(const state_scan_backward_args &a, hipStream_t s) {
     return a.dtype == SEQ_F32 ? backward<F32>(a, s)
            : a.dtype == SEQ_BF16 ? backward<BF16>(a, s) : backward<F16>(a, s);
+}
+
+void scan_backward_plan(int B, int D, int L, int N, int G, char *buf, size_t len) {
+    const Plan p = make_plan(B, D, L, N, G);
+    std::snprintf(buf, len, "waves=%d positions=%d segments=%d joined=%d", p.W, p.T, p.segments,
+                  p.joined);
 }
 
 int64_t scan_backward_workspace(int B, int D, int L, int N, int G) {

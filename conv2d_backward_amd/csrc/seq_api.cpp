@@ -162,6 +162,23 @@ int state_scan_backward(const state_scan_backward_args *a, hipStream_t stream) {
     return status(seq::launch_scan_backward(*a, stream));
 }
 
+int state_scan_plan(int32_t B, int32_t D, int32_t L, int32_t N, int32_t G, int32_t backward,
+                    char *buf, size_t len) {
+    if (!buf || len == 0) return CONV2D_GI_EINVAL;
+    int rc = check_sizes(SEQ_F32, B, D, L);
+    if (rc == CONV2D_GI_OK)
+        rc = backward ? check_scan_backward(B, D, L, N, G) : check_states(D, N, G);
+    if (rc != CONV2D_GI_OK) return rc;
+    state_scan_args a = {};
+    a.B = B, a.D = D, a.L = L, a.N = N, a.G = G;
+    if (!backward && (rc = check_grid(seq::scan_forward_items(a))) != CONV2D_GI_OK) return rc;
+    if (backward)
+        seq::scan_backward_plan(B, D, L, N, G, buf, len);
+    else
+        seq::scan_forward_plan(a, buf, len);
+    return CONV2D_GI_OK;
+}
+
 int state_scan_step(const state_scan_step_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
     int rc = check_sizes(a->dtype, a->B, a->D, 1);

@@ -18,6 +18,9 @@ int64_t scan_forward_items(const state_scan_args &a);  // of the grid's x
 hipError_t launch_scan_step(const state_scan_step_args &a, hipStream_t s);
 hipError_t launch_scan_backward(const state_scan_backward_args &a, hipStream_t s);
 int64_t scan_backward_workspace(int B, int D, int L, int N, int G);
+// How the work is dealt, as text.
+void scan_forward_plan(const state_scan_args &a, char *buf, size_t len);
+void scan_backward_plan(int B, int D, int L, int N, int G, char *buf, size_t len);
 
 hipError_t launch_norm_forward(const block_norm_args &a, hipStream_t s);
 hipError_t launch_norm_backward(const block_norm_backward_args &a, hipStream_t s);

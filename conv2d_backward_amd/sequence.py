@@ -26,7 +26,7 @@ import os
 from . import LibraryNotBuilt, _check, load_library
 
 __all__ = ["causal_conv", "causal_conv_backward", "causal_conv_step", "state_scan",
-           "state_scan_backward", "state_scan_step", "block_norm", "block_norm_backward",
+           "state_scan_backward", "state_scan_step", "state_scan_plan", "block_norm", "block_norm_backward",
            "ScanGrads", "NormGrads", "SCAN_CHECKPOINT"]
 
 #: Positions between two checkpoints of ``state_scan`` (SEQ_SCAN_CHECKPOINT).
@@ -247,6 +247,14 @@ def state_scan_backward(grad_out, x, dt, A, B, C, checkpoints, D=None, z=None, d
     if B.dim() == 3:
         dB, dC = dB.squeeze(1), dC.squeeze(1)
     return ScanGrads(dx, ddt, dA, dB, dC, dD, dz, dbias, dstate)
+
+
+def state_scan_plan(B, D, L, N, G=1, backward=False):
+    """Host-only: how ``state_scan`` or its backward deals the work of these sizes, as
+    text (include/sequence_ops.h)."""
+    buf = ctypes.create_string_buffer(256)
+    _check(load_library().state_scan_plan(B, D, L, N, G, int(backward), buf, len(buf)))
+    return buf.value.decode()
 
 
 def state_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, softplus=True,

@@ -172,6 +172,17 @@ CONV2D_GI_API int state_scan_backward(const state_scan_backward_args *a, hipStre
 CONV2D_GI_API int64_t state_scan_workspace(int32_t B, int32_t D, int32_t L, int32_t N, int32_t G);
 
 /*
+ * Host-only: how the work of a state_scan_forward (backward = 0) or _backward
+ * call of these sizes is dealt, as text written into buf (NUL-terminated,
+ * truncated to len): waves of a work-group, positions of a lane and, forward,
+ * lanes of a row, waves that share a row's states and states staged at once;
+ * backward, segments of a row and states whose sums over channels are joined at
+ * once.  Returns a status code.
+ */
+CONV2D_GI_API int state_scan_plan(int32_t B, int32_t D, int32_t L, int32_t N, int32_t G,
+                                  int32_t backward, char *buf, size_t len);
+
+/*
  * One position of state_scan for every row: x, dt, z, out [B, D], Bm and Cm
  * [B, G, N] (seq_tensor.channel: the stride between consecutive states), state
  * [lines, D, N] dense fp32, updated in place.
