@@ -198,19 +198,13 @@ __device__ __forceinline__ float softplus(float v) {
     return __builtin_fmaxf(v, 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(w), kLn2, c);
 }
 
-// Lane moves inside rows of 16 lanes (DPP): lanes without a source get `old`.
-template <int CTRL>
-__device__ __forceinline__ float dpp(float old, float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
-        __builtin_bit_cast(int, old), __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
-}
-// The same with 0 in lanes without a source (folds into the consuming instruction).
+// Lane moves (DPP), with 0 in lanes without a source (folds into the consuming instruction).
 template <int CTRL>
 __device__ __forceinline__ float dpp0(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
         0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-constexpr int kRowShl = 0x100, kRowShr = 0x110, kRowRor = 0x120;  // + distance 1..15
+constexpr int kRowRor = 0x120;  // + distance 1..15, inside rows of 16 lanes
 constexpr int kWaveShl = 0x130, kWaveShr = 0x138, kWaveRor = 0x13c;  // by a lane of the wave
 
 // Maps h -> P h + Q compose along the lanes of a row of LANES (16 or 64): with Q
