@@ -285,3 +285,31 @@ def test_stream_of_another_device_is_refused():
               lambda: gi.block_norm(x, x.float(), stream=Elsewhere())):
         with pytest.raises(ValueError, match="cuda:1"):
             f()
+
+
+@pytest.mark.parametrize("case,plans", [
+    ((7, 192, 1030, 33, 64), ("waves=8 lanes=64 positions=8", "waves=8 positions=8")),
+    ((4, 12, 1030, 18, 4), ("waves=8 lanes=64 positions=8", "waves=4 positions=8")),
+    ((4, 560, 500, 24, 16), ("waves=", "waves=8 positions=16"))], ids=str)
+def test_graph_replays_of_large_work_groups(case, plans):
+    """Work-groups with more than 64 KB of LDS, captured: each replay equals the eager pass."""
+    assert all(gi.state_scan_plan(*case, backward=k).startswith(p) for k, p in enumerate(plans))
+    s = base.Scan((*case, "ragged", "dense"), "bf16")
+
+    def both():
+        y, h, marks = s.forward(want_state=True, want_checkpoints=True)
+        return [y, h, marks, *s.backward(marks, want_dstate=True)]
+
+    want = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = both()
+    for _ in range(3):
+        for v in got:
+            v.fill_(7)
+        graph.replay()
+        again = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) and torch.equal(p, r) for p, q, r in zip(got, want, again))
