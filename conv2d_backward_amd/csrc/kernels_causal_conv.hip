@@ -5,8 +5,8 @@
 // read and one write, so memory bounds all three kernels.  A thread owns V = 8
 // consecutive positions of one row (one 16-byte access for 16-bit types) and
 // takes the K-1 positions before them from its neighbour's registers.
-// [4, 4096, 2048] bf16, 4 taps: forward 34 us (134 MB, 3.9 TB/s), backward 44.5 us
-// (201 MB, 4.5 TB/s); one position of [8, 2048] 2.5 us, the latency of its loads.
+// [4, 4096, 2048] bf16, 4 taps: forward 33 us (134 MB, 4.0 TB/s), backward 43 us
+// (201 MB, 4.7 TB/s); one position of [8, 2048] 2.4 us, the latency of its loads.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

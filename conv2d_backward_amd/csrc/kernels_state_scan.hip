@@ -8,11 +8,13 @@
 // log2(lanes) steps, and each lane runs its chain again from the state it then
 // knows, adding C_t h_t to its outputs.  Every exponential is taken once.
 //
-// What bounds it: for each (channel, state, position) one v_exp_f32 (8 cycles of
-// its SIMD for 64 lanes) and five full-rate instructions (4 cycles); the bytes (x,
-// dt, z, y) are 1/N of that many elements.  [1, 4096, 8192] bf16, N = 16: 178 us,
-// the vector ALUs busy for 89% of it; the instructions named would take 103 us, and
-// the lane scan, the steps and gates and the staging of B and C add 3.8 to their 6.
+// What bounds it: for each (channel, state, position) one v_exp_f32 and five fp32
+// instructions; the bytes (x, dt, z, y) are 1/N of that many elements.  A loop of
+// those six on registers reaches 0.182 ps an element with 8 waves a SIMD.
+// [1, 4096, 8192] bf16, N = 16: 178 us for that rate's 98; the lane scan, the steps
+// and gates and the staging of B and C add 3.8 instructions to the six, and there
+// are 4 waves a SIMD (their vector instructions, at 4 cycles each and 8 an
+// exponential, make 0.89 of the time).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -13,11 +13,12 @@
 // the segments then run side by side, each chaining what is behind it.
 //
 // What bounds it: issue of the vector ALUs, 27 instructions for each (channel,
-// state, position): an exponential (two issue slots), 17 for the chains and the
-// sums over states and positions, 5 for the sums over a wave's channels, 2 for the
-// lane scans.  256 registers a lane leave two waves a SIMD, which keep it busy for 80% of
-// the 268 us at [4, 2048, 2048] bf16, N = 16 (with scan_join's 12 us, whose 67 MB
-// come from the caches).
+// state, position): an exponential, 15 of the formula's chains and sums over states
+// and positions, 5 for the sums over a wave's channels, 2 for the lane scans, the
+// rest selects and addresses.  A loop of the formula's 16 on registers reaches 0.389 ps
+// an element with 8 waves a SIMD, 104 us at [4, 2048, 2048] bf16, N = 16; here 256
+// registers a lane leave two waves, and it takes 262 us (and scan_join 12, whose
+// 67 MB come from the caches).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

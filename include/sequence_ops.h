@@ -129,6 +129,9 @@ CONV2D_GI_API int causal_conv_step(const causal_conv_step_args *a, hipStream_t s
  * checkpoints (NULL: not wanted) receives the state before every
  * SEQ_SCAN_CHECKPOINT-th position, [B, D, ceil(L / SEQ_SCAN_CHECKPOINT), N], for
  * the backward call.  The states are kept in fp32 registers throughout.
+ * A is meant to be negative; -inf forgets the state at each position.  Where decays
+ * above 1 multiply beyond fp32's range over up to 1024 positions, a state of 0 may
+ * come out as NaN.
  */
 enum { SEQ_SCAN_CHECKPOINT = 128 };
 typedef struct state_scan_args {
@@ -204,6 +207,7 @@ CONV2D_GI_API int state_scan_step(const state_scan_step_args *a, hipStream_t str
  *   r_out = r + scale * sigmoid(gate) * n   (scale or gate NULL: without it)
  *   u     = rms(r_out) * w_pre              (w_pre NULL: no u)
  *
+ * eps >= 0; at eps = 0 a position whose values are all 0 is 0/0.
  * y, gate and u have the call's type, r and r_out [B, D, L] are fp32 (r_out may
  * be r itself, same strides).  r_out and u are 0 beyond a sequence's length.
  */
