@@ -16,6 +16,7 @@ namespace {
 // Grid sizes: batch items are a grid's y, rows and row pieces its x.
 constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
+constexpr int64_t kMaxStepRows = (int64_t)1 << 28;
 constexpr int64_t kMaxPositions = (int64_t)1 << 26;
 constexpr int64_t kMaxBatchPositions = (int64_t)1 << 31;  // of all batch items; counted in 32 bits
 // A norm's work-groups have 1024 work-items at most, and a grid less than 2^32.
@@ -28,6 +29,15 @@ int check_sizes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
     if (B > kMaxBatch || B * D >= kMaxRows || L > kMaxPositions || B * L >= kMaxBatchPositions)
         return CONV2D_GI_EUNSUPPORTED;
     return CONV2D_GI_OK;
+}
+
+// One position of each row: a batch item is a grid's y, and offsets are 64-bit, so that
+// large batches of wide layers fit too.
+int check_step(int32_t dtype, int64_t B, int64_t D) {
+    const int rc = check_sizes(dtype, 1, D, 1);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (B < 1) return CONV2D_GI_EINVAL;
+    return B > kMaxBatch || B * D >= kMaxStepRows ? CONV2D_GI_EUNSUPPORTED : CONV2D_GI_OK;
 }
 
 int check_norm(int64_t B, int64_t D, int64_t L, bool backward, float eps) {
@@ -116,7 +126,7 @@ int causal_conv_backward(const causal_conv_backward_args *a, hipStream_t stream)
 
 int causal_conv_step(const causal_conv_step_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
-    int rc = check_sizes(a->dtype, a->B, a->D, 1);
+    int rc = check_step(a->dtype, a->B, a->D);
     if (rc == CONV2D_GI_OK) rc = check_taps(a->K);
     if (rc != CONV2D_GI_OK) return rc;
     if (!a->x.data || !a->y.data || !a->w || (!a->state && a->K > 1)) return CONV2D_GI_EINVAL;
@@ -181,7 +191,7 @@ int state_scan_plan(int32_t B, int32_t D, int32_t L, int32_t N, int32_t G, int32
 
 int state_scan_step(const state_scan_step_args *a, hipStream_t stream) {
     if (!a) return CONV2D_GI_EINVAL;
-    int rc = check_sizes(a->dtype, a->B, a->D, 1);
+    int rc = check_step(a->dtype, a->B, a->D);
     if (rc == CONV2D_GI_OK) rc = check_states(a->D, a->N, a->G);
     if (rc != CONV2D_GI_OK) return rc;
     if (!a->x.data || !a->dt.data || !a->Bm.data || !a->Cm.data || !a->y.data || !a->A ||

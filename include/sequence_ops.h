@@ -49,8 +49,9 @@ extern "C" {
 enum { SEQ_F32 = 0, SEQ_BF16 = 1, SEQ_F16 = 2 };
 
 /* Limits: taps of a causal convolution, states of a scan, channels of a norm.
-   Of every entry: B <= 65535, B*D < 2^24, L <= 2^26, B*L < 2^31 (norms: about
-   2^27, block_norm_forward with 1025 .. 2048 channels 2^26: whole tiles of positions);
+   Of every entry: B <= 65535, B*D < 2^24 (single tokens: D < 2^24, B*D < 2^28),
+   L <= 2^26, B*L < 2^31 (norms: about 2^27, block_norm_forward with 1025 .. 2048
+   channels 2^26, in whole tiles of positions);
    of state_scan_backward also 2*B*G*N*(L+256) + D*(N+2) < 2^32 - 512. */
 enum { SEQ_MAX_TAPS = 8, SEQ_MAX_STATES = 256, SEQ_MAX_NORM_CHANNELS = 65536 };
 

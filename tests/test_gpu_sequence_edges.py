@@ -271,6 +271,27 @@ def test_scan_of_more_states_and_positions_than_gradients_have():
     assert torch.equal(y, y[:1].expand_as(y)) and torch.equal(state, state[:1].expand_as(state))
 
 
+@pytest.mark.parametrize("B,D", [(4200, 4096), (2048, 8200)])
+def test_generation_steps_of_large_batches(B, D):
+    """B*D beyond 2^24: rows of two kinds in turn, so that one of each tells all."""
+    i = Inputs(B, "bf16")
+    kinds = torch.arange(B, device="cuda") % 2
+    x, dt, Bm, Cm = i.normal(2, D), i.normal(2, D, scale=0.3), i.normal(2, 1, 4), i.normal(2, 1, 4)
+    w, A, bias = i.params(D, 4, scale=0.5), i.params(D, 4, low=-4, high=-0.05), i.params(D, low=-5, high=-3)
+    lines, states = i.normal(2, D, 3), i.params(2, D, 4)
+    line, state = lines[kinds], states[kinds]
+    y = gi.causal_conv_step(x[kinds], line, w)
+    ry, rline, S = oracle.causal_conv(num(x)[0][..., None], *num(w), None, True, *num(lines))
+    check(y[:2], ry[..., 0], S[..., 0], 18 + S.max(), "y")
+    assert torch.equal(y, y[kinds]) and torch.equal(line, line[kinds]) and (num(line[:2])[0] == rline).all()
+    y = gi.state_scan_step(x[kinds], dt[kinds], A, Bm[kinds], Cm[kinds], state, dt_bias=bias)
+    ry, rh, S, H = oracle.state_scan(*[v[..., None] for v in num(x, dt)], *num(A), *[v[..., None] for v in num(Bm, Cm)],
+                                     None, None, *num(bias), True, *num(states))
+    check(y[:2], ry[..., 0], S[..., 0], 96 + 8 * 4, "y")
+    check(state[:2], rh, H, 96, "state")
+    assert torch.equal(y, y[kinds]) and torch.equal(state, state[kinds])
+
+
 # ---- streams -------------------------------------------------------------------------------------
 
 

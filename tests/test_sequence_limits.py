@@ -46,3 +46,15 @@ def test_norm_is_refused_by_the_columns_its_work_groups_have(lib):  # noqa: F811
         assert call("block_norm", **sizes) == code, (L, D)
     assert call("block_norm_backward", B=8, D=1500, L=1 << 23, **{"dr.channel": 0}) == gi.EINVAL
     assert call("block_norm", B=65535, D=64, L=1, **{"r_out.channel": 0, "r_out.batch": 0}) == gi.EINVAL
+
+
+def test_generation_steps_of_large_batches(lib):  # noqa: F811
+    """B*D < 2^24 is for forms whose grid runs over all rows; a step's does not."""
+    for name in ("causal_conv_step", "state_scan_step"):
+        for B, D, code in ((4096, 4096, gi.EINVAL), (2048, 8192, gi.EINVAL), (65535, 4000, gi.EINVAL),
+                           (65535, 4100, gi.EUNSUPPORTED), (1, 1 << 24, gi.EUNSUPPORTED), (1, (1 << 24) - 2, gi.EINVAL),
+                           (0, 4, gi.EINVAL)):
+            sizes = dict(B=B, D=D, lines=65535)
+            if code == gi.EINVAL:
+                sizes.update(APART, **{"y.batch": 0})
+            assert call(name, **sizes) == code, (name, B, D)
