@@ -10,8 +10,8 @@ If the library has not been built, importing works but every call raises
 
 The C entry points mirror these names (include/conv2d_grad_input.h; the test
 hooks are in include/conv2d_grad_input_testing.h and are thread-local).  The
-sequence operators (causal_conv, state_scan, block_norm; include/sequence_ops.h)
-are in ``conv2d_backward_amd.sequence`` and reached from here as well.
+sequence operators (causal_conv, state_scan, gated_scan, block_norm, project_int8;
+include/sequence_ops.h) are in ``conv2d_backward_amd.sequence`` and reached from here as well.
 """
 from __future__ import annotations
 
@@ -25,6 +25,8 @@ __all__ = [
     "VARIANT_COL2IM",
     "causal_conv", "causal_conv_backward", "causal_conv_step", "state_scan", "state_scan_backward",
     "state_scan_step", "state_scan_plan", "block_norm", "block_norm_backward", "ScanGrads", "NormGrads", "SCAN_CHECKPOINT",
+    "gated_scan", "gated_scan_backward", "gated_scan_step", "gated_scan_plan", "GatedGrads",
+    "quantize_tokens", "quantize_weight", "project_int8", "project_int8_step", "INT8_ROW",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -548,6 +550,8 @@ def forward(x, weight, *, stride: int, padding, out=None, stream=None):
 
 
 # (It needs the names above, and loads neither torch nor its extension module before a call.)
-from .sequence import (SCAN_CHECKPOINT, NormGrads, ScanGrads, block_norm,  # noqa: E402
-                       block_norm_backward, causal_conv, causal_conv_backward, causal_conv_step,
-                       state_scan, state_scan_backward, state_scan_plan, state_scan_step)
+from .sequence import (INT8_ROW, SCAN_CHECKPOINT, GatedGrads, NormGrads, ScanGrads,  # noqa: E402
+                       block_norm, block_norm_backward, causal_conv, causal_conv_backward,
+                       causal_conv_step, gated_scan, gated_scan_backward, gated_scan_plan,
+                       gated_scan_step, project_int8, project_int8_step, quantize_tokens,
+                       quantize_weight, state_scan, state_scan_backward, state_scan_plan, state_scan_step)

@@ -38,6 +38,8 @@ SOURCES = [
     "kernels_state_scan.hip",
     "kernels_state_scan_bwd.hip",
     "kernels_block_norm.hip",
+    "kernels_gated_scan.hip",
+    "kernels_int8.hip",
     "seq_api.cpp",
     "kernels_peak.hip",
 ]

@@ -1,0 +1,536 @@
+// kernels_gated_scan.hip -- the gated recurrence: prompts, its gradients, and one
+// position of it against a state cache.
+//
+// h_t = a_t h_{t-1} + m_t e_t with a = exp(A sr), sr = sigmoid(r + r_bias), m =
+// sqrt(1 - a^2) and e = sigmoid(i + i_bias) x is a chain along the positions, and
+// maps h -> P h + Q compose.  A lane takes 8 consecutive positions, runs their chain
+// once from 0 for its map, 16 lanes (a DPP row) combine their maps in four steps, the
+// rows of a wave and the waves of a work-group theirs one after the other, and each
+// lane runs its chain again from the state it then knows.  The gradient q of h is the
+// same chain from the right, c -> a_t (gy_t + c), whose maps have the same P; h is run
+// again from the checkpoint that the forward call leaves every 128 positions, one
+// for each row of lanes.
+//
+// What bounds it: memory.  A position has 5 activations forward and 9 backward, and
+// some 40 and 70 fp32 instructions beside 8 of the slow ones (exponentials, roots,
+// reciprocals).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdio>
+
+#include "seq_common.h"
+#include "seq_kernels.h"
+
+namespace seq {
+namespace {
+
+constexpr int T = 8;            // positions of a lane
+constexpr int kRow = 16 * T;    // positions of a row of lanes
+static_assert(kRow == SEQ_SCAN_CHECKPOINT, "a checkpoint for every row of lanes");
+
+// 1 - a^2 = -e^v + 1, v = 2 u, loses all digits in fp32 where a is near 1, which is
+// where such layers work (u is -1e-4 to -0.1).  With t = e^u - 1 it is -t (2 + t), and t
+// comes from its series up to u^7 / 5040 above -0.3 (the next term is 5e-9 there), from a
+// below, where a - 1 has lost less than two bits.
+struct Decay {
+    float a, n;  // e^u, 1 - e^2u
+};
+__device__ __forceinline__ Decay decay(float sr, float A, float A2) {
+    const float u = sr * A;
+    Decay d;
+    d.a = exp2_fast(sr * A2);
+    float t = __builtin_fmaf(u, 1.f / 5040, 1.f / 720);
+    t = __builtin_fmaf(u, t, 1.f / 120);
+    t = __builtin_fmaf(u, t, 1.f / 24);
+    t = __builtin_fmaf(u, t, 1.f / 6);
+    t = __builtin_fmaf(u, t, 0.5f);
+    t = __builtin_fmaf(u, t, 1.f) * u;
+    t = u > -0.3f ? t : d.a - 1.f;
+    d.n = -t * (2.f + t);
+    return d;
+}
+// A rate of -inf becomes the lowest float: a closed gate (sr = 0) then still keeps the state.
+__device__ __forceinline__ float finite_rate(float A) {
+    return A < -3.4028234664e38f ? -3.4028234664e38f : A;
+}
+
+// sigmoid(v + bias), the bias times -log2(e).
+__device__ __forceinline__ float gate(float v, float bias) {
+    return __builtin_amdgcn_rcpf(1.f + exp2_fast(__builtin_fmaf(v, -kLog2e, bias)));
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float old, float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+        __builtin_bit_cast(int, old), __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+constexpr int kRowShl1 = 0x101, kRowShr1 = 0x111, kRowFirst = 0x150, kRowLast = 0x15f;
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// Inclusive maps of the lanes of a row, from its first lane (or, BACK, from its last).
+template <bool BACK>
+__device__ __forceinline__ void scan_row(float &P, float &Q) {
+    if constexpr (BACK)
+        asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP1, "shl") SEQ_STEP1("row_shl:8" SEQ_ALL)
+            "s_nop 0" : "+v"(Q), "+v"(P));
+    else
+        asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP1, "shr") SEQ_STEP1("row_shr:8" SEQ_ALL)
+            "s_nop 0" : "+v"(Q), "+v"(P));
+}
+
+// The value that enters each lane, from its map (P, Q) and the value `start` that enters
+// the work-group's row of W * LANES lanes; start becomes what leaves it.  W > 1: `meet`
+// has W maps, which nothing else uses before the barrier after the next one.
+template <int LANES, int W, bool BACK>
+__device__ __forceinline__ float enter(float P, float Q, float &start, float2 *meet) {
+    scan_row<BACK>(P, Q);
+    const float before_P = BACK ? dpp<kRowShl1>(1.f, P) : dpp<kRowShr1>(1.f, P);
+    const float before_Q = BACK ? dpp<kRowShl1>(0.f, Q) : dpp<kRowShr1>(0.f, Q);
+    if constexpr (LANES == 16) {
+        static_assert(W == 1, "rows of 16 lanes are in one wave");
+        const float into = __builtin_fmaf(before_P, start, before_Q);
+        const float all_P = BACK ? dpp<kRowFirst>(0.f, P) : dpp<kRowLast>(0.f, P);
+        const float all_Q = BACK ? dpp<kRowFirst>(0.f, Q) : dpp<kRowLast>(0.f, Q);
+        start = __builtin_fmaf(all_P, start, all_Q);
+        return into;
+    } else {
+        // The rows in the chain's order.
+        float rP[4], rQ[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int lane = BACK ? 48 - 16 * k : 16 * k + 15;
+            rP[k] = lane_value(P, lane);
+            rQ[k] = lane_value(Q, lane);
+        }
+        float mine = start;
+        if constexpr (W > 1) {
+            float wP = rP[0], wQ = rQ[0];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) {
+                wQ = __builtin_fmaf(rP[k], wQ, rQ[k]);
+                wP *= rP[k];
+            }
+            const int wave = threadIdx.x / 64;
+            if (threadIdx.x % 64 == 0) meet[wave] = float2{wP, wQ};
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const int w = BACK ? W - 1 - k : k;
+                const float2 v = meet[w];
+                if (w == wave) mine = start;
+                start = __builtin_fmaf(v.x, start, v.y);
+            }
+        }
+        const int place = threadIdx.x % 64 / 16, row = BACK ? 3 - place : place;
+        float s = mine, at = mine;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            s = __builtin_fmaf(rP[k], s, rQ[k]);
+            if (row > k) at = s;
+        }
+        if constexpr (W == 1) start = __builtin_fmaf(rP[3], s, rQ[3]);
+        return __builtin_fmaf(before_P, at, before_Q);
+    }
+}
+
+template <class E>
+struct GatedFwd {
+    View<E> x, r, i, z, y;
+    const float *A, *r_bias, *i_bias, *state_in;
+    float *state_out, *checkpoints;
+    const int32_t *lengths;
+    int rows, D, L, marks;
+};
+
+// Rows of a work-group: one of W waves, or, W = 1, four waves with 64 / LANES rows each.
+template <int LANES, int W>
+constexpr int kThreadsOf = W == 1 ? 256 : 64 * W;
+template <int LANES, int W>
+constexpr int kRowsOf = kThreadsOf<LANES, W> / (LANES * W);
+
+template <class E, int LANES, int W>
+__global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_forward(GatedFwd<E> a) {
+    constexpr int CHUNK = LANES * W * T, ROWS = kRowsOf<LANES, W>;
+    __shared__ float2 meet[2][W];
+    const int lane = threadIdx.x % (LANES * W);
+    const int row = blockIdx.x * ROWS + threadIdx.x / (LANES * W);
+    if (row >= a.rows) return;  // (W > 1: one row, all or none)
+    const int b = row / a.D, d = row - b * a.D;
+    const int len = length_of(a.lengths, b, a.L);
+    const float A = finite_rate(a.A[d]), A2 = decay_rate(a.A[d]);
+    const float r_bias = a.r_bias ? a.r_bias[d] * -kLog2e : 0.f;
+    const float i_bias = a.i_bias ? a.i_bias[d] * -kLog2e : 0.f;
+    const auto *x = a.x.row(b, d), *r = a.r.row(b, d), *i = a.i.row(b, d);
+    const auto *z = a.z.p ? a.z.row(b, d) : nullptr;
+    auto *y = a.y.row(b, d);
+    float state = a.state_in ? a.state_in[row] : 0.f;
+    float *marks = a.checkpoints ? a.checkpoints + (int64_t)row * a.marks : nullptr;
+    Octet<E> nx, nr, ni, nz;
+    const auto prefetch = [&](int t) {
+        nx.load(x + t, len - t);
+        nr.load(r + t, len - t);
+        ni.load(i + t, len - t);
+        if (z) nz.load(z + t, len - t);
+    };
+    if (len > 0) prefetch(lane * T);
+    int c0 = 0;
+    for (int turn = 0; c0 < len; c0 += CHUNK, turn ^= 1) {
+        const int t0 = c0 + lane * T;
+        float av[T], in[T], f[T], P = 1.f, Q = 0.f;
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            const float sr = gate(nr.at(k), r_bias), si = gate(ni.at(k), i_bias);
+            const Decay v = decay(sr, A, A2);
+            av[k] = v.a;
+            in[k] = __builtin_amdgcn_sqrtf(v.n) * (si * nx.at(k));
+            if (z) f[k] = nz.at(k) * sigmoid(nz.at(k));
+        }
+        if (c0 + CHUNK > len) {
+#pragma unroll
+            for (int k = 0; k < T; ++k) {  // beyond the length the state passes unchanged
+                av[k] = len - t0 > k ? av[k] : 1.f;
+                in[k] = len - t0 > k ? in[k] : 0.f;
+            }
+        }
+        if (c0 + CHUNK < len) prefetch(t0 + CHUNK);
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            Q = __builtin_fmaf(av[k], Q, in[k]);
+            P *= av[k];
+        }
+        float h = enter<LANES, W, false>(P, Q, state, meet[turn]);
+        if (marks && t0 % SEQ_SCAN_CHECKPOINT == 0 && t0 < a.L)
+            marks[t0 / SEQ_SCAN_CHECKPOINT] = h;
+        float out[T];
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            h = __builtin_fmaf(av[k], h, in[k]);
+            out[k] = z ? h * f[k] : h;
+        }
+        if (c0 + CHUNK > len) {
+#pragma unroll
+            for (int k = 0; k < T; ++k) out[k] = len - t0 > k ? out[k] : 0.f;
+        }
+        if (t0 < a.L) store_row<E, T>(y, t0, a.L, out);
+    }
+    float zero[T];
+#pragma unroll
+    for (int k = 0; k < T; ++k) zero[k] = 0.f;
+    for (int t = c0 + lane * T; t < a.L; t += CHUNK) {
+        store_row<E, T>(y, t, a.L, zero);
+        if (marks && t % SEQ_SCAN_CHECKPOINT == 0) marks[t / SEQ_SCAN_CHECKPOINT] = state;
+    }
+    if (a.state_out && lane == 0) a.state_out[row] = state;
+}
+
+template <class E>
+struct GatedBwd {
+    View<E> gout, x, r, i, z, dx, dr, di, dz;
+    const float *A, *r_bias, *i_bias, *checkpoints, *gstate;
+    float *params;  // [rows][3]: a row's part of dA, dr_bias and di_bias
+    float *dstate;
+    const int32_t *lengths;
+    int rows, D, L, marks;
+};
+
+template <class E, int LANES, int W>
+__global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_backward(GatedBwd<E> a) {
+    constexpr int CHUNK = LANES * W * T, ROWS = kRowsOf<LANES, W>;
+    __shared__ float2 meet[2][W];
+    __shared__ float sums[3][W];
+    const int lane = threadIdx.x % (LANES * W);
+    const int row = blockIdx.x * ROWS + threadIdx.x / (LANES * W);
+    if (row >= a.rows) return;
+    const int b = row / a.D, d = row - b * a.D;
+    const int len = length_of(a.lengths, b, a.L);
+    const float A = finite_rate(a.A[d]), A2 = decay_rate(a.A[d]);
+    const float r_bias = a.r_bias ? a.r_bias[d] * -kLog2e : 0.f;
+    const float i_bias = a.i_bias ? a.i_bias[d] * -kLog2e : 0.f;
+    const auto *x = a.x.row(b, d), *r = a.r.row(b, d), *i = a.i.row(b, d), *g = a.gout.row(b, d);
+    const auto *z = a.z.p ? a.z.row(b, d) : nullptr;
+    auto *dx = a.dx.row(b, d), *dr = a.dr.row(b, d), *di = a.di.row(b, d);
+    auto *dz = z ? a.dz.row(b, d) : nullptr;
+    const float *marks = a.checkpoints + (int64_t)row * a.marks;
+    float back = a.gstate ? a.gstate[row] : 0.f;  // the gradient that comes from behind
+    float sum_A = 0.f, sum_r = 0.f, sum_i = 0.f;
+    const int chunks = (len + CHUNK - 1) / CHUNK;
+    Octet<E> nx, nr, ni, nz, ng;
+    float next_h = 0.f;
+    const auto prefetch = [&](int t) {
+        nx.load(x + t, len - t);
+        nr.load(r + t, len - t);
+        ni.load(i + t, len - t);
+        ng.load(g + t, len - t);
+        if (z) nz.load(z + t, len - t);
+        next_h = 0.f;
+        if (lane % 16 == 0 && t < len) next_h = marks[t / SEQ_SCAN_CHECKPOINT];
+    };
+    {
+        float zero[T];
+#pragma unroll
+        for (int k = 0; k < T; ++k) zero[k] = 0.f;
+        for (int t = chunks * CHUNK + lane * T; t < a.L; t += CHUNK) {
+            store_row<E, T>(dx, t, a.L, zero);
+            store_row<E, T>(dr, t, a.L, zero);
+            store_row<E, T>(di, t, a.L, zero);
+            if (z) store_row<E, T>(dz, t, a.L, zero);
+        }
+    }
+    if (chunks > 0) prefetch((chunks - 1) * CHUNK + lane * T);
+    for (int c = chunks - 1, turn = 0; c >= 0; --c, turn ^= 1) {
+        const int c0 = c * CHUNK, t0 = c0 + lane * T;
+        float av[T], m[T], inv[T], si[T], sr[T], e[T], gy[T], slope[T], h = next_h, P = 1.f, Q = 0.f;
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            sr[k] = gate(nr.at(k), r_bias);
+            si[k] = gate(ni.at(k), i_bias);
+            const Decay v = decay(sr[k], A, A2);
+            av[k] = v.a;
+            // 1 / m; where a is 1 the normaliser's slope, infinite there, counts as 0 (and
+            // below the normal range, whose root v_sqrt_f32 too takes for 0).
+            inv[k] = v.n >= 1.17549435e-38f ? __builtin_amdgcn_rsqf(v.n) : 0.f * v.n;
+            m[k] = v.n * inv[k];
+            e[k] = si[k] * nx.at(k);
+            gy[k] = ng.at(k);
+            if (z) {
+                const float sz = sigmoid(nz.at(k));
+                slope[k] = gy[k] * (sz * __builtin_fmaf(nz.at(k), 1.f - sz, 1.f));
+                gy[k] *= nz.at(k) * sz;
+            }
+        }
+        if (c0 + CHUNK > len) {
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                const bool in = len - t0 > k;
+                av[k] = in ? av[k] : 1.f;
+                m[k] = in ? m[k] : 0.f;
+                inv[k] = in ? inv[k] : 0.f;
+                e[k] = in ? e[k] : 0.f;
+                gy[k] = in ? gy[k] : 0.f;
+            }
+        }
+        if (c > 0) prefetch(t0 - CHUNK);
+        // h again, from the checkpoint before the row of lanes.
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            Q = __builtin_fmaf(av[k], Q, m[k] * e[k]);
+            P *= av[k];
+        }
+        {
+            float at = dpp<kRowFirst>(0.f, h), row_P = P;
+            h = enter<16, 1, false>(row_P, Q, at, nullptr);
+        }
+        float before[T];  // h before the position
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            before[k] = h;
+            h = __builtin_fmaf(av[k], h, m[k] * e[k]);
+            if (z) slope[k] *= h;
+        }
+        if (z && t0 < a.L) {
+            if (c0 + CHUNK > len) {
+#pragma unroll
+                for (int k = 0; k < T; ++k) slope[k] = len - t0 > k ? slope[k] : 0.f;
+            }
+            store_row<E, T>(dz, t0, a.L, slope);
+        }
+        Q = 0.f;
+#pragma unroll
+        for (int k = T - 1; k >= 0; --k) Q = av[k] * (gy[k] + Q);
+        float q = enter<LANES, W, true>(P, Q, back, meet[turn]);
+        float odx[T], odr[T], odi[T];
+#pragma unroll
+        for (int k = T - 1; k >= 0; --k) {
+            q += gy[k];
+            const float du = q * (av[k] * (before[k] - av[k] * inv[k] * e[k])) * sr[k];
+            const float qm = q * m[k];
+            odx[k] = qm * si[k];
+            odi[k] = qm * e[k] * (1.f - si[k]);
+            odr[k] = du * A * (1.f - sr[k]);
+            q *= av[k];
+            if (c0 + CHUNK > len) {
+                const bool in = len - t0 > k;
+                odx[k] = in ? odx[k] : 0.f;
+                odi[k] = in ? odi[k] : 0.f;
+                odr[k] = in ? odr[k] : 0.f;
+                sum_A += in ? du : 0.f;
+            } else {
+                sum_A += du;
+            }
+            sum_r += odr[k];
+            sum_i += odi[k];
+        }
+        if (t0 < a.L) {
+            store_row<E, T>(dx, t0, a.L, odx);
+            store_row<E, T>(dr, t0, a.L, odr);
+            store_row<E, T>(di, t0, a.L, odi);
+        }
+    }
+    if (a.dstate && lane == 0) a.dstate[row] = back;
+    float sum[3] = {sum_A, sum_r, sum_i};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+#pragma unroll
+        for (int s = 1; s < LANES; s *= 2) sum[k] += lane_xor(sum[k], s);
+    }
+    if constexpr (W > 1) {
+        if (lane % 64 == 0) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) sums[k][lane / 64] = sum[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            sum[k] = 0.f;
+            for (int w = 0; w < W; ++w) sum[k] += sums[k][w];
+        }
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) a.params[(int64_t)row * 3 + k] = sum[k];
+    }
+}
+
+// Sums over the batch, in its order.
+__global__ __launch_bounds__(256) void gated_join(const float *params, float *dA, float *dr_bias,
+                                                  float *di_bias, int B, int D) {
+    const int d = blockIdx.x * 256 + threadIdx.x;
+    if (d >= D) return;
+    float sum[3] = {0.f, 0.f, 0.f};
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sum[k] += params[((int64_t)b * D + d) * 3 + k];
+    dA[d] = sum[0];
+    if (dr_bias) dr_bias[d] = sum[1];
+    if (di_bias) di_bias[d] = sum[2];
+}
+
+template <class E>
+struct GatedStep {
+    View<E> x, r, i, z, y;
+    const float *A, *r_bias, *i_bias;
+    float *state;
+    const int32_t *slots;
+    int D, lines;
+};
+
+template <class E>
+__global__ __launch_bounds__(256) void gated_step(GatedStep<E> a) {
+    const int d = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
+    if (d >= a.D) return;
+    const int slot = a.slots ? a.slots[b] : b;
+    float out = 0.f;
+    if (slot >= 0 && slot < a.lines) {
+        float *state = a.state + (int64_t)slot * a.D + d;
+        const float sr = gate(E::up(*a.r.row(b, d)), a.r_bias ? a.r_bias[d] * -kLog2e : 0.f);
+        const float si = gate(E::up(*a.i.row(b, d)), a.i_bias ? a.i_bias[d] * -kLog2e : 0.f);
+        const Decay v = decay(sr, finite_rate(a.A[d]), decay_rate(a.A[d]));
+        out = __builtin_fmaf(v.a, *state, __builtin_amdgcn_sqrtf(v.n) * (si * E::up(*a.x.row(b, d))));
+        *state = out;
+        if (a.z.p) {
+            const float z = E::up(*a.z.row(b, d));
+            out *= z * sigmoid(z);
+        }
+    }
+    *a.y.row(b, d) = E::down(out);
+}
+
+// How the rows are dealt: lanes of a row in a wave, waves of a row.
+struct Deal {
+    int lanes, waves;
+};
+Deal pick_deal(int64_t rows, int64_t L) {
+    if (L <= 2 * kRow) return {16, 1};
+    Deal v{64, 1};
+    while (v.waves < 16 && v.waves * 64 * T < L && rows * v.waves < 4096) v.waves *= 2;
+    return v;
+}
+
+template <class E, int LANES, int W>
+hipError_t forward(const gated_scan_args &a, hipStream_t s) {
+    GatedFwd<E> k{view<E>(a.x), view<E>(a.r), view<E>(a.i), view<E>(a.z), view<E>(a.y), a.A,
+                  a.r_bias, a.i_bias, a.state_in, a.state_out, a.checkpoints, a.lengths,
+                  a.B * a.D, a.D, a.L, (a.L + kRow - 1) / kRow};
+    constexpr int ROWS = kRowsOf<LANES, W>;
+    gated_forward<E, LANES, W>
+        <<<(unsigned)((k.rows + ROWS - 1) / ROWS), kThreadsOf<LANES, W>, 0, s>>>(k);
+    return hipGetLastError();
+}
+
+template <class E, int LANES, int W>
+hipError_t backward(const gated_scan_backward_args &a, hipStream_t s) {
+    GatedBwd<E> k{view<E>(a.gout), view<E>(a.x), view<E>(a.r), view<E>(a.i), view<E>(a.z),
+                  view<E>(a.dx), view<E>(a.dr), view<E>(a.di), view<E>(a.dz), a.A, a.r_bias,
+                  a.i_bias, a.checkpoints, a.gstate, static_cast<float *>(a.workspace), a.dstate,
+                  a.lengths, a.B * a.D, a.D, a.L, (a.L + kRow - 1) / kRow};
+    constexpr int ROWS = kRowsOf<LANES, W>;
+    gated_backward<E, LANES, W>
+        <<<(unsigned)((k.rows + ROWS - 1) / ROWS), kThreadsOf<LANES, W>, 0, s>>>(k);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    gated_join<<<(unsigned)((a.D + 255) / 256), 256, 0, s>>>(k.params, a.dA, a.dr_bias, a.di_bias,
+                                                             a.B, a.D);
+    return hipGetLastError();
+}
+
+template <class E>
+hipError_t forward_any(const gated_scan_args &a, hipStream_t s) {
+    const Deal v = pick_deal((int64_t)a.B * a.D, a.L);
+    if (v.lanes == 16) return forward<E, 16, 1>(a, s);
+    switch (v.waves) {
+        case 1: return forward<E, 64, 1>(a, s);
+        case 2: return forward<E, 64, 2>(a, s);
+        case 4: return forward<E, 64, 4>(a, s);
+        case 8: return forward<E, 64, 8>(a, s);
+        default: return forward<E, 64, 16>(a, s);
+    }
+}
+
+template <class E>
+hipError_t backward_any(const gated_scan_backward_args &a, hipStream_t s) {
+    const Deal v = pick_deal((int64_t)a.B * a.D, a.L);
+    if (v.lanes == 16) return backward<E, 16, 1>(a, s);
+    switch (v.waves) {
+        case 1: return backward<E, 64, 1>(a, s);
+        case 2: return backward<E, 64, 2>(a, s);
+        case 4: return backward<E, 64, 4>(a, s);
+        case 8: return backward<E, 64, 8>(a, s);
+        default: return backward<E, 64, 16>(a, s);
+    }
+}
+
+template <class E>
+hipError_t step(const gated_scan_step_args &a, hipStream_t s) {
+    GatedStep<E> k{view<E>(a.x), view<E>(a.r), view<E>(a.i), view<E>(a.z), view<E>(a.y), a.A,
+                   a.r_bias, a.i_bias, a.state, a.slots, a.D, a.lines};
+    gated_step<E><<<dim3((unsigned)((a.D + 255) / 256), (unsigned)a.B), 256, 0, s>>>(k);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t gated_backward_workspace(int B, int D) { return (int64_t)B * D * 3 * sizeof(float); }
+
+void gated_plan(int64_t rows, int64_t L, int backward, char *buf, size_t len) {
+    const Deal v = pick_deal(rows, L);
+    std::snprintf(buf, len, "lanes=%d waves=%d", v.lanes, v.waves);
+}
+hipError_t launch_gated_forward(const gated_scan_args &a, hipStream_t s) {
+    return a.dtype == SEQ_F32 ? forward_any<F32>(a, s)
+           : a.dtype == SEQ_BF16 ? forward_any<BF16>(a, s) : forward_any<F16>(a, s);
+}
+hipError_t launch_gated_backward(const gated_scan_backward_args &a, hipStream_t s) {
+    return a.dtype == SEQ_F32 ? backward_any<F32>(a, s)
+           : a.dtype == SEQ_BF16 ? backward_any<BF16>(a, s) : backward_any<F16>(a, s);
+}
+hipError_t launch_gated_step(const gated_scan_step_args &a, hipStream_t s) {
+    return a.dtype == SEQ_F32 ? step<F32>(a, s)
+           : a.dtype == SEQ_BF16 ? step<BF16>(a, s) : step<F16>(a, s);
+}
+
+}  // namespace seq

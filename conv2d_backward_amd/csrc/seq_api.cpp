@@ -21,6 +21,8 @@ constexpr int64_t kMaxPositions = (int64_t)1 << 26;
 constexpr int64_t kMaxBatchPositions = (int64_t)1 << 31;  // of all batch items; counted in 32 bits
 // A norm's work-groups have 1024 work-items at most, and a grid less than 2^32.
 constexpr int64_t kMaxNormTiles = (int64_t)1 << 22;
+constexpr int64_t kMaxCodeRows = (int64_t)1 << 23;
+constexpr int64_t kMaxProduct = (int64_t)1 << 35;  // elements of a product's result
 constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;  // work-items of a grid along one axis
 
 int check_sizes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
@@ -83,6 +85,30 @@ bool is_apart(const seq_tensor &t, int64_t B, int64_t D, int64_t L) {
     // Channels inside a batch item, or batch items inside a channel.
     return (c >= row && b >= item) || (b >= row && c >= all);
 }
+
+int64_t int8_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ_INT8_ROW; }
+
+// Of a quantization.  A work-group has one position at least and 256 work-items, 1024 with more
+// positions.
+int check_codes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
+    if (dtype != SEQ_F32 && dtype != SEQ_BF16 && dtype != SEQ_F16) return CONV2D_GI_EINVAL;
+    if (B < 1 || D < 1 || L < 1) return CONV2D_GI_EINVAL;
+    return D > SEQ_MAX_INT8_CHANNELS || B * L >= kMaxCodeRows ? CONV2D_GI_EUNSUPPORTED
+                                                              : CONV2D_GI_OK;
+}
+
+// Of a product.  K bounds the sums: 128^2 * 65536 is below 2^31.  The smallest tiles have 16
+// work-items for each 256 elements of y, and a grid less than 2^32.
+int check_product(int32_t dtype, int64_t B, int64_t E, int64_t L, int64_t K) {
+    const int rc = check_codes(dtype, B, 1, L);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (E < 1 || K < SEQ_INT8_ROW || K % SEQ_INT8_ROW != 0) return CONV2D_GI_EINVAL;
+    return K > SEQ_MAX_INT8_CHANNELS || E >= kMaxRows || E * (B * L) >= kMaxProduct
+               ? CONV2D_GI_EUNSUPPORTED
+               : CONV2D_GI_OK;
+}
+
+bool is_codes(const void *p) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 bool is_workspace(const void *p, int64_t bytes, int64_t needed) {
     return needed == 0 || (p && bytes >= needed && reinterpret_cast<uintptr_t>(p) % 16 == 0);
@@ -240,6 +266,96 @@ int block_norm_backward(const block_norm_backward_args *a, hipStream_t stream) {
                       seq::norm_workspace(a->B, a->D, a->L, 1)))
         return CONV2D_GI_EINVAL;
     return status(seq::launch_norm_backward(*a, stream));
+}
+
+int gated_scan_forward(const gated_scan_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    const int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !a->r.data || !a->i.data || !a->y.data || !a->A) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->y, a->B, a->D, a->L)) return CONV2D_GI_EINVAL;
+    return status(seq::launch_gated_forward(*a, stream));
+}
+
+int64_t gated_scan_workspace(int32_t B, int32_t D, int32_t L) {
+    if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK) return -1;
+    return seq::gated_backward_workspace(B, D);
+}
+
+int gated_scan_backward(const gated_scan_backward_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    const int rc = check_sizes(a->dtype, a->B, a->D, a->L);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->gout.data || !a->x.data || !a->r.data || !a->i.data || !a->A || !a->checkpoints ||
+        !a->dx.data || !a->dr.data || !a->di.data || !a->dA)
+        return CONV2D_GI_EINVAL;
+    if (!a->z.data != !a->dz.data) return CONV2D_GI_EINVAL;
+    if ((a->dr_bias && !a->r_bias) || (a->di_bias && !a->i_bias)) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->dx, a->B, a->D, a->L) || !is_apart(a->dr, a->B, a->D, a->L) ||
+        !is_apart(a->di, a->B, a->D, a->L) || (a->dz.data && !is_apart(a->dz, a->B, a->D, a->L)))
+        return CONV2D_GI_EINVAL;
+    if (!is_workspace(a->workspace, a->workspace_bytes, seq::gated_backward_workspace(a->B, a->D)))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_gated_backward(*a, stream));
+}
+
+int gated_scan_plan(int32_t B, int32_t D, int32_t L, int32_t backward, char *buf, size_t len) {
+    if (!buf || len == 0) return CONV2D_GI_EINVAL;
+    const int rc = check_sizes(SEQ_F32, B, D, L);
+    if (rc != CONV2D_GI_OK) return rc;
+    seq::gated_plan((int64_t)B * D, L, backward, buf, len);
+    return CONV2D_GI_OK;
+}
+
+int gated_scan_step(const gated_scan_step_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    const int rc = check_step(a->dtype, a->B, a->D);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !a->r.data || !a->i.data || !a->y.data || !a->A || !a->state)
+        return CONV2D_GI_EINVAL;
+    if (a->lines < 1 || (!a->slots && a->lines < a->B)) return CONV2D_GI_EINVAL;
+    if (!is_apart(a->y, a->B, a->D, 1)) return CONV2D_GI_EINVAL;
+    return status(seq::launch_gated_step(*a, stream));
+}
+
+int quantize_tokens(const quantize_tokens_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    const int rc = check_codes(a->dtype, a->B, a->D, a->L);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !is_codes(a->codes) || !a->scales || a->K != int8_row(a->D))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_quantize(*a, stream));
+}
+
+int project_int8(const project_int8_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    const int rc = check_product(a->dtype, a->B, a->E, a->L, a->K);
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!is_codes(a->codes) || !is_codes(a->w) || !a->scales || !a->w_scales || !a->y.data ||
+        !is_apart(a->y, a->B, a->E, a->L))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_project(*a, stream));
+}
+
+int64_t project_int8_step_workspace(int32_t B, int32_t D, int32_t E) {
+    if (check_codes(SEQ_F32, B, D, 1) != CONV2D_GI_OK ||
+        check_product(SEQ_F32, B, E, 1, int8_row(D)) != CONV2D_GI_OK)
+        return -1;
+    return seq::project_step_workspace(B, D, E);
+}
+
+int project_int8_step(const project_int8_step_args *a, hipStream_t stream) {
+    if (!a) return CONV2D_GI_EINVAL;
+    int rc = check_codes(a->dtype, a->B, a->D, 1);
+    if (rc == CONV2D_GI_OK) rc = check_product(a->dtype, a->B, a->E, 1, int8_row(a->D));
+    if (rc != CONV2D_GI_OK) return rc;
+    if (!a->x.data || !is_codes(a->w) || !a->w_scales || !a->y.data || a->K != int8_row(a->D) ||
+        !is_apart(a->y, a->B, a->E, 1))
+        return CONV2D_GI_EINVAL;
+    if (!is_workspace(a->workspace, a->workspace_bytes,
+                      seq::project_step_workspace(a->B, a->D, a->E)))
+        return CONV2D_GI_EINVAL;
+    return status(seq::launch_project_step(*a, stream));
 }
 
 }  // extern "C"

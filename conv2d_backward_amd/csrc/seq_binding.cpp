@@ -27,6 +27,7 @@ enum Kind {
     kDense,   // contiguous, of the call's type
     kDense32, // contiguous float32
     kIndex,   // contiguous int32
+    kCodes,   // contiguous int8
 };
 enum Use { kNeeded, kOptional, kOut };
 
@@ -61,7 +62,7 @@ std::string text_of(const int64_t *shape, size_t n) {
 
 at::ScalarType type_of(int kind, at::ScalarType type) {
     if (kind == kAct32 || kind == kDense32) return at::kFloat;
-    return kind == kIndex ? at::kInt : type;
+    return kind == kIndex ? at::kInt : kind == kCodes ? at::kChar : type;
 }
 
 // Appends an operand's fields; false with a Python error set where it does not fit.
@@ -138,12 +139,13 @@ bool bind(const Entry &e, PyObject *given, int64_t *size, bool *known) {
     return true;
 }
 
-// call(entry, stream, sizes, operands) -> status, or the outputs in order.  A size
-// that is None comes from the operands.
+// call(entry, stream, sizes, operands[, code]) -> status, or the outputs in order.  A size
+// that is None comes from the operands.  code: the type of the call where the leading
+// operand does not have it.
 // An operand is a tensor, or None: an optional one is missing, an output is
 // allocated; False: an output is not wanted.
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t count) {
-    if (count != 4) {
+    if (count != 4 && count != 5) {
         PyErr_SetString(PyExc_TypeError, "call takes an entry, a stream, sizes and operands");
         return nullptr;
     }
@@ -166,7 +168,13 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t count) {
         }
         const at::Tensor &lead = THPVariable_Unpack(first);
         const c10::Device device = lead.device();
-        const at::ScalarType type = lead.scalar_type();
+        at::ScalarType type = lead.scalar_type();
+        if (count == 5) {
+            constexpr at::ScalarType kTypes[] = {at::kFloat, at::kBFloat16, at::kHalf};
+            const long given_code = PyLong_AsLong(args[4]);
+            if (PyErr_Occurred()) return nullptr;
+            type = given_code >= 0 && given_code < 3 ? kTypes[given_code] : at::kByte;
+        }
         const int code = type == at::kFloat ? 0 : type == at::kBFloat16 ? 1 : type == at::kHalf ? 2 : -1;
         if (code < 0) {
             refuse("%s must be float32, bfloat16 or float16%s", lead_name);

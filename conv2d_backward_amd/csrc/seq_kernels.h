@@ -27,4 +27,15 @@ hipError_t launch_norm_backward(const block_norm_backward_args &a, hipStream_t s
 int norm_columns(int64_t B, int64_t D, int64_t L);  // positions of a forward work-group
 int64_t norm_workspace(int B, int D, int L, int backward);
 
+hipError_t launch_gated_forward(const gated_scan_args &a, hipStream_t s);
+hipError_t launch_gated_backward(const gated_scan_backward_args &a, hipStream_t s);
+hipError_t launch_gated_step(const gated_scan_step_args &a, hipStream_t s);
+int64_t gated_backward_workspace(int B, int D);
+void gated_plan(int64_t rows, int64_t L, int backward, char *buf, size_t len);
+
+hipError_t launch_quantize(const quantize_tokens_args &a, hipStream_t s);
+hipError_t launch_project(const project_int8_args &a, hipStream_t s);
+hipError_t launch_project_step(const project_int8_step_args &a, hipStream_t s);
+int64_t project_step_workspace(int B, int D, int E);
+
 }  // namespace seq

@@ -1,8 +1,8 @@
 /*
  * sequence_ops.h -- C ABI of the sequence operators of the MI355X (gfx950)
  * convolution library: a depthwise causal convolution, a selective state space
- * scan, and the norms between two residual blocks.  Same shared library,
- * status codes and error text as conv2d_grad_input.h.
+ * scan, a gated recurrence, the norms between two residual blocks, and
+ * projections in 8-bit integers.  Same shared library, status codes and error text as conv2d_grad_input.h.
  *
  * Layouts
  * -------
@@ -52,8 +52,11 @@ enum { SEQ_F32 = 0, SEQ_BF16 = 1, SEQ_F16 = 2 };
    Of every entry: B <= 65535, B*D < 2^24 (single tokens: D < 2^24, B*D < 2^28),
    L <= 2^26, B*L < 2^31 (norms: about 2^27, block_norm_forward with 1025 .. 2048
    channels 2^26, in whole tiles of positions);
-   of state_scan_backward also 2*B*G*N*(L+256) + D*(N+2) < 2^32 - 512. */
-enum { SEQ_MAX_TAPS = 8, SEQ_MAX_STATES = 256, SEQ_MAX_NORM_CHANNELS = 65536 };
+   of state_scan_backward also 2*B*G*N*(L+256) + D*(N+2) < 2^32 - 512;
+   of the 8-bit projections instead: D and K <= SEQ_MAX_INT8_CHANNELS, B*L < 2^23,
+   E < 2^24, B*L*E < 2^35. */
+enum { SEQ_MAX_TAPS = 8, SEQ_MAX_STATES = 256, SEQ_MAX_NORM_CHANNELS = 65536,
+       SEQ_MAX_INT8_CHANNELS = 65536 };
 
 /* An activation [B, D, L]: element (b, d, t) at data[b*batch + d*channel + t].
    Strides in elements; they may be 0 (an input broadcast) or negative. */
@@ -245,6 +248,137 @@ typedef struct block_norm_backward_args {
 CONV2D_GI_API int block_norm_backward(const block_norm_backward_args *a, hipStream_t stream);
 /* Bytes of scratch for block_norm_forward (backward 0) or _backward (1). */
 CONV2D_GI_API int64_t block_norm_workspace(int32_t B, int32_t D, int32_t L, int32_t backward);
+
+/*
+ * gated_scan: the gated recurrence of one state a channel.
+ *
+ *   sr = sigmoid(r + r_bias[d]),  si = sigmoid(i + i_bias[d])
+ *   a[b,d,t] = exp(A[d] * sr[b,d,t])
+ *   h[b,d,t] = a * h[b,d,t-1] + sqrt(1 - a^2) * si * x[b,d,t]
+ *   y[b,d,t] = h * z * sigmoid(z)  (z given) or h           for t < len, 0 beyond
+ *
+ * h before position 0 is state_in ([B, D], NULL: zeros); state_out [B, D] (NULL:
+ * not wanted) is h after the last position.  checkpoints (NULL: not wanted)
+ * receives h before every SEQ_SCAN_CHECKPOINT-th position, [B, D, ceil(L /
+ * SEQ_SCAN_CHECKPOINT)], for the backward call.  h is kept in fp32 throughout.
+ * A is negative: -inf forgets the state wherever the gate r is not fully closed,
+ * 0 keeps it for good and lets nothing in, and above 0 the root gives NaN.
+ */
+typedef struct gated_scan_args {
+    int32_t dtype, B, D, L;
+    seq_tensor x, r, i, z, y;   /* z.data NULL: no gate of the output */
+    const float *A;             /* [D] */
+    const float *r_bias, *i_bias;   /* [D] or NULL */
+    const float *state_in;
+    float *state_out, *checkpoints;
+    const int32_t *lengths;
+} gated_scan_args;
+CONV2D_GI_API int gated_scan_forward(const gated_scan_args *a, hipStream_t stream);
+
+/*
+ * The gradients of gated_scan.  gout is the gradient of y, gstate [B, D] (NULL:
+ * zeros) that of state_out.  With m = sqrt(1 - a^2), gy = gout * silu(z) (or gout)
+ * and q[t] the gradient of h[t]:
+ *   q[t] = gy[t] + a[t+1] * q[t+1]                          (beyond len: gstate)
+ *   dx = q * m * si;   di = q * m * x * si * (1 - si)
+ *   du = q * (a * h[t-1] - a^2 / m * si * x);   dr = du * A * sr * (1 - sr)
+ *   dA = sum over b, t of du * sr;   dr_bias, di_bias = sums of dr, di
+ *   dz = gout * h * (d silu / d z);  dstate = a[0] * q[0]
+ * Where m is 0 (a is 1) the term with 1 / m counts as 0.  dx, dr, di, dz have x's
+ * layout rules and type; dA, dr_bias, di_bias [D], dstate [B, D] fp32.  dx, dr, di and
+ * dA are required, dz with z, the others may be NULL.  checkpoints: as the forward
+ * call on the same inputs wrote them.
+ */
+typedef struct gated_scan_backward_args {
+    int32_t dtype, B, D, L;
+    seq_tensor gout, x, r, i, z, dx, dr, di, dz;
+    const float *A, *r_bias, *i_bias, *checkpoints, *gstate;
+    float *dA, *dr_bias, *di_bias, *dstate;
+    const int32_t *lengths;
+    void *workspace;
+    int64_t workspace_bytes;
+} gated_scan_backward_args;
+CONV2D_GI_API int gated_scan_backward(const gated_scan_backward_args *a, hipStream_t stream);
+CONV2D_GI_API int64_t gated_scan_workspace(int32_t B, int32_t D, int32_t L);
+
+/*
+ * Host-only: how a gated_scan_forward (backward = 0) or _backward call of these
+ * sizes is dealt, as text: lanes of a row in a wave and waves of a row.
+ */
+CONV2D_GI_API int gated_scan_plan(int32_t B, int32_t D, int32_t L, int32_t backward, char *buf,
+                                  size_t len);
+
+/*
+ * One position of gated_scan for every row: x, r, i, z, y [B, D], state [lines, D]
+ * dense fp32, updated in place.
+ */
+typedef struct gated_scan_step_args {
+    int32_t dtype, B, D, lines;
+    seq_tensor x, r, i, z, y;
+    const float *A, *r_bias, *i_bias;
+    float *state;
+    const int32_t *slots;
+} gated_scan_step_args;
+CONV2D_GI_API int gated_scan_step(const gated_scan_step_args *a, hipStream_t stream);
+
+/*
+ * Projections in 8-bit integers: y = W x at every position, with a scale for each
+ * position and one for each output channel.
+ *
+ * Codes.  A row of D numbers v with most = max |v| has the scale most / 127 and the
+ * codes rint(127 v / most) (nearest, ties to even, decided exactly), int8 in
+ * [-127, 127]; a row of zeros has scale 0 and codes 0, one with an infinity or a NaN
+ * scale NaN and codes 0, so that what is made of it is NaN.  Rows of codes are K
+ * bytes, D rounded up to a multiple of SEQ_INT8_ROW, the rest 0; codes are aligned to
+ * 16 bytes.
+ */
+enum { SEQ_INT8_ROW = 128 };
+
+/*
+ * quantize_tokens: codes [B, L, K] and scales [B, L] of the positions of x [B, D, L];
+ * beyond a length both are 0.  A matrix [E, D] is the batch of E positions [E, D, 1].
+ */
+typedef struct quantize_tokens_args {
+    int32_t dtype, B, D, L, K, reserved;
+    seq_tensor x;
+    void *codes;
+    float *scales;
+    const int32_t *lengths;
+} quantize_tokens_args;
+CONV2D_GI_API int quantize_tokens(const quantize_tokens_args *a, hipStream_t stream);
+
+/*
+ * project_int8: y[b,e,l] = scales[b,l] * w_scales[e] * (sum over k of codes[b,l,k] *
+ * w[e,k]) + bias[e], 0 beyond a length.  codes [B, L, K], scales [B, L], w [E, K],
+ * w_scales [E], bias [E] (NULL: none); dtype is y's.  The sum is exact, in 32 bits.
+ */
+typedef struct project_int8_args {
+    int32_t dtype, B, E, L, K, reserved;
+    const void *codes;
+    const float *scales;
+    const void *w;
+    const float *w_scales, *bias;
+    seq_tensor y;
+    const int32_t *lengths;
+} project_int8_args;
+CONV2D_GI_API int project_int8(const project_int8_args *a, hipStream_t stream);
+
+/*
+ * quantize_tokens and project_int8 of one position for every row: y [B, E] from x
+ * [B, D] (seq_tensor.channel: the element stride along D and E).  The result is that
+ * of the two calls, bit for bit.
+ */
+typedef struct project_int8_step_args {
+    int32_t dtype, B, D, E, K, reserved;
+    seq_tensor x;
+    const void *w;
+    const float *w_scales, *bias;
+    seq_tensor y;
+    void *workspace;
+    int64_t workspace_bytes;
+} project_int8_step_args;
+CONV2D_GI_API int project_int8_step(const project_int8_step_args *a, hipStream_t stream);
+CONV2D_GI_API int64_t project_int8_step_workspace(int32_t B, int32_t D, int32_t E);
 
 #ifdef __cplusplus
 }

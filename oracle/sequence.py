@@ -1,6 +1,6 @@
 """Sequence operators in numpy float64, written position by position.
 
-The plain counterpart of causal_conv, state_scan and block_norm: the tests
+The plain counterpart of causal_conv, state_scan, gated_scan, block_norm and project_int8: the tests
 compare the GPU kernels with these, and these with differences.  Every function
 also gives, as ``S``, its outputs' sums with every term taken by magnitude, the
 scale that rounding errors of the sums are measured on.
@@ -250,3 +250,101 @@ def block_norm_grads(gr, gu, y, r_out, w_post=None, w_pre=None, gate=None, scale
         o["dscale"] = (dr * open_ * n).sum((0, 2))
         o["Sdscale"] = (Sdr * open_ * np.abs(n)).sum((0, 2))
     return o
+
+
+def gated_scan(x, r, i, A, z=None, r_bias=None, i_bias=None, state=None, lengths=None, every=0):
+    """(y, new_state, S of y, S of the state[, states before every `every`-th position])."""
+    x, r, i, A, z, r_bias, i_bias, state = _f64(x, r, i, A, z, r_bias, i_bias, state)
+    B, D, L = x.shape
+    y, S = np.zeros((B, D, L)), np.zeros((B, D, L))
+    h = np.zeros((B, D)) if state is None else state.copy()
+    H = np.abs(h)
+    marks = []
+    ns = np.array(_lengths(lengths, B, L))
+    for t in range(L):
+        if every and t % every == 0:
+            marks.append(h.copy())
+        for b in np.nonzero(t < ns)[0]:
+            u = A * sigmoid(r[b, :, t] + (0 if r_bias is None else r_bias))
+            into = np.sqrt(-np.expm1(2 * u)) * x[b, :, t]
+            into = into * sigmoid(i[b, :, t] + (0 if i_bias is None else i_bias))
+            h[b], H[b] = np.exp(u) * h[b] + into, np.exp(u) * H[b] + np.abs(into)
+            f = 1 if z is None else z[b, :, t] * sigmoid(z[b, :, t])
+            y[b, :, t], S[b, :, t] = h[b] * f, H[b] * np.abs(f)
+    return (y, h, S, H, np.stack(marks, 2)) if every else (y, h, S, H)
+
+
+def gated_scan_grads(gout, x, r, i, A, z=None, r_bias=None, i_bias=None, state=None, lengths=None,
+                     gstate=None):
+    """{dx, dr, di, dA, dz, dr_bias, di_bias, dstate} and {"S" + name}."""
+    gout, x, r, i, A, z, r_bias, i_bias, state, gstate = _f64(
+        gout, x, r, i, A, z, r_bias, i_bias, state, gstate)
+    B, D, L = x.shape
+    o = {k: np.zeros((B, D, L)) for k in ("dx", "dr", "di", "dz")}
+    o.update({"dA": np.zeros(D), "dr_bias": np.zeros(D), "di_bias": np.zeros(D), "dstate": np.zeros((B, D))})
+    o.update({"S" + k: np.zeros_like(v) for k, v in o.items()})
+
+    def put(name, at, value, size):
+        o[name][at] += value
+        o["S" + name][at] += size
+
+    for b, n in enumerate(_lengths(lengths, B, L)):
+        sr = sigmoid(r[b, :, :n] + (0 if r_bias is None else r_bias[:, None]))
+        si = sigmoid(i[b, :, :n] + (0 if i_bias is None else i_bias[:, None]))
+        u = A[:, None] * sr
+        a, m = np.exp(u), np.sqrt(-np.expm1(2 * u))
+        with np.errstate(divide="ignore", invalid="ignore"):
+            slope = np.where(m > 0, a * a / m, 0.0)  # of -m along u
+        hs, Hs = np.zeros((n + 1, D)), np.zeros((n + 1, D))
+        if state is not None:
+            hs[0], Hs[0] = state[b], np.abs(state[b])
+        for t in range(n):
+            into = m[:, t] * si[:, t] * x[b, :, t]
+            hs[t + 1] = a[:, t] * hs[t] + into
+            Hs[t + 1] = a[:, t] * Hs[t] + np.abs(into)
+        back = np.zeros(D) if gstate is None else gstate[b].copy()
+        Back = np.abs(back)
+        for t in range(n - 1, -1, -1):
+            at, xt = (b, slice(None), t), x[b, :, t]
+            gy = gout[b, :, t].copy()
+            if z is not None:
+                zt = z[b, :, t]
+                sz = sigmoid(zt)
+                put("dz", at, gy * hs[t + 1] * sz * (1 + zt * (1 - sz)),
+                    np.abs(gy) * Hs[t + 1] * sz * (1 + np.abs(zt) * (1 - sz)))
+                gy *= zt * sz
+            q, Q = gy + back, np.abs(gy) + Back
+            put("dx", at, q * m[:, t] * si[:, t], Q * m[:, t] * si[:, t])
+            di = m[:, t] * xt * si[:, t] * (1 - si[:, t])
+            put("di", at, q * di, Q * np.abs(di))
+            put("di_bias", slice(None), q * di, Q * np.abs(di))
+            enter = slope[:, t] * si[:, t] * xt
+            du, Du = q * (a[:, t] * hs[t] - enter), Q * (a[:, t] * Hs[t] + np.abs(enter))
+            put("dA", slice(None), du * sr[:, t], Du * sr[:, t])
+            f = A * sr[:, t] * (1 - sr[:, t])
+            put("dr", at, du * f, Du * np.abs(f))
+            put("dr_bias", slice(None), du * f, Du * np.abs(f))
+            back, Back = a[:, t] * q, a[:, t] * Q
+        put("dstate", b, back, Back)
+    return o
+
+
+def int8_codes(rows, multiple=128):
+    """(codes [.., K], scales [..] as float32 holds them) of rows [.., D]: rint(127 v / most)."""
+    rows = np.asarray(rows, dtype=np.float64)
+    most = np.abs(rows).max(-1)
+    bad = ~np.isfinite(most)
+    codes = np.zeros(rows.shape[:-1] + (-(-rows.shape[-1] // multiple) * multiple,), np.int8)
+    fine = ~bad & (most > 0)
+    codes[fine, :rows.shape[-1]] = np.rint(127 * rows[fine] / most[fine][..., None])
+    with np.errstate(invalid="ignore"):
+        scales = np.where(bad, np.float32(np.nan), np.float32(most) / np.float32(127))
+    return codes, scales.astype(np.float32)
+
+
+def int8_product(codes, scales, w, w_scales, bias=None):
+    """y [E, n] of codes [n, K] and w [E, K], and the magnitude of its terms."""
+    sums = np.asarray(w, np.float64) @ np.asarray(codes, np.float64).T   # (exact: below 2^53)
+    f = np.asarray(w_scales, np.float64)[:, None] * np.asarray(scales, np.float64)
+    add = np.zeros(len(sums)) if bias is None else np.asarray(bias, np.float64)
+    return sums * f + add[:, None], np.abs(sums * f) + np.abs(add)[:, None]
