@@ -26,45 +26,67 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 // exactly.  Rows of very large or small numbers are scaled by a power of two first, so
 // that 127 v and 1 / most stay in range.
 struct Coder {
-    float factor, most, inv;   // of the scaled row: most, 1 / most
+    float times, most, inv;   // 127 2^k, 2^k most, 1 / (2^k most)
+    uint32_t keep;            // 0 where the row has no codes: zeros, or no numbers
 };
 __device__ __forceinline__ Coder coder(uint32_t most_bits) {
     Coder c;
     const float most = __builtin_bit_cast(float, most_bits);
-    c.factor = most > 0x1p100f ? 0x1p-64f : most < 0x1p-60f ? 0x1p64f : 1.f;
-    c.most = most * c.factor;
-    const bool coded = most_bits != 0 && most_bits < 0x7f800000u;
-    c.inv = coded ? __builtin_amdgcn_rcpf(c.most) : 0.f;
-    c.factor = coded ? c.factor : 0.f;
+    const float power = most > 0x1p100f ? 0x1p-64f : most < 0x1p-60f ? 0x1p64f : 1.f;
+    c.times = 127.f * power;
+    c.most = most * power;
+    c.inv = __builtin_amdgcn_rcpf(c.most);
+    c.keep = most_bits != 0 && most_bits < 0x7f800000u ? ~0u : 0u;
     return c;
 }
 __device__ __forceinline__ float row_scale(uint32_t most_bits) {
     return most_bits < 0x7f800000u ? __builtin_bit_cast(float, most_bits) / 127.f
                                    : __builtin_bit_cast(float, 0x7fc00000u);
 }
+// The code is the low byte of what is returned: adding 1.5 2^23 rounds to an integer, ties
+// to even, and leaves it in the low bits.
+//
 // 16-bit numbers: 127 v is exact in fp32.  One step of Newton's method makes the quotient
 // exact wherever it is half a step between two codes (it is a float then), and off by at
 // most 2^-24 of it elsewhere, where it is at least 2^-18 of it away from the border.
 // float32: the remainder of the nearest candidate, against half of most; 127 v has a low
 // part, and every other term is exact.
 template <class E>
-__device__ __forceinline__ int code(float v, const Coder &c) {
-    v *= c.factor;
-    v = v != v || c.inv == 0.f ? 0.f : v;
-    const float hi = v * 127.f;
-    const float q = hi * c.inv;
+__device__ __forceinline__ uint32_t code(float v, const Coder &c) {
+    const float hi = v * c.times, q = hi * c.inv;
     if constexpr (!std::is_same_v<E, F32>) {
-        return (int)__builtin_rintf(__builtin_fmaf(__builtin_fmaf(-q, c.most, hi), c.inv, q));
+        const float exact = __builtin_fmaf(__builtin_fmaf(-q, c.most, hi), c.inv, q);
+        return __builtin_bit_cast(uint32_t, exact + 12582912.f);
     } else {
         const float k = __builtin_rintf(q);
-        const float r = __builtin_fmaf(-k, c.most, hi), lo = __builtin_fmaf(v, 127.f, -hi);
+        const float r = __builtin_fmaf(-k, c.most, hi), lo = __builtin_fmaf(v, c.times, -hi);
         const float over = (__builtin_fabsf(r) - 0.5f * c.most) + (r < 0.f ? -lo : lo);
-        const int n = (int)k, on = r < 0.f ? -1 : 1;
-        return over > 0.f || (over == 0.f && (n & 1)) ? n + on : n;
+        const uint32_t n = __builtin_bit_cast(uint32_t, k + 12582912.f);
+        return over > 0.f || (over == 0.f && (n & 1)) ? n + (r < 0.f ? -1 : 1) : n;
     }
 }
-__device__ __forceinline__ uint32_t pack(int a, int b, int c, int d) {
-    return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | (uint32_t)d << 24;
+// Four low bytes.
+__device__ __forceinline__ uint32_t pack(const uint32_t (&n)[4], uint32_t keep) {
+    const uint32_t lo = __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400u);
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[3], n[2], 0x04000c0cu), lo, 0x07060100u) & keep;
+}
+
+// The largest magnitudes of rows, as bits: those of |v| order like the numbers, infinities
+// and NaN above all.  16-bit numbers come in pairs.
+__device__ __forceinline__ uint32_t raise(uint32_t most, uint32_t bits, F32) {
+    return max(most, bits & 0x7fffffffu);
+}
+template <class E>
+__device__ __forceinline__ uint32_t raise(uint32_t most, uint32_t bits, E) {
+    typedef unsigned short Pair __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
+        __builtin_bit_cast(Pair, most), __builtin_bit_cast(Pair, bits & 0x7fff7fffu)));
+}
+// Bits of the float that a magnitude is.
+template <class E>
+__device__ __forceinline__ uint32_t wide(uint32_t bits) {
+    return __builtin_bit_cast(uint32_t, E::up(__builtin_bit_cast(
+        typename E::type, (std::conditional_t<sizeof(typename E::type) == 4, uint32_t, uint16_t>)bits)));
 }
 
 template <class E>
@@ -76,61 +98,112 @@ struct Quantize {
     int B, D, L, K, tiles;
 };
 
-// Bits of |v|: they order like the numbers, infinities and NaN above all.
-__device__ __forceinline__ uint32_t magnitude(float v) {
-    return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;
-}
-
-// Positions along the lanes: a work-group has 32 positions, its threads 8 of them and
-// every 64th quad of channels.
+// Positions along the lanes.  A work-group has 64 bytes of positions, its 1024 threads V
+// of them (16 bytes) and four channels at a time, 1024 channels in a round.  The first
+// KEPT rounds stay in registers between the two passes, over the maximum and over the
+// codes; what is beyond is read again.  A wave's loads are 64 bytes of 16 channels, its
+// stores 64 bytes of codes of 4 positions.
 template <class E>
-__global__ __launch_bounds__(256) void quantize_tile(Quantize<E> a) {
-    __shared__ uint32_t meet[4][32];
-    const int b = blockIdx.x / a.tiles, t0 = blockIdx.x % a.tiles * 32;
+constexpr int kTilePositions = 64 / (int)sizeof(typename E::type);
+
+template <class E, int KEPT>
+__global__ __launch_bounds__(1024) void quantize_tile(Quantize<E> a) {
+    using T = typename E::type;
+    constexpr int V = 16 / (int)sizeof(T), TT = 4 * V;
+    typedef typename Vec<T, V>::type Some;
+    __shared__ uint32_t meet[16][16];
+    const int id = gi::xcd_order(blockIdx.x, gridDim.x);
+    const int b = id / a.tiles, t0 = id % a.tiles * TT;
     const int len = length_of(a.lengths, b, a.L);
-    const int t = t0 + threadIdx.x % 4 * 8, quad = threadIdx.x / 4;
-    uint32_t most[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (t < len) {
-        for (int d = quad; d < a.D; d += 64) {
-            Octet<E> v;
-            v.load(a.x.row(b, d) + t, len - t);
+    const int group = threadIdx.x % 4, quad = threadIdx.x / 4, t = t0 + group * V;
+    const int left = len - t;
+    const auto load = [&](int d) {
+        Some v;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) most[k] = max(most[k], magnitude(v.at(k)));
+        for (int k = 0; k < V; ++k) v[k] = 0;
+        if (d < a.D && left > 0) {
+            const T *p = a.x.row(b, d) + t;
+            if (left >= V) {
+                v = *reinterpret_cast<const Some *>(p);
+            } else {
+                T u[V];
+                load_end(p, left, u);
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[k] = u[k];
+            }
         }
+        return v;
+    };
+    Some kept[KEPT][4];
+#pragma unroll
+    for (int r = 0; r < KEPT; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kept[r][j] = load(r * 1024 + quad * 4 + j);
+    // Four words of V positions each.
+    uint32_t words[4] = {0, 0, 0, 0};
+    const auto see = [&](const Some &v) {
+        const v4i bits = __builtin_bit_cast(v4i, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int word = bits[k];
+            words[k] = raise(words[k], word, E{});
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < KEPT; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) see(kept[r][j]);
+    for (int d = KEPT * 1024 + quad * 4; d < a.D; d += 1024) {
+        Some v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = load(d + j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) see(v[j]);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int s = 4; s < 64; s *= 2)
-            most[k] = max(most[k], (uint32_t)__shfl_xor((int)most[k], s, 64));
-    }
-    if (threadIdx.x % 64 < 4) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) meet[threadIdx.x / 64][threadIdx.x % 4 * 8 + k] = most[k];
+            words[k] = raise(words[k], (uint32_t)__shfl_xor((int)words[k], s, 64), E{});
+        if (threadIdx.x % 64 < 4) meet[threadIdx.x / 64][group * 4 + k] = words[k];
     }
     __syncthreads();
-    Coder c[8];
+    Coder c[V];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int p = threadIdx.x % 4 * 8 + k;
-        most[k] = max(max(meet[0][p], meet[1][p]), max(meet[2][p], meet[3][p]));
-        c[k] = coder(most[k]);
-        if (quad == 0 && t + k < a.L)
-            a.scales[(int64_t)b * a.L + t + k] = row_scale(most[k]);
-    }
-    for (int d = quad * 4; d < a.K; d += 256) {
-        Octet<E> v[4];
+    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j].zero();
-            if (d + j < a.D && t < len) v[j].load(a.x.row(b, d + j) + t, len - t);
+        for (int w = 0; w < 16; ++w) words[k] = raise(words[k], meet[w][group * 4 + k], E{});
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+            const int at = k * (V / 4) + h;
+            const uint32_t most = wide<E>(words[k] >> 16 * h);
+            c[at] = coder(most);
+            if (quad == 0 && t + at < a.L) a.scales[(int64_t)b * a.L + t + at] = row_scale(most);
         }
+    }
+    uint32_t *codes = a.codes + ((int64_t)b * a.L + t) * (a.K / 4);
+    const auto write = [&](int d, const Some (&v)[4]) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (t + k < a.L)
-                a.codes[((int64_t)b * a.L + t + k) * (a.K / 4) + d / 4] =
-                    pack(code<E>(v[0].at(k), c[k]), code<E>(v[1].at(k), c[k]),
-                         code<E>(v[2].at(k), c[k]), code<E>(v[3].at(k), c[k]));
+        for (int k = 0; k < V; ++k) {
+            uint32_t n[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const T e = v[j][k];
+                n[j] = code<E>(E::up(e), c[k]);
+            }
+            if (t + k < a.L) codes[k * (a.K / 4) + d / 4] = pack(n, c[k].keep);
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < KEPT; ++r) {
+        const int d = r * 1024 + quad * 4;
+        if (d < a.K) write(d, kept[r]);
+    }
+    for (int d = KEPT * 1024 + quad * 4; d < a.K; d += 1024) {
+        Some v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = load(d + j);
+        write(d, v);
     }
 }
 
@@ -146,7 +219,7 @@ __global__ __launch_bounds__(256) void quantize_row(Quantize<E> a) {
         Octet<E> v;
         v.load(x + d, D - d);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) most = max(most, magnitude(v.at(k)));
+        for (int k = 0; k < 8; ++k) most = raise(most, __builtin_bit_cast(uint32_t, v.at(k)), F32{});
     }
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) most = max(most, (uint32_t)__shfl_xor((int)most, s, 64));
@@ -158,22 +231,25 @@ __global__ __launch_bounds__(256) void quantize_row(Quantize<E> a) {
     for (int d = threadIdx.x * 8; d < a.K; d += 2048) {
         Octet<E> v;
         v.load(x + d, D - d);
-        int n[8];
+        uint32_t n[2][4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) n[k] = code<E>(v.at(k), c);
+        for (int k = 0; k < 8; ++k) n[k / 4][k % 4] = code<E>(v.at(k), c);
         uint2 *to = reinterpret_cast<uint2 *>(a.codes + ((int64_t)b * a.K + d) / 4);
-        *to = uint2{pack(n[0], n[1], n[2], n[3]), pack(n[4], n[5], n[6], n[7])};
+        *to = uint2{pack(n[0], c.keep), pack(n[1], c.keep)};
     }
 }
 
 template <class E>
 hipError_t quantize(const quantize_tokens_args &a, hipStream_t s) {
     Quantize<E> k{view<E>(a.x), static_cast<uint32_t *>(a.codes), a.scales, a.lengths,
-                  a.B, a.D, a.L, a.K, (a.L + 31) / 32};
-    if (a.L == 1 && (a.x.channel == 1 || a.D == 1))
+                  a.B, a.D, a.L, a.K, (a.L + kTilePositions<E> - 1) / kTilePositions<E>};
+    if (a.L == 1 && (a.x.channel == 1 || a.D == 1)) {
         quantize_row<E><<<(unsigned)a.B, 256, 0, s>>>(k);
-    else
-        quantize_tile<E><<<(unsigned)(a.B * (int64_t)k.tiles), 256, 0, s>>>(k);
+    } else {
+        const auto kernel = a.D <= 1024 ? quantize_tile<E, 1>
+                            : a.D <= 2048 ? quantize_tile<E, 2> : quantize_tile<E, 4>;
+        kernel<<<(unsigned)(a.B * (int64_t)k.tiles), 1024, 0, s>>>(k);
+    }
     return hipGetLastError();
 }
 

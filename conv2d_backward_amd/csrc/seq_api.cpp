@@ -21,7 +21,7 @@ constexpr int64_t kMaxPositions = (int64_t)1 << 26;
 constexpr int64_t kMaxBatchPositions = (int64_t)1 << 31;  // of all batch items; counted in 32 bits
 // A norm's work-groups have 1024 work-items at most, and a grid less than 2^32.
 constexpr int64_t kMaxNormTiles = (int64_t)1 << 22;
-constexpr int64_t kMaxCodeRows = (int64_t)1 << 23;
+constexpr int64_t kMaxCodeRows = (int64_t)1 << 22;
 constexpr int64_t kMaxProduct = (int64_t)1 << 35;  // elements of a product's result
 constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;  // work-items of a grid along one axis
 
@@ -88,8 +88,8 @@ bool is_apart(const seq_tensor &t, int64_t B, int64_t D, int64_t L) {
 
 int64_t int8_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ_INT8_ROW; }
 
-// Of a quantization.  A work-group has one position at least and 256 work-items, 1024 with more
-// positions.
+// Of a quantization.  A work-group has 1024 work-items at most and one position at least, and a
+// grid less than 2^32 work-items.
 int check_codes(int32_t dtype, int64_t B, int64_t D, int64_t L) {
     if (dtype != SEQ_F32 && dtype != SEQ_BF16 && dtype != SEQ_F16) return CONV2D_GI_EINVAL;
     if (B < 1 || D < 1 || L < 1) return CONV2D_GI_EINVAL;

@@ -53,7 +53,7 @@ enum { SEQ_F32 = 0, SEQ_BF16 = 1, SEQ_F16 = 2 };
    L <= 2^26, B*L < 2^31 (norms: about 2^27, block_norm_forward with 1025 .. 2048
    channels 2^26, in whole tiles of positions);
    of state_scan_backward also 2*B*G*N*(L+256) + D*(N+2) < 2^32 - 512;
-   of the 8-bit projections instead: D and K <= SEQ_MAX_INT8_CHANNELS, B*L < 2^23,
+   of the 8-bit projections instead: D and K <= SEQ_MAX_INT8_CHANNELS, B*L < 2^22,
    E < 2^24, B*L*E < 2^35. */
 enum { SEQ_MAX_TAPS = 8, SEQ_MAX_STATES = 256, SEQ_MAX_NORM_CHANNELS = 65536,
        SEQ_MAX_INT8_CHANNELS = 65536 };
