@@ -274,15 +274,46 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t *p, long by
 __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint8_t *lds, uint32_t at, int from) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds, 16, at, from, 0, 0);
 }
+// Until at most N of this wave's loads are on their way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ v16i mfma(v4i a, v4i b, v16i c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ v4i mfma16(v4i a, v4i b, v4i c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// Writes consecutive positions n .. n + V - 1 (n < N, counted over the batch) of channel e.
+template <class E, int V>
+__device__ __forceinline__ void store_positions(const Project<E> &a, int n, int e, float (&v)[V]) {
+    int b = n / a.L, l = n - b * a.L;
+    if (n + V <= a.N && l + V <= a.L) {
+        if (a.lengths) {
+            const int left = length_of(a.lengths, b, a.L) - l;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = left > k ? v[k] : 0.f;
+        }
+        store_vec<E, V>(a.y.row(b, e) + l, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if (n + k >= a.N) continue;
+            const bool in = l < length_of(a.lengths, b, a.L);
+            a.y.row(b, e)[l] = E::down(in ? v[k] : 0.f);
+            if (++l == a.L) l = 0, ++b;
+        }
+    }
+}
+
 // Tiles of TM positions and TE channels; waves in WM x WE, each with BM x BE blocks of
-// 32 x 32.  Stages of 128 bytes of k go to LDS by direct loads, one stage ahead.  In
+// 32 x 32.  Steps of 128 bytes of k go to LDS by direct loads, ST - 1 ahead.  In
 // LDS a row is eight 16-byte units, unit u at u ^ (row / 2 % 8): the 16 lanes that a
 // cycle of ds_read_b128 serves then read 16 different units of 256 bytes.
-template <class E, int WM, int WE, int BM, int BE>
+template <class E, int WM, int WE, int BM, int BE, int ST>
 __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
     constexpr int kThreads = 64 * WM * WE, TM = 32 * WM * BM, TE = 32 * WE * BE;
     constexpr int kLoads = (TM + TE) * 8 / kThreads, kStage = (TM + TE) * kStep;
@@ -336,12 +367,18 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
         // sums are consecutive positions.
         const int pos = col / 4 % 2 * 16 + col / 8 * 4 + col % 4;
         const int steps = a.K / kStep;
-        stage(0, 0);
-        for (int k = 0; k < steps; ++k) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < ST - 1; ++k)
+            if (k < steps) stage(k, k);
+        for (int k = 0, at = 0; k < steps; ++k, at = at + 1 < ST ? at + 1 : 0) {
+            // Step k is there: all but the ST - 2 behind it, or, at the end, all.
+            if (steps - k > ST - 2)
+                wait_loads<(ST - 2) * kLoads>();
+            else
+                wait_loads<0>();
             gi::lds_barrier();
-            if (k + 1 < steps) stage((k + 1) & 1, k + 1);
-            const uint8_t *x = smem + (k & 1) * kStage, *w = x + TM * kStep;
+            if (k + ST - 1 < steps) stage(at ? at - 1 : ST - 1, k + ST - 1);
+            const uint8_t *x = smem + at * kStage, *w = x + TM * kStep;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 v4i fx[BM], fw[BE];
@@ -369,8 +406,6 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
     for (int i = 0; i < BM; ++i) {
         const int n = n0 + (wm * BM + i) * 32 + half * 16;
         if (n >= a.N) continue;
-        int b = n / a.L, l = n - b * a.L;
-        const bool whole = n + 16 <= a.N && l + 16 <= a.L;
         float sx[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) sx[k] = a.scales[min(n + k, a.N - 1)];
@@ -385,74 +420,350 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
                 const int sum = acc[i][j][k];
                 v[k] = __builtin_fmaf((float)sum, sx[k] * sw, bias);
             }
-            if (whole) {
-                if (a.lengths) {
-                    const int left = length_of(a.lengths, b, a.L) - l;
+            store_positions<E, 16>(a, n, e, v);
+        }
+    }
+}
+
+template <class E>
+Project<E> project_of(const project_int8_args &a) {
+    return {static_cast<const uint8_t *>(a.codes), static_cast<const uint8_t *>(a.w), a.scales,
+            a.w_scales, a.bias, view<E>(a.y), a.lengths, (int)((int64_t)a.B * a.L), a.E, a.L, a.K, 0, 0};
+}
+
+template <class E, int WM, int WE, int BM, int BE, int ST>
+hipError_t product(const project_int8_args &a, hipStream_t s) {
+    constexpr int TM = 32 * WM * BM, TE = 32 * WE * BE;
+    Project<E> k = project_of<E>(a);
+    k.n_tiles = (k.N + TM - 1) / TM, k.e_tiles = (a.E + TE - 1) / TE;
+    constexpr int bytes = ST * (TM + TE) * kStep;
+    if (bytes > 64 * 1024) {
+        hipError_t e = hipFuncSetAttribute((const void *)project<E, WM, WE, BM, BE, ST>,
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    project<E, WM, WE, BM, BE, ST>
+        <<<(unsigned)((int64_t)k.n_tiles * k.e_tiles), 64 * WM * WE, bytes, s>>>(k);
+    return hipGetLastError();
+}
+
+// The largest of `lanes` (a power of two, 32 or 64) lanes, in each of them.
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lanes) {
+    const auto turned = [](uint32_t u, auto by) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, kRowRor + decltype(by)::value, 0xf, 0xf, true);
+    };
+    v = max(v, turned(v, std::integral_constant<int, 1>{}));
+    v = max(v, turned(v, std::integral_constant<int, 2>{}));
+    v = max(v, turned(v, std::integral_constant<int, 4>{}));
+    v = max(v, turned(v, std::integral_constant<int, 8>{}));
+    // Rows of 16 lanes.
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    const uint32_t low = max(a, b), high = max(c, d);
+    return lanes == 64 ? max(low, high) : threadIdx.x % 64 < 32 ? low : high;
+}
+
+// Products too small to fill the chip with whole rows of k: a work-group has RB blocks of 16
+// channels and NB of 16 positions, and its S waves share k by steps of 128 bytes, wave w with
+// every S-th; their sums meet in LDS.  Each wave brings its steps by direct loads through a
+// ring of DEPTH steps of its own, without a barrier: lanes 8 to a row, because loads straight
+// into operands (each lane another row) reach 9.4 TB/s from the caches where these reach 28.
+// Rows are swizzled as in `project`.
+//
+// What the results are laid out along decides which operand is the first: a lane has four
+// consecutive rows of it.  Along channels (one position a row), the weights.  Along
+// positions, the positions, in the order that gives a lane 4 NB consecutive ones.  With
+// codes inside (at most 16 positions, along channels) they are made here, from x, by every
+// work-group for itself, and wait in LDS, unit u of row r at u ^ r in each 256 bytes.
+enum Form { kAlongChannels, kCodesInside, kAlongPositions };
+
+template <class E>
+struct Split {
+    Project<E> p;
+    View<E> x;   // [N, D]
+    int D, share;
+};
+
+template <class E, int RB, int NB, int S, int DEPTH, int FORM>
+__global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
+    constexpr bool CODES = FORM == kCodesInside;
+    static_assert(!CODES || NB == 1, "the codes of 16 rows");
+    constexpr int ROWS = 16 * (RB + (CODES ? 0 : NB)), kLoads = ROWS / 8, kEntry = ROWS * kStep;
+    const Project<E> &a = t.p;
+    extern __shared__ uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    constexpr int kRing = DEPTH * kEntry, kMeet = RB * NB * 1024;   // bytes of a wave
+    uint8_t *const ring = smem + wave * kRing;
+    v4i *const meet = reinterpret_cast<v4i *>(smem);   // after the rings
+    float *const own_scales = reinterpret_cast<float *>(smem + S * (kRing > kMeet ? kRing : kMeet));
+    uint8_t *const own = reinterpret_cast<uint8_t *>(own_scales + 64);   // [16][pitch]
+    const int pitch = (a.K + 255) / 256 * 256;
+    // Work-groups of the same positions or, where there are more of those, channels follow
+    // each other on one die.
+    const int id = gi::xcd_order(blockIdx.x, gridDim.x);
+    const int e0 = id % a.e_tiles * RB * 16, n0 = id / a.e_tiles * NB * 16;
+    const int row = lane % 16, part = lane / 16;
+    const int steps = a.K / kStep;
+    // Work-groups start at different places, so that rows a power of two apart do not all
+    // come from the same channel of the caches (1 position, 4096 x 4096: 5.7 -> 5.2 us).
+    const int turn = id % steps;
+    const int mine = (steps - wave + S - 1) / S;   // steps of this wave
+    const auto place = [&](int j) {
+        const int k = wave + j * S + turn;
+        return k < steps ? k : k - steps;
+    };
+
+    // Codes inside: a row of x has `share` threads, a power of two; its numbers are on their
+    // way before the weights.
+    constexpr int KEPT = CODES ? 8 : 1;   // octets of a thread that stay in registers
+    const int share = t.share, own_row = tid / share, first = tid % share * 8;
+    const auto load = [&](int d) {
+        Octet<E> v;
+        if (t.x.channel == 1) {
+            v.load(t.x.row(own_row, 0) + d, t.D - d);
+        } else {
+            v.zero();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = left > k ? v[k] : 0.f;
+            for (int k = 0; k < 8; ++k)
+                if (d + k < t.D) v.v[k] = *t.x.row(own_row, d + k);
+        }
+        return v;
+    };
+    Octet<E> kept[KEPT];
+    const int end = CODES && own_row < a.N ? t.D : 0;
+    if constexpr (CODES) {
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i) {
+            kept[i].zero();
+            if (first + i * share * 8 < end) kept[i] = load(first + i * share * 8);
+        }
+    }
+
+    const auto wr = rsrc(a.w + (int64_t)e0 * a.K, (long)min(16 * RB, a.E_ - e0) * a.K);
+    const auto xr = rsrc(a.codes + (CODES ? 0 : (int64_t)n0 * a.K),
+                         CODES ? 0 : (long)min(16 * NB, a.N - n0) * a.K);
+    uint32_t from[kLoads];
+#pragma unroll
+    for (int p = 0; p < kLoads; ++p) {
+        const int r = p * 8 + lane / 8, unit = lane % 8 ^ (r / 2 % 8);
+        const int held = r < 16 * RB ? min(r, a.E_ - e0 - 1) : min(r - 16 * RB, a.N - n0 - 1);
+        from[p] = held * a.K + unit * 16;
+    }
+    const auto bring = [&](int j) {
+#pragma unroll
+        for (int p = 0; p < kLoads; ++p)
+            load_lds(p < 2 * RB ? wr : xr, ring + j % DEPTH * kEntry + p * 1024, from[p],
+                     place(j) * kStep);
+    };
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j)
+        if (j < mine) bring(j);
+
+    if constexpr (CODES) {
+        uint32_t most = 0;
+        const auto see = [&](const Octet<E> &v) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                most = raise(most, __builtin_bit_cast(uint32_t, v.at(k)), F32{});
+        };
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i) see(kept[i]);
+        for (int d = first + KEPT * share * 8; d < end; d += share * 8) see(load(d));
+        most = lanes_max(most, share < 64 ? share : 64);
+        if (share > 64) {
+            uint32_t *const parts = reinterpret_cast<uint32_t *>(own_scales + 16);
+            if (lane == 0) parts[wave] = most;
+            gi::lds_barrier();
+            for (int w = 0; w < share / 64; ++w) most = max(most, parts[tid / share * (share / 64) + w]);
+        }
+        const Coder c = coder(most);
+        if (first == 0) own_scales[own_row] = row_scale(most);
+        const auto write = [&](int d, const Octet<E> &v) {
+            uint32_t q[2][4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) q[k / 4][k % 4] = code<E>(v.at(k), c);
+            *reinterpret_cast<uint2 *>(own + own_row * pitch + ((d / 16) ^ own_row) * 16 + d % 16) =
+                uint2{pack(q[0], c.keep), pack(q[1], c.keep)};
+        };
+        const int bytes = own_row < a.N ? a.K : 0;
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i)
+            if (first + i * share * 8 < bytes) write(first + i * share * 8, kept[i]);
+        for (int d = first + KEPT * share * 8; d < bytes; d += share * 8) write(d, load(d));
+        gi::lds_barrier();
+    }
+
+    v4i acc[RB][NB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[r][n] = v4i{0, 0, 0, 0};
+    // Along positions, row r of block n is position r / 4 * 4 NB + n * 4 + r % 4.
+    const int x_row = FORM == kAlongPositions ? row / 4 * 4 * NB + row % 4 : row;
+    for (int j = 0; j < mine; ++j) {
+        // Step j is there: all but the DEPTH - 1 behind it, or, at the end, all.
+        if (mine - j >= DEPTH)
+            wait_loads<(DEPTH - 1) * kLoads>();
+        else
+            wait_loads<0>();
+        const uint8_t *at = ring + j % DEPTH * kEntry;
+        v4i fw[RB][2], fx[NB][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int u = h * 4 + part;
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                fw[r][h] = *reinterpret_cast<const v4i *>(at + (r * 16 + row) * kStep +
+                                                          (u ^ (row / 2 % 8)) * 16);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const int xn = x_row + n * (FORM == kAlongPositions ? 4 : 16);
+                fx[n][h] = *reinterpret_cast<const v4i *>(
+                    CODES ? own + row * pitch + ((place(j) * 8 + u) ^ row) * 16
+                          : at + (RB * 16 + xn) * kStep + (u ^ (xn / 2 % 8)) * 16);
+            }
+        }
+        if (j + DEPTH < mine) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the ring's place is read
+            bring(j + DEPTH);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    acc[r][n] = FORM == kAlongPositions ? mfma16(fx[n][h], fw[r][h], acc[r][n])
+                                                        : mfma16(fw[r][h], fx[n][h], acc[r][n]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) meet[((r * NB + n) * S + wave) * 64 + lane] = acc[r][n];
+    __syncthreads();
+    const auto sum_of = [&](int block) {
+        v4i sum = meet[block * S * 64 + lane];
+#pragma unroll
+        for (int s = 1; s < S; ++s) sum += meet[(block * S + s) * 64 + lane];
+        return sum;
+    };
+    if constexpr (FORM == kAlongPositions) {
+        for (int r = wave; r < RB; r += S) {
+            const int e = e0 + r * 16 + row, n = n0 + part * 4 * NB;
+            if (e >= a.E_ || n >= a.N) continue;
+            float v[4 * NB];
+            const float sw = a.w_scales[e], bias = a.bias ? a.bias[e] : 0.f;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const v4i sum = sum_of(r * NB + i);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int one = sum[k];
+                    v[4 * i + k] = __builtin_fmaf(
+                        (float)one, a.scales[min(n + 4 * i + k, a.N - 1)] * sw, bias);
                 }
-                store_vec<E, 16>(a.y.row(b, e) + l, v);
+            }
+            store_positions<E, 4 * NB>(a, n, e, v);
+        }
+    } else {
+        for (int block = wave; block < RB * NB; block += S) {
+            const int n = n0 + block % NB * 16 + lane % 16;
+            const int e = e0 + block / NB * 16 + lane / 16 * 4;
+            if (n >= a.N || e >= a.E_) continue;
+            const v4i sum = sum_of(block);
+            const int b = n / a.L, l = n - b * a.L;
+            const bool in = l < length_of(a.lengths, b, a.L);
+            const float sx = CODES ? own_scales[n] : a.scales[n];
+            auto *y = a.y.row(b, e) + l;
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int ek = min(e + k, a.E_ - 1), one = sum[k];
+                v[k] = __builtin_fmaf((float)one, sx * a.w_scales[ek], a.bias ? a.bias[ek] : 0.f);
+                v[k] = in ? v[k] : 0.f;
+            }
+            if (a.y.channel == 1 && e + 4 <= a.E_) {
+                store_vec<E, 4>(y, v);
             } else {
-                int bk = b, lk = l;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    if (n + k >= a.N) continue;
-                    const bool in = lk < length_of(a.lengths, bk, a.L);
-                    a.y.row(bk, e)[lk] = E::down(in ? v[k] : 0.f);
-                    if (++lk == a.L) lk = 0, ++bk;
-                }
+                for (int k = 0; k < 4; ++k)
+                    if (e + k < a.E_) y[k * a.y.channel] = E::down(v[k]);
             }
         }
     }
 }
 
-template <class E, int WM, int WE, int BM, int BE>
-hipError_t product(const project_int8_args &a, hipStream_t s) {
-    constexpr int TM = 32 * WM * BM, TE = 32 * WE * BE;
-    const int64_t N = (int64_t)a.B * a.L;
-    Project<E> k{static_cast<const uint8_t *>(a.codes), static_cast<const uint8_t *>(a.w), a.scales,
-                 a.w_scales, a.bias, view<E>(a.y), a.lengths, (int)N, a.E, a.L, a.K,
-                 (int)((N + TM - 1) / TM), (a.E + TE - 1) / TE};
-    constexpr int bytes = 2 * (TM + TE) * kStep;
+template <class E, int RB, int NB, int S, int DEPTH, int FORM>
+hipError_t split(const project_int8_args &a, const seq_tensor &x, int D, hipStream_t s) {
+    constexpr bool CODES = FORM == kCodesInside;
+    Split<E> k{project_of<E>(a), view<E>(x), D, 64 * S / 16};
+    k.p.n_tiles = (k.p.N + 16 * NB - 1) / (16 * NB), k.p.e_tiles = (a.E + 16 * RB - 1) / (16 * RB);
+    if constexpr (CODES)
+        while (k.share < 64 * S && 64 * S / k.share / 2 >= k.p.N) k.share *= 2;
+    constexpr int kRing = DEPTH * 16 * (RB + (CODES ? 0 : NB)) * kStep, kMeet = RB * NB * 1024;
+    const int bytes = S * std::max(kRing, kMeet) + 256 + (CODES ? 16 * ((a.K + 255) / 256 * 256) : 0);
     if (bytes > 64 * 1024) {
-        hipError_t e = hipFuncSetAttribute((const void *)project<E, WM, WE, BM, BE>,
+        hipError_t e = hipFuncSetAttribute((const void *)project_split<E, RB, NB, S, DEPTH, FORM>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    project<E, WM, WE, BM, BE>
-        <<<(unsigned)((int64_t)k.n_tiles * k.e_tiles), 64 * WM * WE, bytes, s>>>(k);
+    project_split<E, RB, NB, S, DEPTH, FORM>
+        <<<(unsigned)((int64_t)k.p.n_tiles * k.p.e_tiles), 64 * S, bytes, s>>>(k);
     return hipGetLastError();
+}
+
+template <class E, int FORM>
+hipError_t split_any(const project_int8_args &a, hipStream_t s) {
+    const int64_t N = (int64_t)a.B * a.L;
+    if (N <= 16) return a.E > 4096 ? split<E, 2, 1, 8, 2, FORM>(a, {}, 0, s) : split<E, 1, 1, 8, 2, FORM>(a, {}, 0, s);
+    if (N <= 32) return a.E > 4096 ? split<E, 2, 2, 8, 1, FORM>(a, {}, 0, s) : split<E, 1, 2, 8, 1, FORM>(a, {}, 0, s);
+    if (N <= 64 && a.E <= 2048) return split<E, 1, 2, 8, 2, FORM>(a, {}, 0, s);
+    return split<E, 2, 4, 8, 1, FORM>(a, {}, 0, s);
 }
 
 template <class E>
 hipError_t product_any(const project_int8_args &a, hipStream_t s) {
     const int64_t N = (int64_t)a.B * a.L;
     const auto tiles = [&](int64_t t) { return (N + t - 1) / t * ((a.E + t - 1) / t); };
-    if (tiles(256) >= 192) return product<E, 2, 4, 4, 2>(a, s);
-    if (tiles(128) >= 192) return product<E, 2, 2, 2, 2>(a, s);
-    return product<E, 2, 2, 1, 1>(a, s);
+    if (N <= 64 || tiles(64) <= 128)
+        return a.L == 1 ? split_any<E, kAlongChannels>(a, s) : split_any<E, kAlongPositions>(a, s);
+    if (tiles(256) >= 192) return product<E, 2, 4, 4, 2, 2>(a, s);
+    if (tiles(128) >= 192) return product<E, 2, 4, 2, 1, 2>(a, s);
+    return product<E, 2, 2, 1, 1, 3>(a, s);
 }
 
 int64_t code_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ_INT8_ROW; }
 
+// Whether every work-group makes the codes of a single-position call for itself: at most 16
+// rows, few enough numbers, and room in LDS for their codes.
+bool codes_inside(int64_t B, int64_t D) {
+    return B <= 16 && B * D <= 32768 && D <= 8192;
+}
+
 template <class E>
 hipError_t step(const project_int8_step_args &a, hipStream_t s) {
+    project_int8_args p = {};
+    p.dtype = a.dtype, p.B = a.B, p.E = a.E, p.L = 1, p.K = a.K;
+    p.w = a.w, p.w_scales = a.w_scales, p.bias = a.bias, p.y = a.y;
+    if (codes_inside(a.B, a.D))
+        return a.E > 4096 ? split<E, 2, 1, 8, 2, kCodesInside>(p, a.x, a.D, s)
+                          : split<E, 1, 1, 8, 2, kCodesInside>(p, a.x, a.D, s);
     quantize_tokens_args q = {};
     q.dtype = a.dtype, q.B = a.B, q.D = a.D, q.L = 1, q.K = a.K, q.x = a.x;
     q.codes = a.workspace;
     q.scales = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + (int64_t)a.B * a.K);
     hipError_t e = quantize<E>(q, s);
     if (e != hipSuccess) return e;
-    project_int8_args p = {};
-    p.dtype = a.dtype, p.B = a.B, p.E = a.E, p.L = 1, p.K = a.K;
-    p.codes = q.codes, p.scales = q.scales, p.w = a.w, p.w_scales = a.w_scales, p.bias = a.bias;
-    p.y = a.y;
+    p.codes = q.codes, p.scales = q.scales;
     return product_any<E>(p, s);
 }
 
 }  // namespace
 
-int64_t project_step_workspace(int B, int D, int) { return B * (code_row(D) + (int64_t)sizeof(float)); }
+int64_t project_step_workspace(int B, int D) {
+    return codes_inside(B, D) ? 0 : B * (code_row(D) + (int64_t)sizeof(float));
+}
 
 hipError_t launch_quantize(const quantize_tokens_args &a, hipStream_t s) {
     return a.dtype == SEQ_F32 ? quantize<F32>(a, s)
