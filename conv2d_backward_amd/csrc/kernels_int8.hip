@@ -18,7 +18,6 @@ namespace seq {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v16i __attribute__((ext_vector_type(16)));
 
 // ---- codes ---------------------------------------------------------------------------------------
 
@@ -274,13 +273,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t *p, long by
 __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint8_t *lds, uint32_t at, int from) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds, 16, at, from, 0, 0);
 }
+// 4 bytes a lane.
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t *lds, uint32_t at) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds, 4, at, 0, 0, 0);
+}
 // Until at most N of this wave's loads are on their way.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ v16i mfma(v4i a, v4i b, v16i c) {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
 }
 
 __device__ __forceinline__ v4i mfma16(v4i a, v4i b, v4i c) {
@@ -309,23 +309,52 @@ __device__ __forceinline__ void store_positions(const Project<E> &a, int n, int 
     }
 }
 
-// Tiles of TM positions and TE channels; waves in WM x WE, each with BM x BE blocks of
-// 32 x 32.  Steps of 128 bytes of k go to LDS by direct loads, ST - 1 ahead.  In
-// LDS a row is eight 16-byte units, unit u at u ^ (row / 2 % 8): the 16 lanes that a
-// cycle of ds_read_b128 serves then read 16 different units of 256 bytes.
-template <class E, int WM, int WE, int BM, int BE, int ST>
+// 16 bytes of results.
+template <class E>
+__device__ __forceinline__ uint4 packed(const float *v) {
+    uint4 o;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(typename E::type) == 4)
+            w[k] = __builtin_bit_cast(uint32_t, E::down(v[k]));
+        else
+            w[k] = (uint32_t)E::down(v[2 * k]) | (uint32_t)E::down(v[2 * k + 1]) << 16;
+    }
+    o.x = w[0], o.y = w[1], o.z = w[2], o.w = w[3];
+    return o;
+}
+// f(row) for positions, and for channels row / 2 % 8 (above `project`).
+template <int NB>
+__device__ __forceinline__ int position_turn(int row) {
+    return row / 2 % 2 + row / (4 * NB) % 4 * 2;
+}
+
+// Tiles of positions by channels; waves in WM x WE, each with NB x RB blocks of 16 x 16.
+// (The 16 x 16 x 64 product: on numbers that use all bits the chip's power holds it to 4.2
+// POP/s where 32 x 32 x 32 is held to 3.4; on zeros both reach 4.9.)  Steps of 128 bytes of
+// k go to LDS by direct loads, ST of them there or on their way.  A step is two halves of
+// 64 bytes; the operands of a half are read while the products of the one before run, and
+// the barrier that hands over a step lies between the halves, so that the matrix cores have
+// work across it.
+//
+// In LDS a row is eight 16-byte units, unit u at u ^ f(row), so that the 16 lanes that a
+// cycle of ds_read_b128 serves (rows 0..3 and 12..15 of one unit, 4..11 of its neighbour, or
+// the others) read 16 different units of 256 bytes.  Row r of block n of the positions is
+// position r / 4 * 4 NB + n * 4 + r % 4 of the wave's, which gives a lane 4 NB consecutive ones.
+template <class E, int WM, int WE, int NB, int RB, int ST>
 __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
-    constexpr int kThreads = 64 * WM * WE, TM = 32 * WM * BM, TE = 32 * WE * BE;
+    constexpr int kThreads = 64 * WM * WE, TM = 16 * WM * NB, TE = 16 * WE * RB;
     constexpr int kLoads = (TM + TE) * 8 / kThreads, kStage = (TM + TE) * kStep;
     static_assert((TM + TE) * 8 % kThreads == 0 && TM * 8 % kThreads == 0, "whole rounds of loads");
     extern __shared__ uint8_t smem[];
-    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int id = gi::xcd_order(blockIdx.x, gridDim.x);
     // Eight tiles of positions by the tiles of channels, then the next eight.
     const int band = id / (8 * a.e_tiles), in_band = id - band * 8 * a.e_tiles;
     const int wide = min(8, a.n_tiles - band * 8);
     const int n0 = (band * 8 + in_band % wide) * TM, e0 = in_band / wide * TE;
-    const int wm = wave % WM, we = wave / WM, half = lane / 32, col = lane % 32;
+    const int wm = wave % WM, we = wave / WM, row = lane % 16, part = lane / 16;
 
     bool any = a.lengths == nullptr;
     if (a.lengths) {
@@ -336,26 +365,23 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
         any = __syncthreads_or(any);
     }
 
-    v16i acc[BM][BE];
+    v4i acc[RB][NB];
 #pragma unroll
-    for (int i = 0; i < BM; ++i)
+    for (int r = 0; r < RB; ++r)
 #pragma unroll
-        for (int j = 0; j < BE; ++j)
-#pragma unroll
-            for (int k = 0; k < 16; ++k) acc[i][j][k] = 0;
+        for (int n = 0; n < NB; ++n) acc[r][n] = v4i{0, 0, 0, 0};
 
     if (any) {
-        // Each thread's share of a stage: unit tid + p kThreads, at the same offset in every
-        // stage.  Rows past the end are the last one again.
+        // Each thread's share of a step: unit tid + p kThreads, at the same offset in every
+        // step.  Rows past the end are the last one again.
         uint32_t from[kLoads];
-        const uint8_t *x0 = a.codes + (int64_t)n0 * a.K, *w0 = a.w + (int64_t)e0 * a.K;
-        const __amdgpu_buffer_rsrc_t xr = rsrc(x0, (long)min(TM, a.N - n0) * a.K);
-        const __amdgpu_buffer_rsrc_t wr = rsrc(w0, (long)min(TE, a.E_ - e0) * a.K);
+        const auto xr = rsrc(a.codes + (int64_t)n0 * a.K, (long)min(TM, a.N - n0) * a.K);
+        const auto wr = rsrc(a.w + (int64_t)e0 * a.K, (long)min(TE, a.E_ - e0) * a.K);
 #pragma unroll
         for (int p = 0; p < kLoads; ++p) {
-            const int unit = tid + p * kThreads, row = unit / 8 % (TM + TE);
-            const int r = row < TM ? min(row, a.N - n0 - 1) : min(row - TM, a.E_ - e0 - 1);
-            from[p] = r * a.K + (unit % 8 ^ (row / 2 % 8)) * 16;
+            const int r = (tid + p * kThreads) / 8, unit = tid % 8;
+            from[p] = r < TM ? min(r, a.N - n0 - 1) * a.K + (unit ^ position_turn<NB>(r)) * 16
+                             : min(r - TM, a.E_ - e0 - 1) * a.K + (unit ^ r / 2 % 8) * 16;
         }
         const auto stage = [&](int to, int k) {
             uint8_t *lds = smem + to * kStage + wave * 1024;
@@ -363,65 +389,335 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
             for (int p = 0; p < kLoads; ++p)
                 load_lds(p * kThreads < TM * 8 ? xr : wr, lds + p * kThreads * 16, from[p], k * kStep);
         };
-        // A block's row r holds position r / 4 % 2 * 16 + r / 8 * 4 + r % 4, so that a lane's 16
-        // sums are consecutive positions.
-        const int pos = col / 4 % 2 * 16 + col / 8 * 4 + col % 4;
+        // Half h of this lane's rows of block 0; block n of the positions is 512 bytes on,
+        // block r of the channels 2048.
+        const int x_row = wm * 16 * NB + row / 4 * 4 * NB + row % 4, w_row = we * 16 * RB + row;
+        const int x_at = x_row * kStep + (part ^ position_turn<NB>(x_row)) * 16;
+        const int w_at = (TM + w_row) * kStep + (part ^ w_row / 2 % 8) * 16;
+        struct Operands {
+            v4i x[NB], w[RB];
+        };
+        const auto read = [&](Operands &o, int at, int h) {
+            const uint8_t *x = smem + at * kStage + (x_at ^ h * 64), *w = smem + at * kStage + (w_at ^ h * 64);
+#pragma unroll
+            for (int r = 0; r < RB; ++r) o.w[r] = *reinterpret_cast<const v4i *>(w + r * 2048);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) o.x[n] = *reinterpret_cast<const v4i *>(x + n * 512);
+        };
+        const auto multiply = [&](const Operands &o) {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) acc[r][n] = mfma16(o.x[n], o.w[r], acc[r][n]);
+            __builtin_amdgcn_s_setprio(0);
+        };
         const int steps = a.K / kStep;
 #pragma unroll
-        for (int k = 0; k < ST - 1; ++k)
+        for (int k = 0; k < ST; ++k)
             if (k < steps) stage(k, k);
-        for (int k = 0, at = 0; k < steps; ++k, at = at + 1 < ST ? at + 1 : 0) {
-            // Step k is there: all but the ST - 2 behind it, or, at the end, all.
-            if (steps - k > ST - 2)
+        if (steps >= ST)
+            wait_loads<(ST - 1) * kLoads>();
+        else
+            wait_loads<0>();
+        gi::lds_barrier();
+        Operands first, second;
+        read(first, 0, 0);
+        for (int k = 0, at = 0; k < steps; ++k) {
+            const int next = at + 1 < ST ? at + 1 : 0;
+            read(second, at, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(first);
+            __builtin_amdgcn_sched_barrier(0);
+            // Step k + 1 is there (all but the ST - 2 behind it, or, at the end, all), and
+            // everyone has read step k.
+            if (steps - k > ST - 1)
                 wait_loads<(ST - 2) * kLoads>();
             else
                 wait_loads<0>();
             gi::lds_barrier();
-            if (k + ST - 1 < steps) stage(at ? at - 1 : ST - 1, k + ST - 1);
-            const uint8_t *x = smem + at * kStage, *w = x + TM * kStep;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                v4i fx[BM], fw[BE];
-                const int u = kk * 2 + half;
-#pragma unroll
-                for (int i = 0; i < BM; ++i) {
-                    const int row = (wm * BM + i) * 32 + pos;
-                    fx[i] = *reinterpret_cast<const v4i *>(x + row * kStep + (u ^ (row / 2 % 8)) * 16);
-                }
-#pragma unroll
-                for (int j = 0; j < BE; ++j) {
-                    const int row = (we * BE + j) * 32 + col;
-                    fw[j] = *reinterpret_cast<const v4i *>(w + row * kStep + (u ^ (row / 2 % 8)) * 16);
-                }
-#pragma unroll
-                for (int i = 0; i < BM; ++i)
-#pragma unroll
-                    for (int j = 0; j < BE; ++j)
-                        acc[i][j] = mfma(fx[i], fw[j], acc[i][j]);
-            }
+            if (k + 1 < steps) read(first, next, 0);
+            if (k + ST < steps) stage(at, k + ST);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(second);
+            __builtin_amdgcn_sched_barrier(0);
+            at = next;
         }
     }
 
+    const int n = n0 + wm * 16 * NB + part * 4 * NB;
+    if (n >= a.N) return;
 #pragma unroll
-    for (int i = 0; i < BM; ++i) {
-        const int n = n0 + (wm * BM + i) * 32 + half * 16;
-        if (n >= a.N) continue;
-        float sx[16];
+    for (int i = 0; i < NB; i += 4 < NB ? 4 : NB) {
+        constexpr int V = NB < 4 ? 4 * NB : 16;   // positions stored at once
+        const int m = n + 4 * i;
+        if (m >= a.N) continue;
+        float sx[V];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) sx[k] = a.scales[min(n + k, a.N - 1)];
+        for (int k = 0; k < V; ++k) sx[k] = a.scales[min(m + k, a.N - 1)];
 #pragma unroll
-        for (int j = 0; j < BE; ++j) {
-            const int e = e0 + (we * BE + j) * 32 + col;
+        for (int r = 0; r < RB; ++r) {
+            const int e = e0 + (we * RB + r) * 16 + row;
             if (e >= a.E_) continue;
             const float sw = a.w_scales[e], bias = a.bias ? a.bias[e] : 0.f;
+            float v[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int sum = acc[r][i + k / 4][k % 4];
+                v[k] = __builtin_fmaf((float)sum, sx[k] * sw, bias);
+            }
+            store_positions<E, V>(a, m, e, v);
+        }
+    }
+}
+
+// The same for products that fill the chip: tiles of 256 x 256, one work-group a compute
+// unit, which goes through its tiles as one stream of steps: the first steps of the next tile
+// are on their way before the last products of this one, and the results leave while they
+// come.  A tile by a work-group of its own takes 14.6 us beside its steps ([1, 4096, 8192] x
+// 8192: 250 us in all).  The results of 16 channels at a time turn in LDS, so that a store
+// writes whole lines (16-bit results; float32's leave as they lie).
+constexpr int kStreamWM = 4, kStreamWE = 2, kStreamNB = 4, kStreamRB = 8;
+constexpr int kStreamTile = 256, kStreamWaves = kStreamWM * kStreamWE;
+constexpr int kStreamStage = 2 * kStreamTile * kStep;
+// LDS: two steps, two sets of the tile's scales and biases, 2 KB a wave for results.
+constexpr int kStreamScales = 2 * kStreamStage, kStreamTurn = kStreamScales + 2 * 4096;
+constexpr int kStreamBytes = kStreamTurn + kStreamWaves * 2048;
+
+template <class E>
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E> a) {
+    constexpr int NB = kStreamNB, RB = kStreamRB, TM = kStreamTile, TE = kStreamTile;
+    constexpr int kThreads = 64 * kStreamWaves, kLoads = (TM + TE) * 8 / kThreads;
+    using T = typename E::type;
+    constexpr int kStores = RB * 64 * (int)sizeof(T) / 64;   // of a wave and whole tile
+    extern __shared__ uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int wm = wave % kStreamWM, we = wave / kStreamWM, row = lane % 16, part = lane / 16;
+    const int tiles = a.n_tiles * a.e_tiles, steps = a.K / kStep;
+
+    struct Tile {
+        int n0, e0;
+        bool any;   // a position inside a length
+    };
+    const auto tile_of = [&](int number) {
+        const int id = gi::xcd_order(number, tiles);
+        const int band = id / (8 * a.e_tiles), in_band = id - band * 8 * a.e_tiles;
+        const int wide = min(8, a.n_tiles - band * 8);
+        Tile t{(band * 8 + in_band % wide) * TM, in_band / wide * TE, true};
+        if (a.lengths) {
+            bool any = false;
+#pragma unroll 1
+            for (int i = 0; i < TM; i += 64) {
+                const int n = t.n0 + i + lane, b = min(n, a.N - 1) / a.L;
+                any = any || (n < a.N && n - b * a.L < length_of(a.lengths, b, a.L));
+            }
+            t.any = __any(any);
+        }
+        return t;
+    };
+
+    // Each thread's share of a step: unit tid + p kThreads, 64 rows on each time (which turns
+    // the units no further).  Rows past the end are past the resource, and come as zeros.
+    __amdgpu_buffer_rsrc_t xr, wr;
+    const auto aim = [&](const Tile &t) {
+        xr = rsrc(a.codes + (int64_t)t.n0 * a.K, t.any ? (long)min(TM, a.N - t.n0) * a.K : 0);
+        wr = rsrc(a.w + (int64_t)t.e0 * a.K, t.any ? (long)min(TE, a.E_ - t.e0) * a.K : 0);
+    };
+    uint32_t x_from = tid / 8 * a.K + (tid % 8 ^ position_turn<NB>(tid / 8)) * 16;
+    uint32_t w_from = tid / 8 * a.K + (tid % 8 ^ tid / 16 % 8) * 16;
+    // Load p of a step's kLoads.
+    const auto load_one = [&](int to, int k, int p) {
+        uint8_t *lds = smem + to * kStreamStage + wave * 1024 + p * kThreads * 16;
+        const int rows = p % (kLoads / 2) * 64;
+        if (p < kLoads / 2)
+            load_lds(xr, lds, x_from + rows * a.K, k * kStep);
+        else
+            load_lds(wr, lds, w_from + rows * a.K, k * kStep);
+    };
+    const auto stage = [&](int to, int k) {
+#pragma unroll
+        for (int p = 0; p < kLoads; ++p) load_one(to, k, p);
+    };
+    // Scales of the positions, scales of the channels, biases: 256 floats each, 64 a load and
+    // two loads a wave (a fourth part is loaded in vain); what is past the end is 0.
+    const auto stage_scales = [&](int to, const Tile &t) {
+        const int which = wave / 2;
+        const float *p = which == 0 ? a.scales + t.n0 : which == 1 || !a.bias ? a.w_scales + t.e0 : a.bias + t.e0;
+        const int held = which == 0 ? min(TM, a.N - t.n0) : which == 1 || (which == 2 && a.bias) ? min(TE, a.E_ - t.e0) : 0;
+        const auto r = rsrc(reinterpret_cast<const uint8_t *>(p), held * 4L);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int first = wave % 2 * 128 + i * 64;
+            load_lds4(r, smem + kStreamScales + to * 4096 + which * 1024 + first * 4, (first + lane) * 4);
+        }
+    };
+
+    // Half h of this lane's rows of block 0; block n of the positions is 512 bytes on, block r
+    // of the channels 2048.
+    const int x_row = wm * 16 * NB + row / 4 * 4 * NB + row % 4, w_row = we * 16 * RB + row;
+    const int x_at = x_row * kStep + (part ^ position_turn<NB>(x_row)) * 16;
+    const int w_at = (TM + w_row) * kStep + (part ^ w_row / 2 % 8) * 16;
+    struct Operands {
+        v4i x[NB], w[RB];
+    };
+    // Read i of a half's NB + RB.
+    const auto read_one = [&](Operands &o, int at, int h, int i) {
+        if (i < NB)
+            o.x[i] = *reinterpret_cast<const v4i *>(smem + at * kStreamStage + (x_at ^ h * 64) + i * 512);
+        else
+            o.w[i - NB] = *reinterpret_cast<const v4i *>(smem + at * kStreamStage + (w_at ^ h * 64) +
+                                                         (i - NB) * 2048);
+    };
+    v4i acc[RB][NB];
+    // The products of a half.  Among them, a few apart, go the reads of the half after it and,
+    // LOAD, the loads of a step: all at once they would fill the queues in front of the LDS and
+    // the caches, and the products behind them would wait ([1, 4096, 8192] x 8192 in steps of
+    // 1.6 us for 1.4).
+    const auto multiply = [&](const Operands &o, Operands &fill, int from, int h, auto load, int to, int k) {
+        constexpr bool LOAD = decltype(load)::value;
+        if constexpr (LOAD) asm volatile("" : "+v"(x_from), "+v"(w_from));   // (opaque: nothing kept)
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < RB * NB; ++i) {
+            acc[i / NB][i % NB] = mfma16(o.x[i % NB], o.w[i / NB], acc[i / NB][i % NB]);
+            if (i % 2 == 1 && i / 2 < NB + RB) read_one(fill, from, h, i / 2);
+            if (LOAD && i % 4 == 2) load_one(to, k, i / 4);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+    };
+    static_assert(RB * NB / 2 >= NB + RB && RB * NB / 4 == kLoads, "a place for every read and load");
+
+    // Tiles without a position inside a length have no products: they are written here.
+    const auto empty = [&](const Tile &t) {
+        const int n = t.n0 + wave % 4 * 64 + lane, b = min(n, a.N - 1) / a.L;
+        T *y = a.y.row(b, t.e0) + (n - b * a.L);
+#pragma unroll 1
+        for (int c = wave / 4; c < min(TE, a.E_ - t.e0); c += 2)
+            if (n < a.N) y[c * a.y.channel] = 0;
+    };
+    int number = blockIdx.x;
+    const auto following = [&](Tile &t) {   // the next tile with products
+        for (; number < tiles; number += gridDim.x) {
+            t = tile_of(number);
+            if (t.any) {
+                number += gridDim.x;
+                return true;
+            }
+            empty(t);
+        }
+        return false;
+    };
+
+    Tile now;
+    if (!following(now)) return;
+    aim(now);
+    stage_scales(0, now);
+    stage(0, 0);
+    stage(1, 1);
+    wait_loads<kLoads>();
+    gi::lds_barrier();
+    Operands first, second;
+    int at = 0, set = 0;
+    bool whole_stores = false;   // whether the tile before has left in exactly kStores stores
+    for (bool more = true; more;) {
+        Tile next{0, 0, false};
+        more = following(next);
+        next.any = more;
+#pragma unroll
+        for (int i = 0; i < NB + RB; ++i) read_one(first, at, 0, i);
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) acc[r][n] = v4i{0, 0, 0, 0};
+#pragma clang loop unroll(disable)
+        for (int k = 0; k < steps; ++k, at ^= 1) {
+            multiply(first, second, at, 1, std::false_type{}, 0, 0);
+            // The following step is there, and everyone has read this one.  Before a tile's
+            // second step the stores of the tile before may still be on their way.
+            if (k == 0 && whole_stores)
+                wait_loads<kStores>();
+            else
+                wait_loads<0>();
+            gi::lds_barrier();
+            if (k == steps - 2) {
+                if (more) stage_scales(set ^ 1, next);
+                aim(next);   // (after the last tile: at nothing)
+            }
+            multiply(second, first, at ^ 1, 0, std::true_type{}, at, k + 2 < steps ? k + 2 : k + 2 - steps);
+        }
+        const float *sx = reinterpret_cast<const float *>(smem + kStreamScales + set * 4096);
+        // (opaque: addresses that depend on the lane alone would be kept over the steps)
+        int lane = tid % 64;
+        asm volatile("" : "+v"(lane));
+        const int row = lane % 16, part = lane / 16;
+        const int n = now.n0 + wm * 64, e = now.e0 + we * 128;
+        // A wave's 64 positions leave as whole lines where they are in one batch item and
+        // inside its length, else one by one, a lane a position.
+        const int b = min(n + lane, a.N - 1) / a.L, l = n + lane - b * a.L;
+        const bool here = n + lane < a.N, inside = here && l < length_of(a.lengths, b, a.L);
+        const int b0 = __builtin_amdgcn_readfirstlane(b);
+        const bool fast = __all(inside && b == b0);
+        whole_stores = fast && e + 128 <= a.E_;
+        T *const y_lane = a.y.row(b, e) + l;   // (not followed where there is no position)
+        float sn[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sn[k] = sx[wm * 64 + part * 16 + k];
+        // A row of results is 64 positions; 2 KB of rows turn at once.
+        constexpr int kLine = 64 * (int)sizeof(T), kRows = 2048 / kLine, kUnits = kLine / 16;
+        constexpr int kOwn = kUnits / 4, V = 16 / (int)sizeof(T);   // units of a lane, results of a unit
+        uint8_t *const turn = smem + kStreamTurn + wave * 2048;
+        T *const y_line = a.y.row(b0, e + lane / kUnits) + __builtin_amdgcn_readfirstlane(l) + lane % kUnits * V;
+        const auto turned = [&](int c) {   // of row c: its units are at u ^ turned
+            return c / 2 % 2 * 2 + c / 4 % 2 + c / 8 % 2 * 4;
+        };
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int er = we * 128 + r * 16 + row;
+            const float sw = sx[256 + er], bias = sx[512 + er];
             float v[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                const int sum = acc[i][j][k];
-                v[k] = __builtin_fmaf((float)sum, sx[k] * sw, bias);
+                const int sum = acc[r][k / 4][k % 4];
+                v[k] = __builtin_fmaf((float)sum, sn[k] * sw, bias);
             }
-            store_positions<E, 16>(a, n, e, v);
+#pragma unroll
+            for (int half = 0; half < 16 / kRows; ++half) {
+                if (row / kRows == half) {
+#pragma unroll
+                    for (int u = 0; u < kOwn; ++u)
+                        *reinterpret_cast<uint4 *>(turn + row % kRows * kLine +
+                                                   ((part * kOwn + u) ^ turned(row)) * 16) = packed<E>(v + u * V);
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                const int c0 = r * 16 + half * kRows;   // the first row's channel
+                if (fast) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        constexpr int kPart = 64 / kUnits;   // rows of a store
+                        const int c = i * kPart + lane / kUnits, u = lane % kUnits;
+                        const uint4 o = *reinterpret_cast<const uint4 *>(
+                            turn + c * kLine + (u ^ turned(half * kRows + c)) * 16);
+                        typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+                        if (e + c0 + c < a.E_)
+                            *reinterpret_cast<Words *>(y_line + (c0 + i * kPart) * a.y.channel) =
+                                Words{o.x, o.y, o.z, o.w};
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < min(kRows, a.E_ - e - c0); ++c) {
+                        const T o = *reinterpret_cast<const T *>(
+                            turn + c * kLine + ((lane / V) ^ turned(half * kRows + c)) * 16 +
+                            lane % V * (int)sizeof(T));
+                        if (here) y_lane[(c0 + c) * a.y.channel] = inside ? o : (T)0;
+                    }
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
         }
+        now = next;
+        set ^= 1;
     }
 }
 
@@ -431,18 +727,18 @@ Project<E> project_of(const project_int8_args &a) {
             a.w_scales, a.bias, view<E>(a.y), a.lengths, (int)((int64_t)a.B * a.L), a.E, a.L, a.K, 0, 0};
 }
 
-template <class E, int WM, int WE, int BM, int BE, int ST>
+template <class E, int WM, int WE, int NB, int RB, int ST>
 hipError_t product(const project_int8_args &a, hipStream_t s) {
-    constexpr int TM = 32 * WM * BM, TE = 32 * WE * BE;
+    constexpr int TM = 16 * WM * NB, TE = 16 * WE * RB;
     Project<E> k = project_of<E>(a);
     k.n_tiles = (k.N + TM - 1) / TM, k.e_tiles = (a.E + TE - 1) / TE;
     constexpr int bytes = ST * (TM + TE) * kStep;
     if (bytes > 64 * 1024) {
-        hipError_t e = hipFuncSetAttribute((const void *)project<E, WM, WE, BM, BE, ST>,
+        hipError_t e = hipFuncSetAttribute((const void *)project<E, WM, WE, NB, RB, ST>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    project<E, WM, WE, BM, BE, ST>
+    project<E, WM, WE, NB, RB, ST>
         <<<(unsigned)((int64_t)k.n_tiles * k.e_tiles), 64 * WM * WE, bytes, s>>>(k);
     return hipGetLastError();
 }
@@ -491,7 +787,7 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
     constexpr int ROWS = 16 * (RB + (CODES ? 0 : NB)), kLoads = ROWS / 8, kEntry = ROWS * kStep;
     const Project<E> &a = t.p;
     extern __shared__ uint8_t smem[];
-    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     constexpr int kRing = DEPTH * kEntry, kMeet = RB * NB * 1024;   // bytes of a wave
     uint8_t *const ring = smem + wave * kRing;
     v4i *const meet = reinterpret_cast<v4i *>(smem);   // after the rings
@@ -545,7 +841,8 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
     uint32_t from[kLoads];
 #pragma unroll
     for (int p = 0; p < kLoads; ++p) {
-        const int r = p * 8 + lane / 8, unit = lane % 8 ^ (r / 2 % 8);
+        const int r = p * 8 + lane / 8;
+        const int unit = lane % 8 ^ (FORM == kAlongPositions && r >= 16 * RB ? position_turn<NB>(r - 16 * RB) : r / 2 % 8);
         const int held = r < 16 * RB ? min(r, a.E_ - e0 - 1) : min(r - 16 * RB, a.N - n0 - 1);
         from[p] = held * a.K + unit * 16;
     }
@@ -618,9 +915,10 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 const int xn = x_row + n * (FORM == kAlongPositions ? 4 : 16);
+                const int turned = u ^ (FORM == kAlongPositions ? position_turn<NB>(xn) : xn / 2 % 8);
                 fx[n][h] = *reinterpret_cast<const v4i *>(
                     CODES ? own + row * pitch + ((place(j) * 8 + u) ^ row) * 16
-                          : at + (RB * 16 + xn) * kStep + (u ^ (xn / 2 % 8)) * 16);
+                          : at + (RB * 16 + xn) * kStep + turned * 16);
             }
         }
         if (j + DEPTH < mine) {
@@ -713,6 +1011,18 @@ hipError_t split(const project_int8_args &a, const seq_tensor &x, int D, hipStre
     return hipGetLastError();
 }
 
+template <class E>
+hipError_t stream(const project_int8_args &a, hipStream_t s) {
+    Project<E> k = project_of<E>(a);
+    k.n_tiles = (k.N + kStreamTile - 1) / kStreamTile, k.e_tiles = (a.E + kStreamTile - 1) / kStreamTile;
+    hipError_t e = hipFuncSetAttribute((const void *)project_stream<E>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
+    if (e != hipSuccess) return e;
+    const int64_t tiles = (int64_t)k.n_tiles * k.e_tiles;
+    project_stream<E><<<(unsigned)std::min<int64_t>(tiles, 256), 64 * kStreamWaves, kStreamBytes, s>>>(k);
+    return hipGetLastError();
+}
+
 template <class E, int FORM>
 hipError_t split_any(const project_int8_args &a, hipStream_t s) {
     const int64_t N = (int64_t)a.B * a.L;
@@ -728,9 +1038,9 @@ hipError_t product_any(const project_int8_args &a, hipStream_t s) {
     const auto tiles = [&](int64_t t) { return (N + t - 1) / t * ((a.E + t - 1) / t); };
     if (N <= 64 || tiles(64) <= 128)
         return a.L == 1 ? split_any<E, kAlongChannels>(a, s) : split_any<E, kAlongPositions>(a, s);
-    if (tiles(256) >= 192) return product<E, 2, 4, 4, 2, 2>(a, s);
-    if (tiles(128) >= 192) return product<E, 2, 4, 2, 1, 2>(a, s);
-    return product<E, 2, 2, 1, 1, 3>(a, s);
+    if (tiles(256) >= 192 && a.K >= 2 * kStep) return stream<E>(a, s);
+    if (tiles(128) >= 192) return product<E, 2, 4, 4, 2, 2>(a, s);
+    return product<E, 2, 2, 2, 2, 3>(a, s);
 }
 
 int64_t code_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ_INT8_ROW; }

@@ -155,6 +155,17 @@ def test_product(case, dtype):
     Product(case, dtype).check()
 
 
+@pytest.mark.parametrize("case", [
+    # Tiles of 256 for every compute unit, and more; 2, 3 and 5 steps of k; items that end inside a tile.
+    (1, 3500, 3400, 256, None, "padded"), (1, 5000, 4200, 256, None, "dense"), (7, 6500, 300, 384, "ragged", "dense"),
+    (2, 3333, 1900, 640, None, "slice"), (1, 5120, 5120, 384, None, "dense"), (3, 8200, 1000, 256, "none", "dense")], ids=str)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_of_many_tiles(case, dtype):
+    s = Product(case, dtype)
+    y = s.check()
+    assert torch.equal(s.run(), y)
+
+
 def test_product_without_bias():
     Product((2, 70, 90, 256, None, "dense"), "f32", bias=False).check()
 
