@@ -312,18 +312,22 @@ __device__ __forceinline__ void store_positions(const Project<E> &a, int n, int 
 // 16 bytes of results.
 template <class E>
 __device__ __forceinline__ uint4 packed(const float *v) {
-    uint4 o;
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(typename E::type) == 4)
-            w[k] = __builtin_bit_cast(uint32_t, E::down(v[k]));
-        else
-            w[k] = (uint32_t)E::down(v[2 * k]) | (uint32_t)E::down(v[2 * k + 1]) << 16;
+        if constexpr (std::is_same_v<E, F32>) {
+            w[k] = __builtin_bit_cast(uint32_t, v[k]);
+        } else {
+            using H = std::conditional_t<std::is_same_v<E, BF16>, __bf16, _Float16>;
+            typedef float Floats __attribute__((ext_vector_type(2)));
+            typedef H Halves __attribute__((ext_vector_type(2)));
+            w[k] = __builtin_bit_cast(
+                uint32_t, __builtin_convertvector((Floats{v[2 * k], v[2 * k + 1]}), Halves));
+        }
     }
-    o.x = w[0], o.y = w[1], o.z = w[2], o.w = w[3];
-    return o;
+    return uint4{w[0], w[1], w[2], w[3]};
 }
+
 // f(row) for positions, and for channels row / 2 % 8 (above `project`).
 template <int NB>
 __device__ __forceinline__ int position_turn(int row) {
@@ -648,29 +652,41 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
         }
         const float *sx = reinterpret_cast<const float *>(smem + kStreamScales + set * 4096);
         // (opaque: addresses that depend on the lane alone would be kept over the steps)
-        int lane = tid % 64;
+        unsigned lane = tid % 64;
         asm volatile("" : "+v"(lane));
-        const int row = lane % 16, part = lane / 16;
+        lane &= 63;
+        const unsigned row = lane % 16, part = lane / 16;
         const int n = now.n0 + wm * 64, e = now.e0 + we * 128;
         // A wave's 64 positions leave as whole lines where they are in one batch item and
-        // inside its length, else one by one, a lane a position.
-        const int b = min(n + lane, a.N - 1) / a.L, l = n + lane - b * a.L;
-        const bool here = n + lane < a.N, inside = here && l < length_of(a.lengths, b, a.L);
+        // inside its length, and its channels are all there; else one by one, a lane a position.
+        const int b = min(n + (int)lane, a.N - 1) / a.L, l = n + (int)lane - b * a.L;
+        const bool here = n + (int)lane < a.N, inside = here && l < length_of(a.lengths, b, a.L);
         const int b0 = __builtin_amdgcn_readfirstlane(b);
-        const bool fast = __all(inside && b == b0);
-        whole_stores = fast && e + 128 <= a.E_;
-        T *const y_lane = a.y.row(b, e) + l;   // (not followed where there is no position)
+        whole_stores = __all(inside && b == b0) && e + 128 <= a.E_;
         float sn[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) sn[k] = sx[wm * 64 + part * 16 + k];
-        // A row of results is 64 positions; 2 KB of rows turn at once.
+        // A row of results is 64 positions; 2 KB of rows turn at once, unit u of row c at u ^
+        // turned(c).
         constexpr int kLine = 64 * (int)sizeof(T), kRows = 2048 / kLine, kUnits = kLine / 16;
         constexpr int kOwn = kUnits / 4, V = 16 / (int)sizeof(T);   // units of a lane, results of a unit
+        constexpr int kPart = 64 / kUnits;                          // rows of a store
         uint8_t *const turn = smem + kStreamTurn + wave * 2048;
-        T *const y_line = a.y.row(b0, e + lane / kUnits) + __builtin_amdgcn_readfirstlane(l) + lane % kUnits * V;
-        const auto turned = [&](int c) {   // of row c: its units are at u ^ turned
-            return c / 2 % 2 * 2 + c / 4 % 2 + c / 8 % 2 * 4;
-        };
+        const auto turned = [](unsigned c) { return (c & 2) | (c >> 2 & 1) | (c >> 1 & 4); };
+        uint8_t *put[kOwn];
+        const uint8_t *get[2];
+#pragma unroll
+        for (int u = 0; u < kOwn; ++u)
+            put[u] = turn + row % kRows * kLine + ((part * kOwn + u) ^ turned(row % kRows)) * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const unsigned c = i * kPart + lane / kUnits;
+            get[i] = turn + c * kLine + (lane % kUnits ^ turned(c)) * 16;
+        }
+        T *y = a.y.row(b, e) + l;   // (not followed where there is no position)
+        if (whole_stores)
+            y = a.y.row(b0, e + lane / kUnits) + __builtin_amdgcn_readfirstlane(l) + lane % kUnits * V;
+        const int64_t channel = a.y.channel;
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             __builtin_amdgcn_sched_barrier(0);
@@ -686,31 +702,23 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
             for (int half = 0; half < 16 / kRows; ++half) {
                 if (row / kRows == half) {
 #pragma unroll
-                    for (int u = 0; u < kOwn; ++u)
-                        *reinterpret_cast<uint4 *>(turn + row % kRows * kLine +
-                                                   ((part * kOwn + u) ^ turned(row)) * 16) = packed<E>(v + u * V);
+                    for (int u = 0; u < kOwn; ++u) *reinterpret_cast<uint4 *>(put[u]) = packed<E>(v + u * V);
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 const int c0 = r * 16 + half * kRows;   // the first row's channel
-                if (fast) {
+                if (whole_stores) {
+                    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        constexpr int kPart = 64 / kUnits;   // rows of a store
-                        const int c = i * kPart + lane / kUnits, u = lane % kUnits;
-                        const uint4 o = *reinterpret_cast<const uint4 *>(
-                            turn + c * kLine + (u ^ turned(half * kRows + c)) * 16);
-                        typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
-                        if (e + c0 + c < a.E_)
-                            *reinterpret_cast<Words *>(y_line + (c0 + i * kPart) * a.y.channel) =
-                                Words{o.x, o.y, o.z, o.w};
+                        const uint4 o = *reinterpret_cast<const uint4 *>(get[i]);
+                        *reinterpret_cast<Words *>(y + (c0 + i * kPart) * channel) = Words{o.x, o.y, o.z, o.w};
                     }
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < min(kRows, a.E_ - e - c0); ++c) {
                         const T o = *reinterpret_cast<const T *>(
-                            turn + c * kLine + ((lane / V) ^ turned(half * kRows + c)) * 16 +
-                            lane % V * (int)sizeof(T));
-                        if (here) y_lane[(c0 + c) * a.y.channel] = inside ? o : (T)0;
+                            turn + c * kLine + ((lane / V) ^ turned(c)) * 16 + lane % V * sizeof(T));
+                        if (here) y[(c0 + c) * channel] = inside ? o : (T)0;
                     }
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
