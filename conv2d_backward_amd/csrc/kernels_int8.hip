@@ -328,6 +328,89 @@ __device__ __forceinline__ uint4 packed(const float *v) {
     return uint4{w[0], w[1], w[2], w[3]};
 }
 
+// The results of a wave, 16 NB positions from n by 16 RB channels from e, whose sums sum(r, k)
+// a lane has for position part * 4 NB + k and channel r * 16 + row.  They turn in `turn`, 16
+// channels (float32: 8) at a time, so that a store writes whole lines; where the positions are
+// not all in one batch item and inside its length, or channels are missing, they leave one by
+// one, a lane a position.  Returns whether that took exactly RB NB sizeof(T) / 4 stores.
+template <class E, int NB, int RB, class Sx, class Sw, class Bias, class Sum>
+__device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t *turn, Sx scale_of,
+                                      Sw w_scale_of, Bias bias_of, Sum sum) {
+    using T = typename E::type;
+    // (opaque: addresses that depend on the lane alone would be kept over the caller's steps)
+    unsigned lane = threadIdx.x % 64;
+    asm volatile("" : "+v"(lane));
+    lane &= 63;
+    const unsigned row = lane % 16, part = lane / 16;
+    constexpr int P = 16 * NB;   // positions, at most a lane each
+    const int at = n + (int)(lane % P), b = min(at, a.N - 1) / a.L, l = at - b * a.L;
+    const bool here = at < a.N, inside = here && l < length_of(a.lengths, b, a.L);
+    const int b0 = __builtin_amdgcn_readfirstlane(b);
+    const bool whole = __all(inside && b == b0) && e + 16 * RB <= a.E_;
+    float sn[4 * NB];
+#pragma unroll
+    for (int k = 0; k < 4 * NB; ++k) sn[k] = scale_of(part * 4 * NB + k);
+    // Unit u of row c is at u ^ turned(c).
+    constexpr int kLine = P * (int)sizeof(T), kRows = sizeof(T) == 2 ? 16 : 8, kUnits = kLine / 16;
+    constexpr int kOwn = kUnits / 4, V = 16 / (int)sizeof(T);   // units of a lane, results of a unit
+    constexpr int kPart = 64 / kUnits, kTimes = kRows / kPart;  // rows of a store, stores
+    const auto turned = [](unsigned c) {
+        return ((c & 2) | (c >> 2 & 1) | (c >> 1 & 4)) & (kUnits - 1);
+    };
+    uint8_t *put[kOwn];
+    const uint8_t *get[kTimes];
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u)
+        put[u] = turn + row % kRows * kLine + ((part * kOwn + u) ^ turned(row % kRows)) * 16;
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+        const unsigned c = i * kPart + lane / kUnits;
+        get[i] = turn + c * kLine + (lane % kUnits ^ turned(c)) * 16;
+    }
+    T *y = a.y.row(b, e) + l;   // (not followed where there is no position)
+    if (whole)
+        y = a.y.row(b0, e + lane / kUnits) + __builtin_amdgcn_readfirstlane(l) + lane % kUnits * V;
+    const int64_t channel = a.y.channel;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+        __builtin_amdgcn_sched_barrier(0);
+        const float sw = w_scale_of(r * 16 + row), bias = bias_of(r * 16 + row);
+        float v[4 * NB];
+#pragma unroll
+        for (int k = 0; k < 4 * NB; ++k) {
+            const int one = sum(r, k);
+            v[k] = __builtin_fmaf((float)one, sn[k] * sw, bias);
+        }
+#pragma unroll
+        for (int half = 0; half < 16 / kRows; ++half) {
+            if (row / kRows == half) {
+#pragma unroll
+                for (int u = 0; u < kOwn; ++u) *reinterpret_cast<uint4 *>(put[u]) = packed<E>(v + u * V);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            const int c0 = r * 16 + half * kRows;   // the first row's channel
+            if (whole) {
+                typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) {
+                    const uint4 o = *reinterpret_cast<const uint4 *>(get[i]);
+                    *reinterpret_cast<Words *>(y + (c0 + i * kPart) * channel) = Words{o.x, o.y, o.z, o.w};
+                }
+            } else {
+                constexpr int kSide = 64 / P;   // channels at once
+#pragma unroll 1
+                for (int c = lane / P; c < min(kRows, a.E_ - e - c0); c += kSide) {
+                    const T o = *reinterpret_cast<const T *>(
+                        turn + c * kLine + ((lane % P / V) ^ turned(c)) * 16 + lane % V * sizeof(T));
+                    if (here) y[(c0 + c) * channel] = inside ? o : (T)0;
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+    }
+    return whole;
+}
+
 // f(row) for positions, and for channels row / 2 % 8 (above `project`).
 template <int NB>
 __device__ __forceinline__ int position_turn(int row) {
@@ -449,30 +532,13 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
         }
     }
 
-    const int n = n0 + wm * 16 * NB + part * 4 * NB;
-    if (n >= a.N) return;
-#pragma unroll
-    for (int i = 0; i < NB; i += 4 < NB ? 4 : NB) {
-        constexpr int V = NB < 4 ? 4 * NB : 16;   // positions stored at once
-        const int m = n + 4 * i;
-        if (m >= a.N) continue;
-        float sx[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) sx[k] = a.scales[min(m + k, a.N - 1)];
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            const int e = e0 + (we * RB + r) * 16 + row;
-            if (e >= a.E_) continue;
-            const float sw = a.w_scales[e], bias = a.bias ? a.bias[e] : 0.f;
-            float v[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int sum = acc[r][i + k / 4][k % 4];
-                v[k] = __builtin_fmaf((float)sum, sx[k] * sw, bias);
-            }
-            store_positions<E, V>(a, m, e, v);
-        }
-    }
+    // (every wave has read its last operands before the last barrier)
+    const int n = n0 + wm * 16 * NB, e = e0 + we * 16 * RB;
+    leave<E, NB, RB>(
+        a, n, e, smem + wave * 2048, [&](int k) { return a.scales[min(n + k, a.N - 1)]; },
+        [&](int c) { return a.w_scales[min(e + c, a.E_ - 1)]; },
+        [&](int c) { return a.bias ? a.bias[min(e + c, a.E_ - 1)] : 0.f; },
+        [&](int r, int k) { return acc[r][k / 4][k % 4]; });
 }
 
 // The same for products that fill the chip: tiles of 256 x 256, one work-group a compute
@@ -651,79 +717,10 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
             multiply(second, first, at ^ 1, 0, std::true_type{}, at, k + 2 < steps ? k + 2 : k + 2 - steps);
         }
         const float *sx = reinterpret_cast<const float *>(smem + kStreamScales + set * 4096);
-        // (opaque: addresses that depend on the lane alone would be kept over the steps)
-        unsigned lane = tid % 64;
-        asm volatile("" : "+v"(lane));
-        lane &= 63;
-        const unsigned row = lane % 16, part = lane / 16;
-        const int n = now.n0 + wm * 64, e = now.e0 + we * 128;
-        // A wave's 64 positions leave as whole lines where they are in one batch item and
-        // inside its length, and its channels are all there; else one by one, a lane a position.
-        const int b = min(n + (int)lane, a.N - 1) / a.L, l = n + (int)lane - b * a.L;
-        const bool here = n + (int)lane < a.N, inside = here && l < length_of(a.lengths, b, a.L);
-        const int b0 = __builtin_amdgcn_readfirstlane(b);
-        whole_stores = __all(inside && b == b0) && e + 128 <= a.E_;
-        float sn[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) sn[k] = sx[wm * 64 + part * 16 + k];
-        // A row of results is 64 positions; 2 KB of rows turn at once, unit u of row c at u ^
-        // turned(c).
-        constexpr int kLine = 64 * (int)sizeof(T), kRows = 2048 / kLine, kUnits = kLine / 16;
-        constexpr int kOwn = kUnits / 4, V = 16 / (int)sizeof(T);   // units of a lane, results of a unit
-        constexpr int kPart = 64 / kUnits;                          // rows of a store
-        uint8_t *const turn = smem + kStreamTurn + wave * 2048;
-        const auto turned = [](unsigned c) { return (c & 2) | (c >> 2 & 1) | (c >> 1 & 4); };
-        uint8_t *put[kOwn];
-        const uint8_t *get[2];
-#pragma unroll
-        for (int u = 0; u < kOwn; ++u)
-            put[u] = turn + row % kRows * kLine + ((part * kOwn + u) ^ turned(row % kRows)) * 16;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const unsigned c = i * kPart + lane / kUnits;
-            get[i] = turn + c * kLine + (lane % kUnits ^ turned(c)) * 16;
-        }
-        T *y = a.y.row(b, e) + l;   // (not followed where there is no position)
-        if (whole_stores)
-            y = a.y.row(b0, e + lane / kUnits) + __builtin_amdgcn_readfirstlane(l) + lane % kUnits * V;
-        const int64_t channel = a.y.channel;
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            __builtin_amdgcn_sched_barrier(0);
-            const int er = we * 128 + r * 16 + row;
-            const float sw = sx[256 + er], bias = sx[512 + er];
-            float v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int sum = acc[r][k / 4][k % 4];
-                v[k] = __builtin_fmaf((float)sum, sn[k] * sw, bias);
-            }
-#pragma unroll
-            for (int half = 0; half < 16 / kRows; ++half) {
-                if (row / kRows == half) {
-#pragma unroll
-                    for (int u = 0; u < kOwn; ++u) *reinterpret_cast<uint4 *>(put[u]) = packed<E>(v + u * V);
-                }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                const int c0 = r * 16 + half * kRows;   // the first row's channel
-                if (whole_stores) {
-                    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 o = *reinterpret_cast<const uint4 *>(get[i]);
-                        *reinterpret_cast<Words *>(y + (c0 + i * kPart) * channel) = Words{o.x, o.y, o.z, o.w};
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < min(kRows, a.E_ - e - c0); ++c) {
-                        const T o = *reinterpret_cast<const T *>(
-                            turn + c * kLine + ((lane / V) ^ turned(c)) * 16 + lane % V * sizeof(T));
-                        if (here) y[(c0 + c) * channel] = inside ? o : (T)0;
-                    }
-                }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            }
-        }
+        whole_stores = leave<E, NB, RB>(
+            a, now.n0 + wm * 64, now.e0 + we * 128, smem + kStreamTurn + wave * 2048,
+            [&](int k) { return sx[wm * 64 + k]; }, [&](int c) { return sx[256 + we * 128 + c]; },
+            [&](int c) { return sx[512 + we * 128 + c]; }, [&](int r, int k) { return acc[r][k / 4][k % 4]; });
         now = next;
         set ^= 1;
     }
