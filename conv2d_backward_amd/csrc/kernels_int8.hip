@@ -97,24 +97,21 @@ struct Quantize {
     int B, D, L, K, tiles;
 };
 
-// Positions along the lanes.  A work-group has 64 bytes of positions, its 1024 threads V
-// of them (16 bytes) and four channels at a time, 1024 channels in a round.  The first
-// KEPT rounds stay in registers between the two passes, over the maximum and over the
-// codes; what is beyond is read again.  A wave's loads are 64 bytes of 16 channels, its
-// stores 64 bytes of codes of 4 positions.
-template <class E>
-constexpr int kTilePositions = 64 / (int)sizeof(typename E::type);
-
-template <class E, int KEPT>
-__global__ __launch_bounds__(1024) void quantize_tile(Quantize<E> a) {
+// Positions along the lanes.  A work-group has 16 G bytes of positions, each thread of its W
+// waves V of them (16 bytes) and four channels at a time, 256 W / G channels in a round.  The
+// first KEPT rounds stay in registers between the two passes, over the maximum and over the
+// codes; what is beyond is read again.  With G = 4 a wave's loads are 64 bytes of 16
+// channels, its stores 64 bytes of codes of 4 positions.
+template <class E, int G, int W, int KEPT>
+__global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
     using T = typename E::type;
-    constexpr int V = 16 / (int)sizeof(T), TT = 4 * V;
+    constexpr int V = 16 / (int)sizeof(T), TT = G * V, kRound = 256 * W / G;
     typedef typename Vec<T, V>::type Some;
-    __shared__ uint32_t meet[16][16];
+    __shared__ uint32_t meet[W][4 * G];
     const int id = gi::xcd_order(blockIdx.x, gridDim.x);
     const int b = id / a.tiles, t0 = id % a.tiles * TT;
     const int len = length_of(a.lengths, b, a.L);
-    const int group = threadIdx.x % 4, quad = threadIdx.x / 4, t = t0 + group * V;
+    const int group = threadIdx.x % G, quad = threadIdx.x / G, t = t0 + group * V;
     const int left = len - t;
     const auto load = [&](int d) {
         Some v;
@@ -137,7 +134,7 @@ __global__ __launch_bounds__(1024) void quantize_tile(Quantize<E> a) {
 #pragma unroll
     for (int r = 0; r < KEPT; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kept[r][j] = load(r * 1024 + quad * 4 + j);
+        for (int j = 0; j < 4; ++j) kept[r][j] = load(r * kRound + quad * 4 + j);
     // Four words of V positions each.
     uint32_t words[4] = {0, 0, 0, 0};
     const auto see = [&](const Some &v) {
@@ -152,7 +149,7 @@ __global__ __launch_bounds__(1024) void quantize_tile(Quantize<E> a) {
     for (int r = 0; r < KEPT; ++r)
 #pragma unroll
         for (int j = 0; j < 4; ++j) see(kept[r][j]);
-    for (int d = KEPT * 1024 + quad * 4; d < a.D; d += 1024) {
+    for (int d = KEPT * kRound + quad * 4; d < a.D; d += kRound) {
         Some v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = load(d + j);
@@ -162,16 +159,16 @@ __global__ __launch_bounds__(1024) void quantize_tile(Quantize<E> a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int s = 4; s < 64; s *= 2)
+        for (int s = G; s < 64; s *= 2)
             words[k] = raise(words[k], (uint32_t)__shfl_xor((int)words[k], s, 64), E{});
-        if (threadIdx.x % 64 < 4) meet[threadIdx.x / 64][group * 4 + k] = words[k];
+        if (threadIdx.x % 64 < G) meet[threadIdx.x / 64][group * 4 + k] = words[k];
     }
     __syncthreads();
     Coder c[V];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int w = 0; w < 16; ++w) words[k] = raise(words[k], meet[w][group * 4 + k], E{});
+        for (int w = 0; w < W; ++w) words[k] = raise(words[k], meet[w][group * 4 + k], E{});
 #pragma unroll
         for (int h = 0; h < V / 4; ++h) {
             const int at = k * (V / 4) + h;
@@ -195,10 +192,10 @@ __global__ __launch_bounds__(1024) void quantize_tile(Quantize<E> a) {
     };
 #pragma unroll
     for (int r = 0; r < KEPT; ++r) {
-        const int d = r * 1024 + quad * 4;
+        const int d = r * kRound + quad * 4;
         if (d < a.K) write(d, kept[r]);
     }
-    for (int d = KEPT * 1024 + quad * 4; d < a.K; d += 1024) {
+    for (int d = KEPT * kRound + quad * 4; d < a.K; d += kRound) {
         Some v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = load(d + j);
@@ -238,18 +235,33 @@ __global__ __launch_bounds__(256) void quantize_row(Quantize<E> a) {
     }
 }
 
+template <class E, int G, int W>
+hipError_t quantize_tiles(Quantize<E> k, hipStream_t s) {
+    constexpr int TT = G * 16 / (int)sizeof(typename E::type), kRound = 256 * W / G;
+    k.tiles = (k.L + TT - 1) / TT;
+    const auto kernel = k.D <= kRound ? quantize_tile<E, G, W, 1>
+                        : k.D <= 2 * kRound ? quantize_tile<E, G, W, 2> : quantize_tile<E, G, W, 4>;
+    kernel<<<(unsigned)(k.B * (int64_t)k.tiles), 64 * W, 0, s>>>(k);
+    return hipGetLastError();
+}
+
 template <class E>
 hipError_t quantize(const quantize_tokens_args &a, hipStream_t s) {
     Quantize<E> k{view<E>(a.x), static_cast<uint32_t *>(a.codes), a.scales, a.lengths,
-                  a.B, a.D, a.L, a.K, (a.L + kTilePositions<E> - 1) / kTilePositions<E>};
+                  a.B, a.D, a.L, a.K, 0};
     if (a.L == 1 && (a.x.channel == 1 || a.D == 1)) {
         quantize_row<E><<<(unsigned)a.B, 256, 0, s>>>(k);
-    } else {
-        const auto kernel = a.D <= 1024 ? quantize_tile<E, 1>
-                            : a.D <= 2048 ? quantize_tile<E, 2> : quantize_tile<E, 4>;
-        kernel<<<(unsigned)(a.B * (int64_t)k.tiles), 1024, 0, s>>>(k);
+        return hipGetLastError();
     }
-    return hipGetLastError();
+    // Few positions are shared out finer, so that more compute units have some, though a
+    // cache line then goes to several of them.  Measured (us; G, W of 4, 16 / 2, 16 / 2, 8 /
+    // 1, 8): [1, 4096, 8192] bf16 23.9 / 27.6 / 25.5 / 29.8, [4, 2048, 2048] bf16 13.6 / 16.2 /
+    // 14.2 / 17.3, [2, 2051, 777] f32 11.4 / 9.0 / 9.8 / 10.7, [2, 1024, 1000] bf16 6.9 / 6.1 /
+    // 5.2 / 5.6, [5, 1000, 301] f16 8.4 / 7.9 / 7.1 / 5.9, [1, 8192, 2000] bf16 34 / 21 / 26 / 19.
+    const int64_t groups = (int64_t)a.B * ((a.L * sizeof(typename E::type) + 15) / 16);
+    if (groups >= 1024) return quantize_tiles<E, 4, 16>(k, s);
+    if (groups < 256) return quantize_tiles<E, 1, 8>(k, s);
+    return a.D > 1024 ? quantize_tiles<E, 2, 16>(k, s) : quantize_tiles<E, 2, 8>(k, s);
 }
 
 // ---- the product ---------------------------------------------------------------------------------

@@ -59,6 +59,15 @@ def test_codes(case, dtype):
     check_codes(x, codes, scales, n)
 
 
+@pytest.mark.parametrize("case", [
+    # Enough positions for every way they are shared out, with channels for every number of rounds kept and beyond.
+    (1, 1500, 3000, None, "dense"), (1, 3000, 2500, None, "slice"), (1, 4500, 2100, None, "padded"),
+    (1, 8300, 2100, None, "dense"), (7, 600, 620, "ragged", "padded"), (4, 900, 2101, None, "dense"),
+    (8, 1100, 1030, None, "dense"), (8, 2100, 1030, None, "swapped"), (8, 4200, 1030, None, "dense")], ids=str)
+def test_codes_of_many_positions(case):
+    test_codes(case, "bf16")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("L", [1, 40])
 def test_codes_at_the_borders(dtype, L):
