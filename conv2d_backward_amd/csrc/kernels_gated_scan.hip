@@ -29,32 +29,25 @@ constexpr int T = 8;            // positions of a lane
 constexpr int kRow = 16 * T;    // positions of a row of lanes
 static_assert(kRow == SEQ_SCAN_CHECKPOINT, "a checkpoint for every row of lanes");
 
-// 1 - a^2 = -e^v + 1, v = 2 u, loses all digits in fp32 where a is near 1, which is
-// where such layers work (u is -1e-4 to -0.1).  With t = e^u - 1 it is -t (2 + t), and t
-// comes from its series up to u^7 / 5040 above -0.3 (the next term is 5e-9 there), from a
-// below, where a - 1 has lost less than two bits.
+// 1 - a^2 loses all digits in fp32 where a is near 1, which is where such layers work (u is
+// -1e-4 to -0.1).  It is -2 a sinh(u), and sinh(u) / u has a short series in u^2: up to u^6 / 5040
+// the next term is 1e-8 of it at |u| = 0.5.  Below that 1 - a^2 itself has lost less than a bit.
+// Everything is in l = u log2(e), so that no u is needed.
 struct Decay {
     float a, n;  // e^u, 1 - e^2u
 };
-__device__ __forceinline__ Decay decay(float sr, float A, float A2) {
-    const float u = sr * A;
+__device__ __forceinline__ Decay decay(float sr, float A2) {
+    constexpr float k = kLn2 * kLn2;
+    const float l = sr * A2, w = l * l;
     Decay d;
-    d.a = exp2_fast(sr * A2);
-    float t = __builtin_fmaf(u, 1.f / 5040, 1.f / 720);
-    t = __builtin_fmaf(u, t, 1.f / 120);
-    t = __builtin_fmaf(u, t, 1.f / 24);
-    t = __builtin_fmaf(u, t, 1.f / 6);
-    t = __builtin_fmaf(u, t, 0.5f);
-    t = __builtin_fmaf(u, t, 1.f) * u;
-    t = u > -0.3f ? t : d.a - 1.f;
-    d.n = -t * (2.f + t);
+    d.a = exp2_fast(l);
+    float s = __builtin_fmaf(w, -2 * kLn2 * k * k * k / 5040, -2 * kLn2 * k * k / 120);
+    s = __builtin_fmaf(w, s, -2 * kLn2 * k / 6);
+    s = __builtin_fmaf(w, s, -2 * kLn2);
+    const float near = d.a * (l * s), far = __builtin_fmaf(-d.a, d.a, 1.f);
+    d.n = l > -0.5f * kLog2e ? near : far;
     return d;
 }
-// A rate of -inf becomes the lowest float: a closed gate (sr = 0) then still keeps the state.
-__device__ __forceinline__ float finite_rate(float A) {
-    return A < -3.4028234664e38f ? -3.4028234664e38f : A;
-}
-
 // sigmoid(v + bias), the bias times -log2(e).
 __device__ __forceinline__ float gate(float v, float bias) {
     return __builtin_amdgcn_rcpf(1.f + exp2_fast(__builtin_fmaf(v, -kLog2e, bias)));
@@ -66,16 +59,26 @@ __device__ __forceinline__ float dpp(float old, float v) {
         __builtin_bit_cast(int, old), __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
 }
 constexpr int kRowShl1 = 0x101, kRowShr1 = 0x111, kRowFirst = 0x150, kRowLast = 0x15f;
+// Of four lanes, each other's: the lane that each takes from.
+constexpr int kQuad3012 = 0x93, kQuad1230 = 0x39, kQuad2301 = 0x4e, kQuadFirst = 0x00, kQuadLast = 0xff;
 
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __builtin_bit_cast(float,
                               __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 
-// Inclusive maps of the lanes of a row, from its first lane (or, BACK, from its last).
-template <bool BACK>
+// Inclusive maps of 16 lanes (or of 4), from the first lane (or, BACK, from the last).
+template <int LANES, bool BACK>
 __device__ __forceinline__ void scan_row(float &P, float &Q) {
-    if constexpr (BACK)
+    if constexpr (LANES == 4) {
+        const unsigned lane = BACK ? 3 - threadIdx.x % 4 : threadIdx.x % 4;
+        const float p1 = dpp<BACK ? kQuad1230 : kQuad3012>(0.f, P), q1 = dpp<BACK ? kQuad1230 : kQuad3012>(0.f, Q);
+        Q = lane >= 1 ? __builtin_fmaf(P, q1, Q) : Q;
+        P = lane >= 1 ? P * p1 : P;
+        const float p2 = dpp<kQuad2301>(0.f, P), q2 = dpp<kQuad2301>(0.f, Q);
+        Q = lane >= 2 ? __builtin_fmaf(P, q2, Q) : Q;
+        P = lane >= 2 ? P * p2 : P;
+    } else if constexpr (BACK)
         asm("s_nop 1\n\t" SEQ_ROW_STEPS(SEQ_STEP1, "shl") SEQ_STEP1("row_shl:8" SEQ_ALL)
             "s_nop 0" : "+v"(Q), "+v"(P));
     else
@@ -88,7 +91,17 @@ __device__ __forceinline__ void scan_row(float &P, float &Q) {
 // has W maps, which nothing else uses before the barrier after the next one.
 template <int LANES, int W, bool BACK>
 __device__ __forceinline__ float enter(float P, float Q, float &start, float2 *meet) {
-    scan_row<BACK>(P, Q);
+    scan_row<LANES, BACK>(P, Q);
+    if constexpr (LANES == 4) {
+        static_assert(W == 1, "rows of 4 lanes are in one wave");
+        const bool end = threadIdx.x % 4 == (BACK ? 3 : 0);
+        const float p = dpp<BACK ? kQuad1230 : kQuad3012>(0.f, P), q = dpp<BACK ? kQuad1230 : kQuad3012>(0.f, Q);
+        const float into = end ? start : __builtin_fmaf(p, start, q);
+        const float all_P = dpp<BACK ? kQuadFirst : kQuadLast>(0.f, P);
+        const float all_Q = dpp<BACK ? kQuadFirst : kQuadLast>(0.f, Q);
+        start = __builtin_fmaf(all_P, start, all_Q);
+        return into;
+    }
     const float before_P = BACK ? dpp<kRowShl1>(1.f, P) : dpp<kRowShr1>(1.f, P);
     const float before_Q = BACK ? dpp<kRowShl1>(0.f, Q) : dpp<kRowShr1>(0.f, Q);
     if constexpr (LANES == 16) {
@@ -98,7 +111,7 @@ __device__ __forceinline__ float enter(float P, float Q, float &start, float2 *m
         const float all_Q = BACK ? dpp<kRowFirst>(0.f, Q) : dpp<kRowLast>(0.f, Q);
         start = __builtin_fmaf(all_P, start, all_Q);
         return into;
-    } else {
+    } else if constexpr (LANES == 64) {
         // The rows in the chain's order.
         float rP[4], rQ[4];
 #pragma unroll
@@ -162,7 +175,7 @@ __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_forward(GatedFwd
     if (row >= a.rows) return;  // (W > 1: one row, all or none)
     const int b = row / a.D, d = row - b * a.D;
     const int len = length_of(a.lengths, b, a.L);
-    const float A = finite_rate(a.A[d]), A2 = decay_rate(a.A[d]);
+    const float A2 = decay_rate(a.A[d]);
     const float r_bias = a.r_bias ? a.r_bias[d] * -kLog2e : 0.f;
     const float i_bias = a.i_bias ? a.i_bias[d] * -kLog2e : 0.f;
     const auto *x = a.x.row(b, d), *r = a.r.row(b, d), *i = a.i.row(b, d);
@@ -185,7 +198,7 @@ __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_forward(GatedFwd
 #pragma unroll
         for (int k = 0; k < T; ++k) {
             const float sr = gate(nr.at(k), r_bias), si = gate(ni.at(k), i_bias);
-            const Decay v = decay(sr, A, A2);
+            const Decay v = decay(sr, A2);
             av[k] = v.a;
             in[k] = __builtin_amdgcn_sqrtf(v.n) * (si * nx.at(k));
             if (z) f[k] = nz.at(k) * sigmoid(nz.at(k));
@@ -241,6 +254,7 @@ struct GatedBwd {
 template <class E, int LANES, int W>
 __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_backward(GatedBwd<E> a) {
     constexpr int CHUNK = LANES * W * T, ROWS = kRowsOf<LANES, W>;
+    constexpr int kH = LANES == 4 ? 4 : 16;   // lanes that run h again from a checkpoint together
     __shared__ float2 meet[2][W];
     __shared__ float sums[3][W];
     const int lane = threadIdx.x % (LANES * W);
@@ -248,7 +262,7 @@ __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_backward(GatedBw
     if (row >= a.rows) return;
     const int b = row / a.D, d = row - b * a.D;
     const int len = length_of(a.lengths, b, a.L);
-    const float A = finite_rate(a.A[d]), A2 = decay_rate(a.A[d]);
+    const float A2 = decay_rate(a.A[d]), A = A2 * kLn2;
     const float r_bias = a.r_bias ? a.r_bias[d] * -kLog2e : 0.f;
     const float i_bias = a.i_bias ? a.i_bias[d] * -kLog2e : 0.f;
     const auto *x = a.x.row(b, d), *r = a.r.row(b, d), *i = a.i.row(b, d), *g = a.gout.row(b, d);
@@ -268,7 +282,7 @@ __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_backward(GatedBw
         ng.load(g + t, len - t);
         if (z) nz.load(z + t, len - t);
         next_h = 0.f;
-        if (lane % 16 == 0 && t < len) next_h = marks[t / SEQ_SCAN_CHECKPOINT];
+        if (lane % kH == 0 && t < len) next_h = marks[t / SEQ_SCAN_CHECKPOINT];
     };
     {
         float zero[T];
@@ -289,7 +303,7 @@ __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_backward(GatedBw
         for (int k = 0; k < T; ++k) {
             sr[k] = gate(nr.at(k), r_bias);
             si[k] = gate(ni.at(k), i_bias);
-            const Decay v = decay(sr[k], A, A2);
+            const Decay v = decay(sr[k], A2);
             av[k] = v.a;
             // 1 / m; where a is 1 the normaliser's slope, infinite there, counts as 0 (and
             // below the normal range, whose root v_sqrt_f32 too takes for 0).
@@ -322,8 +336,8 @@ __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_backward(GatedBw
             P *= av[k];
         }
         {
-            float at = dpp<kRowFirst>(0.f, h), row_P = P;
-            h = enter<16, 1, false>(row_P, Q, at, nullptr);
+            float at = dpp<kH == 4 ? kQuadFirst : kRowFirst>(0.f, h), row_P = P;
+            h = enter<kH, 1, false>(row_P, Q, at, nullptr);
         }
         float before[T];  // h before the position
 #pragma unroll
@@ -396,18 +410,16 @@ __global__ __launch_bounds__((kThreadsOf<LANES, W>)) void gated_backward(GatedBw
     }
 }
 
-// Sums over the batch, in its order.
+// Sums over the batch, in its order, of [B][D][3]: dA, dr_bias, di_bias.
 __global__ __launch_bounds__(256) void gated_join(const float *params, float *dA, float *dr_bias,
                                                   float *di_bias, int B, int D) {
-    const int d = blockIdx.x * 256 + threadIdx.x;
-    if (d >= D) return;
-    float sum[3] = {0.f, 0.f, 0.f};
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) sum[k] += params[((int64_t)b * D + d) * 3 + k];
-    dA[d] = sum[0];
-    if (dr_bias) dr_bias[d] = sum[1];
-    if (di_bias) di_bias[d] = sum[2];
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= 3 * D) return;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int b = 0; b < B; ++b) sum += params[(int64_t)b * 3 * D + i];
+    float *const to = i % 3 == 0 ? dA : i % 3 == 1 ? dr_bias : di_bias;
+    if (to) to[i / 3] = sum;
 }
 
 template <class E>
@@ -419,35 +431,65 @@ struct GatedStep {
     int D, lines;
 };
 
-template <class E>
+// One position: each number is read and written once, V channels a thread (contiguous ones
+// where V > 1), 16 bytes of states for V = 4.
+template <class E, int V>
 __global__ __launch_bounds__(256) void gated_step(GatedStep<E> a) {
-    const int d = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
+    const int d = (blockIdx.x * 256 + threadIdx.x) * V, b = blockIdx.y;
     if (d >= a.D) return;
     const int slot = a.slots ? a.slots[b] : b;
-    float out = 0.f;
+    float out[V];
     if (slot >= 0 && slot < a.lines) {
         float *state = a.state + (int64_t)slot * a.D + d;
-        const float sr = gate(E::up(*a.r.row(b, d)), a.r_bias ? a.r_bias[d] * -kLog2e : 0.f);
-        const float si = gate(E::up(*a.i.row(b, d)), a.i_bias ? a.i_bias[d] * -kLog2e : 0.f);
-        const Decay v = decay(sr, finite_rate(a.A[d]), decay_rate(a.A[d]));
-        out = __builtin_fmaf(v.a, *state, __builtin_amdgcn_sqrtf(v.n) * (si * E::up(*a.x.row(b, d))));
-        *state = out;
-        if (a.z.p) {
-            const float z = E::up(*a.z.row(b, d));
-            out *= z * sigmoid(z);
+        float x[V], r[V], i[V], z[V], h[V], A[V], rb[V], ib[V];
+        load_vec<F32, V>(state, h);
+        load_vec<E, V>(a.x.row(b, d), x);
+        load_vec<E, V>(a.r.row(b, d), r);
+        load_vec<E, V>(a.i.row(b, d), i);
+        if (a.z.p) load_vec<E, V>(a.z.row(b, d), z);
+        load_vec<F32, V>(a.A + d, A);
+#pragma unroll
+        for (int k = 0; k < V; ++k) rb[k] = ib[k] = 0.f;
+        if (a.r_bias) load_vec<F32, V>(a.r_bias + d, rb);
+        if (a.i_bias) load_vec<F32, V>(a.i_bias + d, ib);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float sr = gate(r[k], rb[k] * -kLog2e), si = gate(i[k], ib[k] * -kLog2e);
+            const Decay v = decay(sr, decay_rate(A[k]));
+            h[k] = __builtin_fmaf(v.a, h[k], __builtin_amdgcn_sqrtf(v.n) * (si * x[k]));
+            out[k] = a.z.p ? h[k] * (z[k] * sigmoid(z[k])) : h[k];
         }
+        store_vec<F32, V>(state, h);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) out[k] = 0.f;
     }
-    *a.y.row(b, d) = E::down(out);
+    store_vec<E, V>(a.y.row(b, d), out);
 }
 
 // How the rows are dealt: lanes of a row in a wave, waves of a row.
 struct Deal {
     int lanes, waves;
 };
-Deal pick_deal(int64_t rows, int64_t L) {
-    if (L <= 2 * kRow) return {16, 1};
+// Rows that fit into few lanes take no more (4 lanes only where that is the whole row:
+// a checkpoint is for 16).  Longer ones take a wave, several where there are too few rows to
+// fill the chip, and where that leaves four chunks to read ahead in; the backward call, whose
+// waves have twice the work, takes two chunks at least instead of a wave more.  Measured (us,
+// forward / backward, 16 lanes, 64 lanes with 1, 2, 4, 8, 16 waves):
+// [1, 4096, 8192] bf16 108 75 74 71 77 87 / 144 134 136 129 154 169,
+// [4, 2048, 2048] bf16 37 30 31 32 64 153 / 65 61 64 71 168 262,
+// [1, 256, 8192] bf16 85 24 14 8.8 6.9 6.4 / 129 38 24 16.5 14.4 14.8,
+// [2, 602, 777] f32 12 7.5 6.3 8.7 13 26 / 23 14.7 17.7 22 32 59,
+// [1, 300, 3000] f16 34 11 8.5 7.3 6.4 11 / 54 19 15 13 15 21,
+// [4, 2000, 500] bf16 13 14 21 34 70 165 / 24 27 43 73 183 268,
+// [1, 600, 500] f32 8.4 4.8 5.3 6.1 8.9 16 / 15.5 9.6 10.2 14 21 34.
+Deal pick_deal(int64_t rows, int64_t L, bool backward) {
+    if (L <= 4 * T) return {4, 1};
+    if (L <= kRow || (L <= 4 * kRow && rows >= 4096)) return {16, 1};
+    constexpr int kWave = 64 * T;
     Deal v{64, 1};
-    while (v.waves < 16 && v.waves * 64 * T < L && rows * v.waves < 4096) v.waves *= 2;
+    while (v.waves < 16 && v.waves * kWave * (backward ? 2 : 1) < L && rows * v.waves < 4096) v.waves *= 2;
+    while (v.waves < 16 && v.waves * kWave * 8 <= L && rows * v.waves < 16384) v.waves *= 2;
     return v;
 }
 
@@ -473,14 +515,15 @@ hipError_t backward(const gated_scan_backward_args &a, hipStream_t s) {
         <<<(unsigned)((k.rows + ROWS - 1) / ROWS), kThreadsOf<LANES, W>, 0, s>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    gated_join<<<(unsigned)((a.D + 255) / 256), 256, 0, s>>>(k.params, a.dA, a.dr_bias, a.di_bias,
+    gated_join<<<(unsigned)((3 * (int64_t)a.D + 255) / 256), 256, 0, s>>>(k.params, a.dA, a.dr_bias, a.di_bias,
                                                              a.B, a.D);
     return hipGetLastError();
 }
 
 template <class E>
 hipError_t forward_any(const gated_scan_args &a, hipStream_t s) {
-    const Deal v = pick_deal((int64_t)a.B * a.D, a.L);
+    const Deal v = pick_deal((int64_t)a.B * a.D, a.L, false);
+    if (v.lanes == 4) return forward<E, 4, 1>(a, s);
     if (v.lanes == 16) return forward<E, 16, 1>(a, s);
     switch (v.waves) {
         case 1: return forward<E, 64, 1>(a, s);
@@ -493,7 +536,8 @@ hipError_t forward_any(const gated_scan_args &a, hipStream_t s) {
 
 template <class E>
 hipError_t backward_any(const gated_scan_backward_args &a, hipStream_t s) {
-    const Deal v = pick_deal((int64_t)a.B * a.D, a.L);
+    const Deal v = pick_deal((int64_t)a.B * a.D, a.L, true);
+    if (v.lanes == 4) return backward<E, 4, 1>(a, s);
     if (v.lanes == 16) return backward<E, 16, 1>(a, s);
     switch (v.waves) {
         case 1: return backward<E, 64, 1>(a, s);
@@ -508,7 +552,15 @@ template <class E>
 hipError_t step(const gated_scan_step_args &a, hipStream_t s) {
     GatedStep<E> k{view<E>(a.x), view<E>(a.r), view<E>(a.i), view<E>(a.z), view<E>(a.y), a.A,
                    a.r_bias, a.i_bias, a.state, a.slots, a.D, a.lines};
-    gated_step<E><<<dim3((unsigned)((a.D + 255) / 256), (unsigned)a.B), 256, 0, s>>>(k);
+    const bool dense = a.D % 4 == 0 && a.x.channel == 1 && a.r.channel == 1 && a.i.channel == 1 &&
+                       (a.z.channel == 1 || !a.z.data) && a.y.channel == 1;
+    // Four channels a thread where that still leaves the chip work-groups enough.
+    const int V = dense && (int64_t)a.B * a.D >= 262144 ? 4 : 1;
+    const dim3 grid((unsigned)((a.D + 256 * V - 1) / (256 * V)), (unsigned)a.B);
+    if (V == 4)
+        gated_step<E, 4><<<grid, 256, 0, s>>>(k);
+    else
+        gated_step<E, 1><<<grid, 256, 0, s>>>(k);
     return hipGetLastError();
 }
 
@@ -517,7 +569,7 @@ hipError_t step(const gated_scan_step_args &a, hipStream_t s) {
 int64_t gated_backward_workspace(int B, int D) { return (int64_t)B * D * 3 * sizeof(float); }
 
 void gated_plan(int64_t rows, int64_t L, int backward, char *buf, size_t len) {
-    const Deal v = pick_deal(rows, L);
+    const Deal v = pick_deal(rows, L, backward != 0);
     std::snprintf(buf, len, "lanes=%d waves=%d", v.lanes, v.waves);
 }
 hipError_t launch_gated_forward(const gated_scan_args &a, hipStream_t s) {
