@@ -279,7 +279,7 @@ int gated_scan_forward(const gated_scan_args *a, hipStream_t stream) {
 
 int64_t gated_scan_workspace(int32_t B, int32_t D, int32_t L) {
     if (check_sizes(SEQ_F32, B, D, L) != CONV2D_GI_OK) return -1;
-    return seq::gated_backward_workspace(B, D);
+    return seq::gated_backward_workspace(B, D, L);
 }
 
 int gated_scan_backward(const gated_scan_backward_args *a, hipStream_t stream) {
@@ -294,7 +294,7 @@ int gated_scan_backward(const gated_scan_backward_args *a, hipStream_t stream) {
     if (!is_apart(a->dx, a->B, a->D, a->L) || !is_apart(a->dr, a->B, a->D, a->L) ||
         !is_apart(a->di, a->B, a->D, a->L) || (a->dz.data && !is_apart(a->dz, a->B, a->D, a->L)))
         return CONV2D_GI_EINVAL;
-    if (!is_workspace(a->workspace, a->workspace_bytes, seq::gated_backward_workspace(a->B, a->D)))
+    if (!is_workspace(a->workspace, a->workspace_bytes, seq::gated_backward_workspace(a->B, a->D, a->L)))
         return CONV2D_GI_EINVAL;
     return status(seq::launch_gated_backward(*a, stream));
 }

@@ -30,7 +30,7 @@ int64_t norm_workspace(int B, int D, int L, int backward);
 hipError_t launch_gated_forward(const gated_scan_args &a, hipStream_t s);
 hipError_t launch_gated_backward(const gated_scan_backward_args &a, hipStream_t s);
 hipError_t launch_gated_step(const gated_scan_step_args &a, hipStream_t s);
-int64_t gated_backward_workspace(int B, int D);
+int64_t gated_backward_workspace(int B, int D, int L);  // 0: none needed
 void gated_plan(int64_t rows, int64_t L, int backward, char *buf, size_t len);
 
 hipError_t launch_quantize(const quantize_tokens_args &a, hipStream_t s);

@@ -34,7 +34,8 @@ CASES = [  # B, D, L, lengths, layout
     (3, 6, 8, "none", "dense"), (1, 17, 127, None, "padded"), (1, 33, 128, None, "slice"), (2, 5, 129, None, "swapped"),
     (7, 3, 256, "ragged", "slice"), (7, 3, 257, "ragged", "padded"), (2, 9, 511, None, "dense"), (1, 5, 513, None, "slice"),
     (3, 4, 1030, "ragged", "swapped"), (1, 3, 2049, None, "padded"), (4, 2, 4100, "ragged", "dense"),
-    (2, 1, 9001, None, "dense"),
+    (2, 1, 9001, None, "dense"), (9, 21, 33, None, "dense"), (20, 7, 5, None, "slice"), (5, 35, 31, "ragged", "padded"),
+    (7, 18, 100, "ragged", "dense"), (4, 3, 4500, "ragged", "dense"), (10, 5, 1300, None, "dense"),
 ]
 
 
@@ -101,6 +102,15 @@ def test_forward(case, dtype):
 def test_backward(case, dtype):
     s = Gated(case, dtype)
     s.check_backward(s.forward(want_checkpoints=True)[2])
+
+
+@pytest.mark.parametrize("case", [
+    # Enough rows for every way they are dealt that few rows do not have.
+    (3, 1400, 150, None, "dense"), (1, 4100, 520, None, "dense"), (2, 2100, 300, None, "padded"), (1, 1100, 4200, None, "dense")],
+    ids=str)
+def test_many_rows(case):
+    s = Gated(case, "bf16")
+    s.check_backward(s.check_forward())
 
 
 @pytest.mark.parametrize("gate,extras", [(False, True), (True, False), (False, False)])
