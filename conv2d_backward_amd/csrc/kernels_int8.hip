@@ -345,7 +345,8 @@ __device__ __forceinline__ uint4 packed(const float *v) {
 // channels (float32: 8) at a time, so that a store writes whole lines; where the positions are
 // not all in one batch item and inside its length, or channels are missing, they leave one by
 // one, a lane a position.  Returns whether that took exactly RB NB sizeof(T) / 4 stores.
-template <class E, int NB, int RB, class Sx, class Sw, class Bias, class Sum>
+// SWAPPED: the bias goes by positions.
+template <class E, int NB, int RB, bool SWAPPED, class Sx, class Sw, class Bias, class Sum>
 __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t *turn, Sx scale_of,
                                       Sw w_scale_of, Bias bias_of, Sum sum) {
     using T = typename E::type;
@@ -359,9 +360,12 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
     const bool here = at < a.N, inside = here && l < length_of(a.lengths, b, a.L);
     const int b0 = __builtin_amdgcn_readfirstlane(b);
     const bool whole = __all(inside && b == b0) && e + 16 * RB <= a.E_;
-    float sn[4 * NB];
+    float sn[4 * NB], bn[SWAPPED ? 4 * NB : 1];
 #pragma unroll
-    for (int k = 0; k < 4 * NB; ++k) sn[k] = scale_of(part * 4 * NB + k);
+    for (int k = 0; k < 4 * NB; ++k) {
+        sn[k] = scale_of(part * 4 * NB + k);
+        if constexpr (SWAPPED) bn[k] = bias_of(part * 4 * NB + k);
+    }
     // Unit u of row c is at u ^ turned(c).
     constexpr int kLine = P * (int)sizeof(T), kRows = sizeof(T) == 2 ? 16 : 8, kUnits = kLine / 16;
     constexpr int kOwn = kUnits / 4, V = 16 / (int)sizeof(T);   // units of a lane, results of a unit
@@ -386,12 +390,13 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
         __builtin_amdgcn_sched_barrier(0);
-        const float sw = w_scale_of(r * 16 + row), bias = bias_of(r * 16 + row);
-        float v[4 * NB];
+        const float sw = w_scale_of(r * 16 + row);
+        float bias = 0.f, v[4 * NB];
+        if constexpr (!SWAPPED) bias = bias_of(r * 16 + row);
 #pragma unroll
         for (int k = 0; k < 4 * NB; ++k) {
             const int one = sum(r, k);
-            v[k] = __builtin_fmaf((float)one, sn[k] * sw, bias);
+            v[k] = __builtin_fmaf((float)one, sn[k] * sw, SWAPPED ? bn[SWAPPED ? k : 0] : bias);
         }
 #pragma unroll
         for (int half = 0; half < 16 / kRows; ++half) {
@@ -437,11 +442,14 @@ __device__ __forceinline__ int position_turn(int row) {
 // the barrier that hands over a step lies between the halves, so that the matrix cores have
 // work across it.
 //
+// SWAPPED: single positions, whose results lie along the channels.  The caller gives the weights
+// as positions and the positions as weights; the bias then goes by positions.
+//
 // In LDS a row is eight 16-byte units, unit u at u ^ f(row), so that the 16 lanes that a
 // cycle of ds_read_b128 serves (rows 0..3 and 12..15 of one unit, 4..11 of its neighbour, or
 // the others) read 16 different units of 256 bytes.  Row r of block n of the positions is
 // position r / 4 * 4 NB + n * 4 + r % 4 of the wave's, which gives a lane 4 NB consecutive ones.
-template <class E, int WM, int WE, int NB, int RB, int ST>
+template <class E, int WM, int WE, int NB, int RB, int ST, bool SWAPPED>
 __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
     constexpr int kThreads = 64 * WM * WE, TM = 16 * WM * NB, TE = 16 * WE * RB;
     constexpr int kLoads = (TM + TE) * 8 / kThreads, kStage = (TM + TE) * kStep;
@@ -504,12 +512,10 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
             for (int n = 0; n < NB; ++n) o.x[n] = *reinterpret_cast<const v4i *>(x + n * 512);
         };
         const auto multiply = [&](const Operands &o) {
-            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int r = 0; r < RB; ++r) acc[r][n] = mfma16(o.x[n], o.w[r], acc[r][n]);
-            __builtin_amdgcn_s_setprio(0);
         };
         const int steps = a.K / kStep;
 #pragma unroll
@@ -546,10 +552,10 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
 
     // (every wave has read its last operands before the last barrier)
     const int n = n0 + wm * 16 * NB, e = e0 + we * 16 * RB;
-    leave<E, NB, RB>(
+    leave<E, NB, RB, SWAPPED>(
         a, n, e, smem + wave * 2048, [&](int k) { return a.scales[min(n + k, a.N - 1)]; },
         [&](int c) { return a.w_scales[min(e + c, a.E_ - 1)]; },
-        [&](int c) { return a.bias ? a.bias[min(e + c, a.E_ - 1)] : 0.f; },
+        [&](int i) { return !a.bias ? 0.f : SWAPPED ? a.bias[min(n + i, a.N - 1)] : a.bias[min(e + i, a.E_ - 1)]; },
         [&](int r, int k) { return acc[r][k / 4][k % 4]; });
 }
 
@@ -566,7 +572,7 @@ constexpr int kStreamStage = 2 * kStreamTile * kStep;
 constexpr int kStreamScales = 2 * kStreamStage, kStreamTurn = kStreamScales + 2 * 4096;
 constexpr int kStreamBytes = kStreamTurn + kStreamWaves * 2048;
 
-template <class E>
+template <class E, bool SWAPPED>
 __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E> a) {
     constexpr int NB = kStreamNB, RB = kStreamRB, TM = kStreamTile, TE = kStreamTile;
     constexpr int kThreads = 64 * kStreamWaves, kLoads = (TM + TE) * 8 / kThreads;
@@ -623,9 +629,10 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
     // Scales of the positions, scales of the channels, biases: 256 floats each, 64 a load and
     // two loads a wave (a fourth part is loaded in vain); what is past the end is 0.
     const auto stage_scales = [&](int to, const Tile &t) {
-        const int which = wave / 2;
-        const float *p = which == 0 ? a.scales + t.n0 : which == 1 || !a.bias ? a.w_scales + t.e0 : a.bias + t.e0;
-        const int held = which == 0 ? min(TM, a.N - t.n0) : which == 1 || (which == 2 && a.bias) ? min(TE, a.E_ - t.e0) : 0;
+        const int which = wave / 2, of_n = min(TM, a.N - t.n0), of_e = min(TE, a.E_ - t.e0);
+        const float *p = which == 0 ? a.scales + t.n0 : a.w_scales + t.e0;
+        int held = which == 0 ? of_n : which == 1 ? of_e : 0;
+        if (which == 2 && a.bias) p = a.bias + (SWAPPED ? t.n0 : t.e0), held = SWAPPED ? of_n : of_e;
         const auto r = rsrc(reinterpret_cast<const uint8_t *>(p), held * 4L);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -658,7 +665,6 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
     const auto multiply = [&](const Operands &o, Operands &fill, int from, int h, auto load, int to, int k) {
         constexpr bool LOAD = decltype(load)::value;
         if constexpr (LOAD) asm volatile("" : "+v"(x_from), "+v"(w_from));   // (opaque: nothing kept)
-        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < RB * NB; ++i) {
             acc[i / NB][i % NB] = mfma16(o.x[i % NB], o.w[i / NB], acc[i / NB][i % NB]);
@@ -666,7 +672,6 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
             if (LOAD && i % 4 == 2) load_one(to, k, i / 4);
             __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_s_setprio(0);
     };
     static_assert(RB * NB / 2 >= NB + RB && RB * NB / 4 == kLoads, "a place for every read and load");
 
@@ -729,10 +734,10 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
             multiply(second, first, at ^ 1, 0, std::true_type{}, at, k + 2 < steps ? k + 2 : k + 2 - steps);
         }
         const float *sx = reinterpret_cast<const float *>(smem + kStreamScales + set * 4096);
-        whole_stores = leave<E, NB, RB>(
+        whole_stores = leave<E, NB, RB, SWAPPED>(
             a, now.n0 + wm * 64, now.e0 + we * 128, smem + kStreamTurn + wave * 2048,
             [&](int k) { return sx[wm * 64 + k]; }, [&](int c) { return sx[256 + we * 128 + c]; },
-            [&](int c) { return sx[512 + we * 128 + c]; }, [&](int r, int k) { return acc[r][k / 4][k % 4]; });
+            [&](int i) { return sx[512 + (SWAPPED ? wm * 64 : we * 128) + i]; }, [&](int r, int k) { return acc[r][k / 4][k % 4]; });
         now = next;
         set ^= 1;
     }
@@ -744,18 +749,17 @@ Project<E> project_of(const project_int8_args &a) {
             a.w_scales, a.bias, view<E>(a.y), a.lengths, (int)((int64_t)a.B * a.L), a.E, a.L, a.K, 0, 0};
 }
 
-template <class E, int WM, int WE, int NB, int RB, int ST>
-hipError_t product(const project_int8_args &a, hipStream_t s) {
+template <class E, int WM, int WE, int NB, int RB, int ST, bool SWAPPED>
+hipError_t product(Project<E> k, hipStream_t s) {
     constexpr int TM = 16 * WM * NB, TE = 16 * WE * RB;
-    Project<E> k = project_of<E>(a);
-    k.n_tiles = (k.N + TM - 1) / TM, k.e_tiles = (a.E + TE - 1) / TE;
+    k.n_tiles = (k.N + TM - 1) / TM, k.e_tiles = (k.E_ + TE - 1) / TE;
     constexpr int bytes = ST * (TM + TE) * kStep;
     if (bytes > 64 * 1024) {
-        hipError_t e = hipFuncSetAttribute((const void *)project<E, WM, WE, NB, RB, ST>,
+        hipError_t e = hipFuncSetAttribute((const void *)project<E, WM, WE, NB, RB, ST, SWAPPED>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    project<E, WM, WE, NB, RB, ST>
+    project<E, WM, WE, NB, RB, ST, SWAPPED>
         <<<(unsigned)((int64_t)k.n_tiles * k.e_tiles), 64 * WM * WE, bytes, s>>>(k);
     return hipGetLastError();
 }
@@ -1028,15 +1032,15 @@ hipError_t split(const project_int8_args &a, const seq_tensor &x, int D, hipStre
     return hipGetLastError();
 }
 
-template <class E>
-hipError_t stream(const project_int8_args &a, hipStream_t s) {
-    Project<E> k = project_of<E>(a);
-    k.n_tiles = (k.N + kStreamTile - 1) / kStreamTile, k.e_tiles = (a.E + kStreamTile - 1) / kStreamTile;
-    hipError_t e = hipFuncSetAttribute((const void *)project_stream<E>,
+template <class E, bool SWAPPED>
+hipError_t stream(Project<E> k, hipStream_t s) {
+    k.n_tiles = (k.N + kStreamTile - 1) / kStreamTile, k.e_tiles = (k.E_ + kStreamTile - 1) / kStreamTile;
+    hipError_t e = hipFuncSetAttribute((const void *)project_stream<E, SWAPPED>,
                                        hipFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t)k.n_tiles * k.e_tiles;
-    project_stream<E><<<(unsigned)std::min<int64_t>(tiles, 256), 64 * kStreamWaves, kStreamBytes, s>>>(k);
+    project_stream<E, SWAPPED>
+        <<<(unsigned)std::min<int64_t>(tiles, 256), 64 * kStreamWaves, kStreamBytes, s>>>(k);
     return hipGetLastError();
 }
 
@@ -1049,15 +1053,28 @@ hipError_t split_any(const project_int8_args &a, hipStream_t s) {
     return split<E, 2, 4, 8, 1, FORM>(a, {}, 0, s);
 }
 
+template <class E, bool SWAPPED>
+hipError_t tiles_any(const Project<E> &k, hipStream_t s) {
+    const auto tiles = [&](int64_t t) { return (k.N + t - 1) / t * ((k.E_ + t - 1) / t); };
+    if (tiles(256) >= 192 && k.K >= 2 * kStep) return stream<E, SWAPPED>(k, s);
+    if (tiles(128) >= 192) return product<E, 2, 4, 4, 2, 2, SWAPPED>(k, s);
+    return product<E, 2, 2, 2, 2, 3, SWAPPED>(k, s);
+}
+
 template <class E>
 hipError_t product_any(const project_int8_args &a, hipStream_t s) {
-    const int64_t N = (int64_t)a.B * a.L;
-    const auto tiles = [&](int64_t t) { return (N + t - 1) / t * ((a.E + t - 1) / t); };
-    if (N <= 64 || tiles(64) <= 128)
+    Project<E> k = project_of<E>(a);
+    if (k.N <= 64 || (int64_t)((k.N + 63) / 64) * ((a.E + 63) / 64) <= 128)
         return a.L == 1 ? split_any<E, kAlongChannels>(a, s) : split_any<E, kAlongPositions>(a, s);
-    if (tiles(256) >= 192 && a.K >= 2 * kStep) return stream<E>(a, s);
-    if (tiles(128) >= 192) return product<E, 2, 4, 4, 2, 2>(a, s);
-    return product<E, 2, 2, 2, 2, 3>(a, s);
+    if (a.L > 1 || a.lengths || a.y.channel != 1) return tiles_any<E, false>(k, s);
+    // One position a row, results along the channels: they are the positions of one batch item.
+    std::swap(k.codes, k.w);
+    std::swap(k.scales, k.w_scales);
+    std::swap(k.N, k.E_);
+    k.L = k.N;
+    k.y.channel = k.y.batch;
+    k.y.batch = 0;
+    return tiles_any<E, true>(k, s);
 }
 
 int64_t code_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ_INT8_ROW; }

@@ -192,7 +192,8 @@ def test_largest_sums():
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("B,D,E", [(1, 1, 1), (1, 64, 70), (3, 130, 33), (8, 2048, 300), (16, 1000, 515), (17, 300, 64),
                                    (33, 515, 100), (64, 128, 2000), (65, 700, 130), (130, 260, 400), (2, 4100, 1030),
-                                   (16, 9000, 20)])
+                                   (16, 9000, 20), (300, 260, 2100), (1100, 128, 1500), (2100, 300, 6300),
+                                   (500, 64, 3300), (2100, 128, 1800)])
 def test_step(B, D, E, dtype):
     """One call is the two calls, bit for bit, whatever the strides."""
     i = Inputs(B + D + E, dtype)
