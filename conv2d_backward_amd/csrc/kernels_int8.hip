@@ -1057,7 +1057,7 @@ template <class E, bool SWAPPED>
 hipError_t tiles_any(const Project<E> &k, hipStream_t s) {
     const auto tiles = [&](int64_t t) { return (k.N + t - 1) / t * ((k.E_ + t - 1) / t); };
     if (tiles(256) >= 192 && k.K >= 2 * kStep) return stream<E, SWAPPED>(k, s);
-    if (tiles(128) >= 192) return product<E, 2, 4, 4, 2, 2, SWAPPED>(k, s);
+    if (tiles(128) >= 208) return product<E, 2, 4, 4, 2, 2, SWAPPED>(k, s);
     return product<E, 2, 2, 2, 2, 3, SWAPPED>(k, s);
 }
 
