@@ -791,7 +791,8 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lanes) {
 // consecutive rows of it.  Along channels (one position a row), the weights.  Along
 // positions, the positions, in the order that gives a lane 4 NB consecutive ones.  With
 // codes inside (at most 16 positions, along channels) they are made here, from x, by every
-// work-group for itself, and wait in LDS, unit u of row r at u ^ r in each 256 bytes.
+// work-group for itself, and wait in LDS, unit u of row r at u ^ r in each 256 bytes; the
+// operand's rows without a position are the last one again.
 enum Form { kAlongChannels, kCodesInside, kAlongPositions };
 
 template <class E>
@@ -813,7 +814,7 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
     uint8_t *const ring = smem + wave * kRing;
     v4i *const meet = reinterpret_cast<v4i *>(smem);   // after the rings
     float *const own_scales = reinterpret_cast<float *>(smem + S * (kRing > kMeet ? kRing : kMeet));
-    uint8_t *const own = reinterpret_cast<uint8_t *>(own_scales + 64);   // [16][pitch]
+    uint8_t *const own = reinterpret_cast<uint8_t *>(own_scales + 64);   // [N][pitch]
     const int pitch = (a.K + 255) / 256 * 256;
     // Work-groups of the same positions or, where there are more of those, channels follow
     // each other on one die.
@@ -918,6 +919,8 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
         for (int n = 0; n < NB; ++n) acc[r][n] = v4i{0, 0, 0, 0};
     // Along positions, row r of block n is position r / 4 * 4 NB + n * 4 + r % 4.
     const int x_row = FORM == kAlongPositions ? row / 4 * 4 * NB + row % 4 : row;
+    const int held = min(row, a.N - 1);
+    const uint8_t *const own_at = own + held * pitch;
     for (int j = 0; j < mine; ++j) {
         // Step j is there: all but the DEPTH - 1 behind it, or, at the end, all.
         if (mine - j >= DEPTH)
@@ -938,7 +941,7 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
                 const int xn = x_row + n * (FORM == kAlongPositions ? 4 : 16);
                 const int turned = u ^ (FORM == kAlongPositions ? position_turn<NB>(xn) : xn / 2 % 8);
                 fx[n][h] = *reinterpret_cast<const v4i *>(
-                    CODES ? own + row * pitch + ((place(j) * 8 + u) ^ row) * 16
+                    CODES ? own_at + ((place(j) * 8 + u) ^ held) * 16
                           : at + (RB * 16 + xn) * kStep + turned * 16);
             }
         }
@@ -1021,7 +1024,7 @@ hipError_t split(const project_int8_args &a, const seq_tensor &x, int D, hipStre
     if constexpr (CODES)
         while (k.share < 64 * S && 64 * S / k.share / 2 >= k.p.N) k.share *= 2;
     constexpr int kRing = DEPTH * 16 * (RB + (CODES ? 0 : NB)) * kStep, kMeet = RB * NB * 1024;
-    const int bytes = S * std::max(kRing, kMeet) + 256 + (CODES ? 16 * ((a.K + 255) / 256 * 256) : 0);
+    const int bytes = S * std::max(kRing, kMeet) + 256 + (CODES ? k.p.N * ((a.K + 255) / 256 * 256) : 0);
     if (bytes > 64 * 1024) {
         hipError_t e = hipFuncSetAttribute((const void *)project_split<E, RB, NB, S, DEPTH, FORM>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1082,7 +1085,7 @@ int64_t code_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ
 // Whether every work-group makes the codes of a single-position call for itself: at most 16
 // rows, few enough numbers, and room in LDS for their codes.
 bool codes_inside(int64_t B, int64_t D) {
-    return B <= 16 && B * D <= 32768 && D <= 8192;
+    return B <= 16 && B * D <= 32768;
 }
 
 template <class E>

@@ -214,6 +214,20 @@ def test_step(B, D, E, dtype):
     assert torch.equal(gi.project_int8_step(x, w, ws), gi.project_int8(codes, scales, w, ws, dtype=i.dtype)[..., 0])
 
 
+@pytest.mark.parametrize("B,D,E", [(1, 8192, 5000), (4, 8192, 300), (1, 8150, 9), (3, 10900, 4100), (2, 16384, 4097),
+                                   (1, 32768, 600), (1, 32769, 40), (16, 2048, 4099), (5, 6500, 70)])
+def test_step_of_few_long_rows(B, D, E):
+    """Codes of all channels of a few rows, made inside the product or before it."""
+    i = Inputs(B + D + E, "bf16")
+    w, ws = gi.quantize_weight(i.normal(E, D))
+    x = i.normal(B, D)
+    want = gi.project_int8(*gi.quantize_tokens(x.unsqueeze(2)), w, ws, dtype=i.dtype)[..., 0]
+    assert torch.equal(gi.project_int8_step(x, w, ws), want)
+    wide = i.normal(B, 2 * D + 1)
+    wide[:, 1::2] = x
+    assert torch.equal(gi.project_int8_step(wide[:, 1::2], w, ws), want)
+
+
 def test_step_with_rows_that_are_no_numbers():
     i = Inputs(2, "bf16")
     w, ws = gi.quantize_weight(i.normal(40, 300))
