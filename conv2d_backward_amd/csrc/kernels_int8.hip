@@ -101,7 +101,8 @@ struct Quantize {
 // waves V of them (16 bytes) and four channels at a time, 256 W / G channels in a round.  The
 // first KEPT rounds stay in registers between the two passes, over the maximum and over the
 // codes; what is beyond is read again.  With G = 4 a wave's loads are 64 bytes of 16
-// channels, its stores 64 bytes of codes of 4 positions.
+// channels, its stores 64 bytes of codes of 4 positions.  Bound by memory: [1, 4096, 8192]
+// bf16 23.7 us, 4.25 TB/s of the 4.85 that a copy reaches, [4, 2048, 2048] 13.5 us.
 template <class E, int G, int W, int KEPT>
 __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
     using T = typename E::type;
@@ -203,7 +204,8 @@ __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
     }
 }
 
-// Channels along the lanes (one position, contiguous channels): a work-group a row.
+// Channels along the lanes (one position, contiguous channels): a work-group a row.  Two round
+// trips and the launch: [64, 4096] bf16 3.0 us.
 template <class E>
 __global__ __launch_bounds__(256) void quantize_row(Quantize<E> a) {
     __shared__ uint32_t meet[4];
@@ -344,8 +346,9 @@ __device__ __forceinline__ uint4 packed(const float *v) {
 // a lane has for position part * 4 NB + k and channel r * 16 + row.  They turn in `turn`, 16
 // channels (float32: 8) at a time, so that a store writes whole lines; where the positions are
 // not all in one batch item and inside its length, or channels are missing, they leave one by
-// one, a lane a position.  Returns whether that took exactly RB NB sizeof(T) / 4 stores.
-// SWAPPED: the bias goes by positions.
+// one, a lane a position, all of them read before the first leaves (3000 positions, 1024 -> 4096
+// channels in tiles of 256: 20.5 us; read one by one 27.5).  Returns whether that took exactly
+// RB NB sizeof(T) / 4 stores.  SWAPPED: the bias goes by positions.
 template <class E, int NB, int RB, bool SWAPPED, class Sx, class Sw, class Bias, class Sum>
 __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t *turn, Sx scale_of,
                                       Sw w_scale_of, Bias bias_of, Sum sum) {
@@ -383,7 +386,8 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
         const unsigned c = i * kPart + lane / kUnits;
         get[i] = turn + c * kLine + (lane % kUnits ^ turned(c)) * 16;
     }
-    T *y = a.y.row(b, e) + l;   // (not followed where there is no position)
+    // (not followed where there is no position)
+    T *y = a.y.row(b, e + lane / P) + l;
     if (whole)
         y = a.y.row(b0, e + lane / kUnits) + __builtin_amdgcn_readfirstlane(l) + lane % kUnits * V;
     const int64_t channel = a.y.channel;
@@ -414,12 +418,22 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
                     *reinterpret_cast<Words *>(y + (c0 + i * kPart) * channel) = Words{o.x, o.y, o.z, o.w};
                 }
             } else {
-                constexpr int kSide = 64 / P;   // channels at once
-#pragma unroll 1
-                for (int c = lane / P; c < min(kRows, a.E_ - e - c0); c += kSide) {
-                    const T o = *reinterpret_cast<const T *>(
+                // kSide channels at once, kSome of a lane.
+                constexpr int kSide = 64 / P, kSome = kRows / kSide;
+                const int first = lane / P, rows = a.E_ - e - c0;
+                T o[kSome], *to = y + c0 * channel;
+#pragma unroll
+                for (int i = 0; i < kSome; ++i) {
+                    const int c = first + i * kSide;
+                    o[i] = *reinterpret_cast<const T *>(
                         turn + c * kLine + ((lane % P / V) ^ turned(c)) * 16 + lane % V * sizeof(T));
-                    if (here) y[(c0 + c) * channel] = inside ? o : (T)0;
+                }
+                if (here) {
+#pragma unroll
+                    for (int i = 0; i < kSome; ++i, to += kSide * channel) {
+                        asm volatile("" : "+v"(to));   // (opaque: all addresses would be kept)
+                        if (first + i * kSide < rows) *to = inside ? o[i] : (T)0;
+                    }
                 }
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -441,6 +455,11 @@ __device__ __forceinline__ int position_turn(int row) {
 // 64 bytes; the operands of a half are read while the products of the one before run, and
 // the barrier that hands over a step lies between the halves, so that the matrix cores have
 // work across it.
+//
+// What bounds it: a step's way from the caches through LDS, which a compute unit hides with what
+// other work-groups it has (tiles of 64: three).  [5, 1000, 301] x 2000 bf16 9.1 us, [2, 2051, 777]
+// x 1027 f32 10.2 us, 650 TOP/s both.  Two groups of waves that share the steps of a tile, with
+// half as many barriers: 11.6 and 10.4.
 //
 // SWAPPED: single positions, whose results lie along the channels.  The caller gives the weights
 // as positions and the positions as weights; the bias then goes by positions.
@@ -555,16 +574,20 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
     leave<E, NB, RB, SWAPPED>(
         a, n, e, smem + wave * 2048, [&](int k) { return a.scales[min(n + k, a.N - 1)]; },
         [&](int c) { return a.w_scales[min(e + c, a.E_ - 1)]; },
-        [&](int i) { return !a.bias ? 0.f : SWAPPED ? a.bias[min(n + i, a.N - 1)] : a.bias[min(e + i, a.E_ - 1)]; },
+        [&](int i) {
+            return !a.bias ? 0.f : SWAPPED ? a.bias[min(n + i, a.N - 1)] : a.bias[min(e + i, a.E_ - 1)];
+        },
         [&](int r, int k) { return acc[r][k / 4][k % 4]; });
 }
 
 // The same for products that fill the chip: tiles of 256 x 256, one work-group a compute
 // unit, which goes through its tiles as one stream of steps: the first steps of the next tile
 // are on their way before the last products of this one, and the results leave while they
-// come.  A tile by a work-group of its own takes 14.6 us beside its steps ([1, 4096, 8192] x
-// 8192: 250 us in all).  The results of 16 channels at a time turn in LDS, so that a store
-// writes whole lines (16-bit results; float32's leave as they lie).
+// come.  [1, 4096, 8192] x 8192 bf16: 207 us, 2660 TOP/s (a tile by a work-group of its own: 250
+// us); 8192 x 8192 x 8192: 387 us, 2840 TOP/s, where the library's product with int32 results
+// takes 467.  What bounds it: power.  A step takes 1.33 us on numbers that use all bits and 1.13
+// on zeros, at the clock of which the matrix cores alone would need 0.85; the results of a tile take
+// 2.9 us beside the steps.
 constexpr int kStreamWM = 4, kStreamWE = 2, kStreamNB = 4, kStreamRB = 8;
 constexpr int kStreamTile = 256, kStreamWaves = kStreamWM * kStreamWE;
 constexpr int kStreamStage = 2 * kStreamTile * kStep;
@@ -660,8 +683,7 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
     v4i acc[RB][NB];
     // The products of a half.  Among them, a few apart, go the reads of the half after it and,
     // LOAD, the loads of a step: all at once they would fill the queues in front of the LDS and
-    // the caches, and the products behind them would wait ([1, 4096, 8192] x 8192 in steps of
-    // 1.6 us for 1.4).
+    // the caches, and the products behind them would wait (a step 1.6 us for 1.4).
     const auto multiply = [&](const Operands &o, Operands &fill, int from, int h, auto load, int to, int k) {
         constexpr bool LOAD = decltype(load)::value;
         if constexpr (LOAD) asm volatile("" : "+v"(x_from), "+v"(w_from));   // (opaque: nothing kept)
@@ -737,7 +759,8 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
         whole_stores = leave<E, NB, RB, SWAPPED>(
             a, now.n0 + wm * 64, now.e0 + we * 128, smem + kStreamTurn + wave * 2048,
             [&](int k) { return sx[wm * 64 + k]; }, [&](int c) { return sx[256 + we * 128 + c]; },
-            [&](int i) { return sx[512 + (SWAPPED ? wm * 64 : we * 128) + i]; }, [&](int r, int k) { return acc[r][k / 4][k % 4]; });
+            [&](int i) { return sx[512 + (SWAPPED ? wm * 64 : we * 128) + i]; },
+            [&](int r, int k) { return acc[r][k / 4][k % 4]; });
         now = next;
         set ^= 1;
     }
@@ -782,10 +805,14 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lanes) {
 
 // Products too small to fill the chip with whole rows of k: a work-group has RB blocks of 16
 // channels and NB of 16 positions, and its S waves share k by steps of 128 bytes, wave w with
-// every S-th; their sums meet in LDS.  Each wave brings its steps by direct loads through a
-// ring of DEPTH steps of its own, without a barrier: lanes 8 to a row, because loads straight
-// into operands (each lane another row) reach 9.4 TB/s from the caches where these reach 28.
-// Rows are swizzled as in `project`.
+// every S-th; their sums meet in LDS.  Each wave brings its steps by direct loads to a place of
+// its own, without a barrier: lanes 8 to a row, because loads straight into operands (each lane
+// another row) reach 9.4 TB/s from the caches where these reach 28.  The next step is on its way
+// while this one's products run; one more ahead was slower ([32, 4096] x 8192 9.1 us for 8.0,
+// [8, 2048] x 4096 3.33 for 3.30): fewer work-groups share a compute unit.
+// Rows are swizzled as in `project`.  Bound by memory where the weights are many ([64, 4096] x 8192
+// bf16 8.1 us, 4.3 TB/s with all of its operands), else by the chain of launch, one round trip
+// to memory, one through LDS and the sums' meeting ([8, 2048] x 4096 3.2 us).
 //
 // What the results are laid out along decides which operand is the first: a lane has four
 // consecutive rows of it.  Along channels (one position a row), the weights.  Along
@@ -802,18 +829,18 @@ struct Split {
     int D, share;
 };
 
-template <class E, int RB, int NB, int S, int DEPTH, int FORM>
+template <class E, int RB, int NB, int S, int FORM>
 __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
     constexpr bool CODES = FORM == kCodesInside;
     static_assert(!CODES || NB == 1, "the codes of 16 rows");
-    constexpr int ROWS = 16 * (RB + (CODES ? 0 : NB)), kLoads = ROWS / 8, kEntry = ROWS * kStep;
+    constexpr int ROWS = 16 * (RB + (CODES ? 0 : NB)), kLoads = ROWS / 8;
     const Project<E> &a = t.p;
     extern __shared__ uint8_t smem[];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
-    constexpr int kRing = DEPTH * kEntry, kMeet = RB * NB * 1024;   // bytes of a wave
-    uint8_t *const ring = smem + wave * kRing;
-    v4i *const meet = reinterpret_cast<v4i *>(smem);   // after the rings
-    float *const own_scales = reinterpret_cast<float *>(smem + S * (kRing > kMeet ? kRing : kMeet));
+    constexpr int kPlace = ROWS * kStep, kMeet = RB * NB * 1024;   // bytes of a wave
+    uint8_t *const here = smem + wave * kPlace;
+    v4i *const meet = reinterpret_cast<v4i *>(smem);   // after the steps
+    float *const own_scales = reinterpret_cast<float *>(smem + S * std::max(kPlace, kMeet));
     uint8_t *const own = reinterpret_cast<uint8_t *>(own_scales + 64);   // [N][pitch]
     const int pitch = (a.K + 255) / 256 * 256;
     // Work-groups of the same positions or, where there are more of those, channels follow
@@ -864,19 +891,17 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
 #pragma unroll
     for (int p = 0; p < kLoads; ++p) {
         const int r = p * 8 + lane / 8;
-        const int unit = lane % 8 ^ (FORM == kAlongPositions && r >= 16 * RB ? position_turn<NB>(r - 16 * RB) : r / 2 % 8);
+        const int unit = lane % 8 ^ (FORM == kAlongPositions && r >= 16 * RB
+                                         ? position_turn<NB>(r - 16 * RB) : r / 2 % 8);
         const int held = r < 16 * RB ? min(r, a.E_ - e0 - 1) : min(r - 16 * RB, a.N - n0 - 1);
         from[p] = held * a.K + unit * 16;
     }
     const auto bring = [&](int j) {
 #pragma unroll
         for (int p = 0; p < kLoads; ++p)
-            load_lds(p < 2 * RB ? wr : xr, ring + j % DEPTH * kEntry + p * 1024, from[p],
-                     place(j) * kStep);
+            load_lds(p < 2 * RB ? wr : xr, here + p * 1024, from[p], place(j) * kStep);
     };
-#pragma unroll
-    for (int j = 0; j < DEPTH; ++j)
-        if (j < mine) bring(j);
+    if (mine > 0) bring(0);
 
     if constexpr (CODES) {
         uint32_t most = 0;
@@ -922,19 +947,14 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
     const int held = min(row, a.N - 1);
     const uint8_t *const own_at = own + held * pitch;
     for (int j = 0; j < mine; ++j) {
-        // Step j is there: all but the DEPTH - 1 behind it, or, at the end, all.
-        if (mine - j >= DEPTH)
-            wait_loads<(DEPTH - 1) * kLoads>();
-        else
-            wait_loads<0>();
-        const uint8_t *at = ring + j % DEPTH * kEntry;
+        wait_loads<0>();
         v4i fw[RB][2], fx[NB][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int u = h * 4 + part;
 #pragma unroll
             for (int r = 0; r < RB; ++r)
-                fw[r][h] = *reinterpret_cast<const v4i *>(at + (r * 16 + row) * kStep +
+                fw[r][h] = *reinterpret_cast<const v4i *>(here + (r * 16 + row) * kStep +
                                                           (u ^ (row / 2 % 8)) * 16);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
@@ -942,12 +962,12 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
                 const int turned = u ^ (FORM == kAlongPositions ? position_turn<NB>(xn) : xn / 2 % 8);
                 fx[n][h] = *reinterpret_cast<const v4i *>(
                     CODES ? own_at + ((place(j) * 8 + u) ^ held) * 16
-                          : at + (RB * 16 + xn) * kStep + turned * 16);
+                          : here + (RB * 16 + xn) * kStep + turned * 16);
             }
         }
-        if (j + DEPTH < mine) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the ring's place is read
-            bring(j + DEPTH);
+        if (j + 1 < mine) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this one is read
+            bring(j + 1);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -1016,21 +1036,21 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
     }
 }
 
-template <class E, int RB, int NB, int S, int DEPTH, int FORM>
+template <class E, int RB, int NB, int S, int FORM>
 hipError_t split(const project_int8_args &a, const seq_tensor &x, int D, hipStream_t s) {
     constexpr bool CODES = FORM == kCodesInside;
     Split<E> k{project_of<E>(a), view<E>(x), D, 64 * S / 16};
     k.p.n_tiles = (k.p.N + 16 * NB - 1) / (16 * NB), k.p.e_tiles = (a.E + 16 * RB - 1) / (16 * RB);
     if constexpr (CODES)
         while (k.share < 64 * S && 64 * S / k.share / 2 >= k.p.N) k.share *= 2;
-    constexpr int kRing = DEPTH * 16 * (RB + (CODES ? 0 : NB)) * kStep, kMeet = RB * NB * 1024;
-    const int bytes = S * std::max(kRing, kMeet) + 256 + (CODES ? k.p.N * ((a.K + 255) / 256 * 256) : 0);
+    constexpr int kPlace = 16 * (RB + (CODES ? 0 : NB)) * kStep, kMeet = RB * NB * 1024;
+    const int bytes = S * std::max(kPlace, kMeet) + 256 + (CODES ? k.p.N * ((a.K + 255) / 256 * 256) : 0);
     if (bytes > 64 * 1024) {
-        hipError_t e = hipFuncSetAttribute((const void *)project_split<E, RB, NB, S, DEPTH, FORM>,
+        hipError_t e = hipFuncSetAttribute((const void *)project_split<E, RB, NB, S, FORM>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    project_split<E, RB, NB, S, DEPTH, FORM>
+    project_split<E, RB, NB, S, FORM>
         <<<(unsigned)((int64_t)k.p.n_tiles * k.p.e_tiles), 64 * S, bytes, s>>>(k);
     return hipGetLastError();
 }
@@ -1047,27 +1067,48 @@ hipError_t stream(Project<E> k, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Blocks of channels RB and positions NB of a work-group: the fewest whose work-groups have a
+// compute unit each, or else more of them, which read less.  Measured (us; RB NB of 1 1, 2 1 /
+// 1 2, 2 2, 2 4): [8, 2048] x 4096 3.3 3.5, [16, 8192] x 8192 12.9 12.1 / [32, 4096] x 4096 5.0
+// 5.5 6.7, [32, 4096] x 8192 8.0 7.2 8.1, [64, 4096] x 2048 5.0 5.6 6.9, [64, 1024] x 4096 3.8
+// 3.6 3.9, [64, 4096] x 8192 12.1 11.9 8.5.
 template <class E, int FORM>
 hipError_t split_any(const project_int8_args &a, hipStream_t s) {
     const int64_t N = (int64_t)a.B * a.L;
-    if (N <= 16) return a.E > 4096 ? split<E, 2, 1, 8, 2, FORM>(a, {}, 0, s) : split<E, 1, 1, 8, 2, FORM>(a, {}, 0, s);
-    if (N <= 32) return a.E > 4096 ? split<E, 2, 2, 8, 1, FORM>(a, {}, 0, s) : split<E, 1, 2, 8, 1, FORM>(a, {}, 0, s);
-    if (N <= 64 && a.E <= 2048) return split<E, 1, 2, 8, 2, FORM>(a, {}, 0, s);
-    return split<E, 2, 4, 8, 1, FORM>(a, {}, 0, s);
+    const auto fits = [&](int64_t RB, int64_t NB) {
+        return (a.E + 16 * RB - 1) / (16 * RB) * ((N + 16 * NB - 1) / (16 * NB)) <= 256;
+    };
+    if (N <= 16)
+        return fits(1, 1) ? split<E, 1, 1, 8, FORM>(a, {}, 0, s) : split<E, 2, 1, 8, FORM>(a, {}, 0, s);
+    if (fits(1, 2)) return split<E, 1, 2, 8, FORM>(a, {}, 0, s);
+    if (N <= 32 || fits(2, 2)) return split<E, 2, 2, 8, FORM>(a, {}, 0, s);
+    return split<E, 2, 4, 8, FORM>(a, {}, 0, s);
 }
 
+// Larger tiles read less, smaller ones leave fewer compute units without one.  Tiles of 256 where
+// at least two thirds of the units' turns have one; measured (us, tiles of 256 / 128, N x E from
+// K): 3300 x 4096 from 2048 (208 of 256 turns) 30 / 36, 2500 x 4096 from 1024 (160) 19.8 / 20.2,
+// 4400 x 4096 from 2048 (288 of 512) 48 / 45, 9000 x 4096 from 2048 (576 of 768) 71 / 75, 8192 x
+// 8192 from 4096 207 / 262.  Tiles of 128 from 208 on, four fifths of a turn (tiles of 128 / 64):
+// 192 tiles 11.0 / 9.2, 208 9.7 / 9.9, 256 8.8 / 11.9, 512 14.5 / 19.8.
 template <class E, bool SWAPPED>
 hipError_t tiles_any(const Project<E> &k, hipStream_t s) {
     const auto tiles = [&](int64_t t) { return (k.N + t - 1) / t * ((k.E_ + t - 1) / t); };
-    if (tiles(256) >= 192 && k.K >= 2 * kStep) return stream<E, SWAPPED>(k, s);
+    const int64_t large = tiles(256), places = (large + 255) / 256 * 256;
+    if (large * 3 >= places * 2 && k.K >= 2 * kStep) return stream<E, SWAPPED>(k, s);
     if (tiles(128) >= 208) return product<E, 2, 4, 4, 2, 2, SWAPPED>(k, s);
     return product<E, 2, 2, 2, 2, 3, SWAPPED>(k, s);
 }
 
+// k is shared out where tiles of whole rows would leave half of the chip without one, and for up to
+// 32 positions, half a tile (us, shared / tiles of 64): 500 x 1024 from 1024 (128 tiles) 4.8 / 5.4,
+// 200 x 2048 from 2048 (128) 6.6 / 7.2, 120 x 4096 from 4096 (128) 9.3 / 11.2, 700 x 1500 from 300 (264)
+// 8.4 / 5.3, 300 x 4096 from 4096 (320) 22 / 13.6, 64 x 16384 from 4096 (256) 17.6 / 16.2; 17 x 65536 from 4096
+// 50 / 63.
 template <class E>
 hipError_t product_any(const project_int8_args &a, hipStream_t s) {
     Project<E> k = project_of<E>(a);
-    if (k.N <= 64 || (int64_t)((k.N + 63) / 64) * ((a.E + 63) / 64) <= 128)
+    if (k.N <= 32 || (int64_t)((k.N + 63) / 64) * ((a.E + 63) / 64) <= 128)
         return a.L == 1 ? split_any<E, kAlongChannels>(a, s) : split_any<E, kAlongPositions>(a, s);
     if (a.L > 1 || a.lengths || a.y.channel != 1) return tiles_any<E, false>(k, s);
     // One position a row, results along the channels: they are the positions of one batch item.
@@ -1082,8 +1123,11 @@ hipError_t product_any(const project_int8_args &a, hipStream_t s) {
 
 int64_t code_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ_INT8_ROW; }
 
-// Whether every work-group makes the codes of a single-position call for itself: at most 16
-// rows, few enough numbers, and room in LDS for their codes.
+// Whether every work-group makes the codes of a single-position call for itself: one block of
+// positions, and few enough numbers to stay in registers in between (us, made inside / by a
+// kernel before it): [8, 2048] x 4096 5.5 / 5.8, [1, 8192] x 4096 8.7 / 11.3, [1, 32768] x 4096
+// 27.9 / 36.1, [16, 2048] x 2048 6.0 / 5.8, [16, 2048] x 8192 7.9 / 7.5, [8, 4096] x 8192 10.0 /
+// 10.4, beside the host's time for a second launch.
 bool codes_inside(int64_t B, int64_t D) {
     return B <= 16 && B * D <= 32768;
 }
@@ -1094,8 +1138,8 @@ hipError_t step(const project_int8_step_args &a, hipStream_t s) {
     p.dtype = a.dtype, p.B = a.B, p.E = a.E, p.L = 1, p.K = a.K;
     p.w = a.w, p.w_scales = a.w_scales, p.bias = a.bias, p.y = a.y;
     if (codes_inside(a.B, a.D))
-        return a.E > 4096 ? split<E, 2, 1, 8, 2, kCodesInside>(p, a.x, a.D, s)
-                          : split<E, 1, 1, 8, 2, kCodesInside>(p, a.x, a.D, s);
+        return a.E > 4096 ? split<E, 2, 1, 8, kCodesInside>(p, a.x, a.D, s)
+                          : split<E, 1, 1, 8, kCodesInside>(p, a.x, a.D, s);
     quantize_tokens_args q = {};
     q.dtype = a.dtype, q.B = a.B, q.D = a.D, q.L = 1, q.K = a.K, q.x = a.x;
     q.codes = a.workspace;

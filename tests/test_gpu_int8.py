@@ -193,7 +193,7 @@ def test_largest_sums():
 @pytest.mark.parametrize("B,D,E", [(1, 1, 1), (1, 64, 70), (3, 130, 33), (8, 2048, 300), (16, 1000, 515), (17, 300, 64),
                                    (33, 515, 100), (64, 128, 2000), (65, 700, 130), (130, 260, 400), (2, 4100, 1030),
                                    (16, 9000, 20), (300, 260, 2100), (1100, 128, 1500), (2100, 300, 6300),
-                                   (500, 64, 3300), (2100, 128, 1800)])
+                                   (500, 64, 3300), (2100, 128, 1800), (40, 130, 8500), (32, 256, 8300)])
 def test_step(B, D, E, dtype):
     """One call is the two calls, bit for bit, whatever the strides."""
     i = Inputs(B + D + E, dtype)
@@ -282,6 +282,50 @@ def test_graph_replays_and_streams():
         want = everything()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("B,D,E,L", [(1, 600, 4096, 3000), (2, 300, 2100, 1000), (3, 1000, 515, 301), (1, 900, 1000, 90),
+                                     (900, 128, 1500, 1), (5, 6500, 70, 1), (3000, 300, 4097, 1)])
+def test_every_size_of_tiles_replays_and_runs_beside_another(B, D, E, L):
+    """Captured and replayed, and on two streams at once."""
+    i = Inputs(B + D + E, "bf16")
+    x, w, ws = i.normal(B, D, L), *gi.quantize_weight(i.normal(E, D))
+    other = i.normal(B, D, L)
+
+    def everything(x, **k):
+        y = gi.project_int8(*gi.quantize_tokens(x, **k), w, ws, dtype=torch.bfloat16, **k)
+        return [y] + ([gi.project_int8_step(x[..., 0], w, ws, **k)] if L == 1 else [])
+
+    want, want_other = everything(x), everything(other)
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for side in sides:
+        side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got, got_other = everything(x, stream=sides[0]), everything(other, stream=sides[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got + got_other, want + want_other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=sides[0]):
+        got = everything(x)
+    for _ in range(3):
+        x.copy_(other)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want_other))
+        other.mul_(-0.5)
+        want_other = everything(other)
+
+
+@pytest.mark.parametrize("E,L", [(40, 70), (300, 1000), (4096, 1600)])
+def test_results_beyond_32_bits(E, L):
+    i = Inputs(5, "bf16")
+    codes, scales = gi.quantize_tokens(i.normal(2, 300, L))
+    w, ws = gi.quantize_weight(i.normal(E, 300))
+    want = gi.project_int8(codes, scales, w, ws, dtype=torch.bfloat16)
+    far = torch.empty(2 ** 31 + 2 * E * L, dtype=torch.bfloat16, device="cuda")
+    out = far.as_strided((2, E, L), (2 ** 31 + 100, L, 1))
+    gi.project_int8(codes, scales, w, ws, out=out)
+    assert torch.equal(out, want)
 
 
 def test_offsets_beyond_32_bits():
