@@ -97,6 +97,52 @@ struct Quantize {
     int B, D, L, K, tiles;
 };
 
+// V positions from t of channel d, `left` of them inside the length: what is not is 0.
+template <class E, int V>
+__device__ __forceinline__ typename Vec<typename E::type, V>::type positions_of(
+    const Quantize<E> &a, int b, int d, int t, int left) {
+    using T = typename E::type;
+    typedef typename Vec<T, V>::type Some;
+    Some v;
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = 0;
+    if (d < a.D && left > 0) {
+        const T *p = a.x.row(b, d) + t;
+        if (left >= V) {
+            v = *reinterpret_cast<const Some *>(p);
+        } else {
+            T u[V];
+            load_end(p, left, u);
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = u[k];
+        }
+    }
+    return v;
+}
+// 16 bytes of them into four words of maxima.
+template <class E, int V>
+__device__ __forceinline__ void see_positions(const typename Vec<typename E::type, V>::type &v,
+                                              uint32_t (&words)[4]) {
+    const v4i bits = __builtin_bit_cast(v4i, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int word = bits[k];
+        words[k] = raise(words[k], word, E{});
+    }
+}
+// Four channels of position k, as codes.
+template <class E, int V>
+__device__ __forceinline__ uint32_t codes_of(const typename Vec<typename E::type, V>::type (&v)[4], int k,
+                                             const Coder &c) {
+    uint32_t n[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const typename E::type e = v[j][k];
+        n[j] = code<E>(E::up(e), c);
+    }
+    return pack(n, c.keep);
+}
+
 // Positions along the lanes.  A work-group has 16 G bytes of positions, each thread of its W
 // waves V of them (16 bytes) and four channels at a time, 256 W / G channels in a round.  The
 // first KEPT rounds stay in registers between the two passes, over the maximum and over the
@@ -114,23 +160,7 @@ __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
     const int len = length_of(a.lengths, b, a.L);
     const int group = threadIdx.x % G, quad = threadIdx.x / G, t = t0 + group * V;
     const int left = len - t;
-    const auto load = [&](int d) {
-        Some v;
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = 0;
-        if (d < a.D && left > 0) {
-            const T *p = a.x.row(b, d) + t;
-            if (left >= V) {
-                v = *reinterpret_cast<const Some *>(p);
-            } else {
-                T u[V];
-                load_end(p, left, u);
-#pragma unroll
-                for (int k = 0; k < V; ++k) v[k] = u[k];
-            }
-        }
-        return v;
-    };
+    const auto load = [&](int d) { return positions_of<E, V>(a, b, d, t, left); };
     Some kept[KEPT][4];
 #pragma unroll
     for (int r = 0; r < KEPT; ++r)
@@ -138,24 +168,16 @@ __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
         for (int j = 0; j < 4; ++j) kept[r][j] = load(r * kRound + quad * 4 + j);
     // Four words of V positions each.
     uint32_t words[4] = {0, 0, 0, 0};
-    const auto see = [&](const Some &v) {
-        const v4i bits = __builtin_bit_cast(v4i, v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int word = bits[k];
-            words[k] = raise(words[k], word, E{});
-        }
-    };
 #pragma unroll
     for (int r = 0; r < KEPT; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) see(kept[r][j]);
+        for (int j = 0; j < 4; ++j) see_positions<E, V>(kept[r][j], words);
     for (int d = KEPT * kRound + quad * 4; d < a.D; d += kRound) {
         Some v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = load(d + j);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) see(v[j]);
+        for (int j = 0; j < 4; ++j) see_positions<E, V>(v[j], words);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -181,15 +203,8 @@ __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
     uint32_t *codes = a.codes + ((int64_t)b * a.L + t) * (a.K / 4);
     const auto write = [&](int d, const Some (&v)[4]) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            uint32_t n[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const T e = v[j][k];
-                n[j] = code<E>(E::up(e), c[k]);
-            }
-            if (t + k < a.L) codes[k * (a.K / 4) + d / 4] = pack(n, c[k].keep);
-        }
+        for (int k = 0; k < V; ++k)
+            if (t + k < a.L) codes[k * (a.K / 4) + d / 4] = codes_of<E, V>(v, k, c[k]);
     };
 #pragma unroll
     for (int r = 0; r < KEPT; ++r) {
@@ -202,6 +217,83 @@ __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
         for (int j = 0; j < 4; ++j) v[j] = load(d + j);
         write(d, v);
     }
+}
+
+// Few positions with many channels: the channels are shared out too, kSlice to a work-group, and
+// two kernels run one after the other.  The first leaves the maxima of each slice where the codes
+// of the row will be: a copy of all of them in every slice's place, from where the work-groups
+// of the second, which have the same slices, take them before they write their codes over them.
+constexpr int kSlice = 512, kSliceG = 4, kSliceW = 8;
+constexpr int kMaxSlices = 32;   // copies of so many fit into the 128 bytes that the last slice may have
+static_assert(kSlice == 256 * kSliceW / kSliceG, "a slice is a round");
+
+template <class E, bool CODES>
+__global__ __launch_bounds__(64 * kSliceW) void quantize_slice(Quantize<E> a) {
+    constexpr int G = kSliceG, W = kSliceW, V = 16 / (int)sizeof(typename E::type), TT = G * V;
+    typedef typename Vec<typename E::type, V>::type Some;
+    __shared__ uint32_t meet[W][4 * G], most[TT];
+    const int id = gi::xcd_order(blockIdx.x, gridDim.x), slice = blockIdx.y, slices = gridDim.y;
+    const int b = id / a.tiles, t0 = id % a.tiles * TT;
+    const int len = length_of(a.lengths, b, a.L);
+    const int group = threadIdx.x % G, quad = threadIdx.x / G, t = t0 + group * V, d = slice * kSlice + quad * 4;
+    uint32_t *const row = a.codes + ((int64_t)b * a.L + t0) * (a.K / 4);   // of position t0
+    Some v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = positions_of<E, V>(a, b, d + j, t, len - t);
+    if constexpr (!CODES) {
+        uint32_t words[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) see_positions<E, V>(v[j], words);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int s = G; s < 64; s *= 2)
+                words[k] = raise(words[k], (uint32_t)__shfl_xor((int)words[k], s, 64), E{});
+            if (threadIdx.x % 64 < G) meet[threadIdx.x / 64][group * 4 + k] = words[k];
+        }
+        __syncthreads();
+        if (threadIdx.x < TT) {
+            const int at = threadIdx.x;   // position: V / 4 of them in a word
+            uint32_t word = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) word = raise(word, meet[w][at / (V / 4)], E{});
+            most[at] = wide<E>(word >> 16 * (at % (V / 4)));
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < TT * slices; i += 64 * W) {
+            const int at = i / slices, copy = i % slices;
+            if (t0 + at < a.L) row[at * (a.K / 4) + copy * (kSlice / 4) + slice] = most[at];
+        }
+    } else {
+        // 64 W / TT threads a position, the first ones of a group of lanes.
+        constexpr int kShare = 64 * W / TT;
+        const int at = threadIdx.x / kShare;
+        uint32_t own = 0;
+        if (t0 + at < a.L)
+            for (int s = threadIdx.x % kShare; s < slices; s += kShare)
+                own = max(own, row[at * (a.K / 4) + slice * (kSlice / 4) + s]);
+#pragma unroll
+        for (int s = 1; s < kShare; s *= 2) own = max(own, (uint32_t)__shfl_xor((int)own, s, 64));
+        if (threadIdx.x % kShare == 0) {
+            most[at] = own;
+            if (slice == 0 && t0 + at < a.L) a.scales[(int64_t)b * a.L + t0 + at] = row_scale(own);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (t + k < a.L && d < a.K)
+                row[(group * V + k) * (a.K / 4) + d / 4] = codes_of<E, V>(v, k, coder(most[group * V + k]));
+    }
+}
+
+template <class E>
+hipError_t quantize_slices(Quantize<E> k, hipStream_t s) {
+    constexpr int TT = kSliceG * 16 / (int)sizeof(typename E::type);
+    k.tiles = (k.L + TT - 1) / TT;
+    const dim3 grid((unsigned)(k.B * (int64_t)k.tiles), (unsigned)((k.D + kSlice - 1) / kSlice));
+    quantize_slice<E, false><<<grid, 64 * kSliceW, 0, s>>>(k);
+    quantize_slice<E, true><<<grid, 64 * kSliceW, 0, s>>>(k);
+    return hipGetLastError();
 }
 
 // Channels along the lanes (one position, contiguous channels): a work-group a row.  Two round
@@ -260,7 +352,15 @@ hipError_t quantize(const quantize_tokens_args &a, hipStream_t s) {
     // 1, 8): [1, 4096, 8192] bf16 23.9 / 27.6 / 25.5 / 29.8, [4, 2048, 2048] bf16 13.6 / 16.2 /
     // 14.2 / 17.3, [2, 2051, 777] f32 11.4 / 9.0 / 9.8 / 10.7, [2, 1024, 1000] bf16 6.9 / 6.1 /
     // 5.2 / 5.6, [5, 1000, 301] f16 8.4 / 7.9 / 7.1 / 5.9, [1, 8192, 2000] bf16 34 / 21 / 26 / 19.
+    // The channels are shared out too where even the finest share leaves half of the compute units
+    // without positions and each of the others with many channels, which bound it ([1, 4096, 100]
+    // as long as [1, 4096, 500]); it costs a second launch.  Measured (us, shared out / not, bf16):
+    // [1, 4096, 500] 8.3 / 11.2, [1, 8192, 100] 7.7 / 18.7, [1, 4096, 2000] 13.7 / 11.0, [1, 2048, 500] 7.7 /
+    // 7.2, [64, 4096, 8] 8.5 / 6.1 (a slice has 64 bytes of positions).
     const int64_t groups = (int64_t)a.B * ((a.L * sizeof(typename E::type) + 15) / 16);
+    const int slices = (a.D + kSlice - 1) / kSlice;
+    if (groups <= 128 && slices > 5 && slices <= kMaxSlices && a.L * sizeof(typename E::type) >= 64)
+        return quantize_slices<E>(k, s);
     if (groups >= 1024) return quantize_tiles<E, 4, 16>(k, s);
     if (groups < 256) return quantize_tiles<E, 1, 8>(k, s);
     return a.D > 1024 ? quantize_tiles<E, 2, 16>(k, s) : quantize_tiles<E, 2, 8>(k, s);

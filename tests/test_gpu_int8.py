@@ -45,6 +45,8 @@ QUANT = [  # B, D, L, lengths, layout
     (3, 40, 31, "none", "dense"), (2, 300, 33, None, "slice"), (5, 1001, 70, "ragged", "padded"),
     (1, 260, 257, None, "swapped"), (4, 300, 1, None, "dense"), (4, 300, 1, None, "slice"), (7, 2050, 1, "ragged", "swapped"),
     (1, 4100, 40, None, "dense"), (2, 9000, 5, None, "slice"), (1, 2000, 64, None, "padded"),
+    (1, 2561, 33, None, "dense"), (3, 4100, 70, "ragged", "padded"), (1, 16384, 40, None, "slice"), (1, 16385, 40, None, "dense"),
+    (2, 8000, 100, "none", "swapped"),
 ]
 
 
@@ -228,6 +230,17 @@ def test_step_of_few_long_rows(B, D, E):
     assert torch.equal(gi.project_int8_step(wide[:, 1::2], w, ws), want)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [300, 4000])
+def test_positions_that_are_no_numbers(D, dtype):
+    i = Inputs(6, dtype)
+    x = i.normal(1, D, 50)
+    x[0, 7, 3], x[0, :, 4], x[0, D - 1, 40] = float("nan"), 0, -float("inf")
+    codes, scales = gi.quantize_tokens(x)
+    check_codes(x, codes, scales)
+    assert torch.isnan(scales[0, [3, 40]]).all() and scales[0, 4] == 0 and torch.isfinite(scales).sum() == 48
+
+
 def test_step_with_rows_that_are_no_numbers():
     i = Inputs(2, "bf16")
     w, ws = gi.quantize_weight(i.normal(40, 300))
@@ -285,7 +298,8 @@ def test_graph_replays_and_streams():
 
 
 @pytest.mark.parametrize("B,D,E,L", [(1, 600, 4096, 3000), (2, 300, 2100, 1000), (3, 1000, 515, 301), (1, 900, 1000, 90),
-                                     (900, 128, 1500, 1), (5, 6500, 70, 1), (3000, 300, 4097, 1)])
+                                     (900, 128, 1500, 1), (5, 6500, 70, 1), (3000, 300, 4097, 1),
+                                     (1, 4096, 300, 90)])
 def test_every_size_of_tiles_replays_and_runs_beside_another(B, D, E, L):
     """Captured and replayed, and on two streams at once."""
     i = Inputs(B + D + E, "bf16")
