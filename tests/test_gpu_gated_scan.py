@@ -248,6 +248,18 @@ def test_outputs_of_the_caller():
     assert (wide[:, :3] == 7).all() and (wide[:, 13:] == 7).all()
 
 
+@pytest.mark.parametrize("L", [3, 100, 700, 3000])
+def test_rate_of_minus_infinity(L):
+    """Forgets as a rate does whose decays are 0 in fp32, with the same gradients."""
+    s = Gated((2, 36, L, None, "dense"), "f32")
+    got = []
+    for rate in (-float("inf"), -1e30):
+        s.A[::3] = rate
+        y, h, marks = s.forward(want_state=True, want_checkpoints=True)
+        got.append([y, h, marks, *s.backward(marks, want_dstate=True)])
+    assert all(torch.equal(p, q) and torch.isfinite(p).all() for p, q in zip(*got))
+
+
 def test_graph_replays():
     """Captured once, replayed with eager work in between: each replay equals the eager pass."""
     s = Gated((2, 36, 700, None, "dense"), "bf16")
