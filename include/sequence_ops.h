@@ -2,7 +2,8 @@
  * sequence_ops.h -- C ABI of the sequence operators of the MI355X (gfx950)
  * convolution library: a depthwise causal convolution, a selective state space
  * scan, a gated recurrence, the norms between two residual blocks, and
- * projections in 8-bit integers.  Same shared library, status codes and error text as conv2d_grad_input.h.
+ * projections in 8-bit integers.  Same shared library, status codes and error
+ * text as conv2d_grad_input.h.
  *
  * Layouts
  * -------
