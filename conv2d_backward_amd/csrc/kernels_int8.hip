@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t codes_of(const typename Vec<typename E::type
 // first KEPT rounds stay in registers between the two passes, over the maximum and over the
 // codes; what is beyond is read again.  With G = 4 a wave's loads are 64 bytes of 16
 // channels, its stores 64 bytes of codes of 4 positions.  Bound by memory: [1, 4096, 8192]
-// bf16 23.7 us, 4.25 TB/s of the 4.85 that a copy reaches, [4, 2048, 2048] 13.5 us.
+// bf16 23.7 us, 4.25 TB/s of the 4.85 that a copy reaches, [4, 2048, 2048] 12.8 us.
 template <class E, int G, int W, int KEPT>
 __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
     using T = typename E::type;
@@ -347,23 +347,31 @@ hipError_t quantize(const quantize_tokens_args &a, hipStream_t s) {
         quantize_row<E><<<(unsigned)a.B, 256, 0, s>>>(k);
         return hipGetLastError();
     }
-    // Few positions are shared out finer, so that more compute units have some, though a
-    // cache line then goes to several of them.  Measured (us; G, W of 4, 16 / 2, 16 / 2, 8 /
-    // 1, 8): [1, 4096, 8192] bf16 23.9 / 27.6 / 25.5 / 29.8, [4, 2048, 2048] bf16 13.6 / 16.2 /
-    // 14.2 / 17.3, [2, 2051, 777] f32 11.4 / 9.0 / 9.8 / 10.7, [2, 1024, 1000] bf16 6.9 / 6.1 /
-    // 5.2 / 5.6, [5, 1000, 301] f16 8.4 / 7.9 / 7.1 / 5.9, [1, 8192, 2000] bf16 34 / 21 / 26 / 19.
-    // The channels are shared out too where even the finest share leaves half of the compute units
-    // without positions and each of the others with many channels, which bound it ([1, 4096, 100]
-    // as long as [1, 4096, 500]); it costs a second launch.  Measured (us, shared out / not, bf16):
-    // [1, 4096, 500] 8.3 / 11.2, [1, 8192, 100] 7.7 / 18.7, [1, 4096, 2000] 13.7 / 11.0, [1, 2048, 500] 7.7 /
-    // 7.2, [64, 4096, 8] 8.5 / 6.1 (a slice has 64 bytes of positions).
-    const int64_t groups = (int64_t)a.B * ((a.L * sizeof(typename E::type) + 15) / 16);
+    const int64_t bytes = a.L * (int64_t)sizeof(typename E::type);
+    // The channels are shared out too where even the finest share leaves half of the compute
+    // units without positions and each of the others with many channels, which bound it ([1,
+    // 4096, 100] as long as [1, 4096, 500]); it costs a second launch.  Measured (us, shared out
+    // / not, bf16): [1, 4096, 500] 8.3 / 11.2, [1, 8192, 100] 7.7 / 18.7, [1, 4096, 2000] 13.7 /
+    // 11.0, [1, 2048, 500] 7.7 / 7.2, [64, 4096, 8] 8.5 / 6.1 (a slice has 64 bytes of
+    // positions).
+    const int64_t groups = a.B * ((bytes + 15) / 16);
     const int slices = (a.D + kSlice - 1) / kSlice;
-    if (groups <= 128 && slices > 5 && slices <= kMaxSlices && a.L * sizeof(typename E::type) >= 64)
+    if (groups <= 128 && slices > 5 && slices <= kMaxSlices && bytes >= 64)
         return quantize_slices<E>(k, s);
-    if (groups >= 1024) return quantize_tiles<E, 4, 16>(k, s);
+    // Few positions are shared out finer, so that more compute units have some, though a cache
+    // line then goes to several of them; positions that end early have no lanes beyond.  More
+    // waves to a position where its channels would not stay in registers otherwise.  Measured
+    // (us; G, W of 4, 16 / 4, 8 / 2, 16 / 2, 8 / 1, 8): [1, 4096, 8192] bf16 23.9 - 27.6 25.5
+    // 29.8, [1, 1024, 8192] 9.6 8.6 11.3 9.7 12.1, [1, 4096, 4096] 18.9 21.9 16.1 15.2 17.0, [2,
+    // 2051, 777] f32 13.2 - 9.5 10.1 11.3, [2, 1024, 1000] bf16 6.7 5.8 6.1 5.1 5.6, [5, 1000,
+    // 301] f16 8.3 7.3 7.7 6.9 5.8, [512, 2048, 16] bf16 18.5 16.2 15.3 13.3 15.0; 1, 8 / 1, 4:
+    // [1024, 2048, 2] 10.7 / 9.0, [2000, 300, 3] 13.3 / 8.4, [256, 4096, 4] 11.7 / 12.3.
     if (groups < 256) return quantize_tiles<E, 1, 8>(k, s);
-    return a.D > 1024 ? quantize_tiles<E, 2, 16>(k, s) : quantize_tiles<E, 2, 8>(k, s);
+    if (bytes <= 16) return a.D <= 2048 ? quantize_tiles<E, 1, 4>(k, s) : quantize_tiles<E, 1, 8>(k, s);
+    if (groups >= 1024 && bytes > 32)
+        return a.D <= 2048 ? quantize_tiles<E, 4, 8>(k, s) : quantize_tiles<E, 4, 16>(k, s);
+    return a.D * (int64_t)sizeof(typename E::type) <= 8192 ? quantize_tiles<E, 2, 8>(k, s)
+                                                           : quantize_tiles<E, 2, 16>(k, s);
 }
 
 // ---- the product ---------------------------------------------------------------------------------
@@ -1200,11 +1208,11 @@ hipError_t tiles_any(const Project<E> &k, hipStream_t s) {
     return product<E, 2, 2, 2, 2, 3, SWAPPED>(k, s);
 }
 
-// k is shared out where tiles of whole rows would leave half of the chip without one, and for up to
-// 32 positions, half a tile (us, shared / tiles of 64): 500 x 1024 from 1024 (128 tiles) 4.8 / 5.4,
-// 200 x 2048 from 2048 (128) 6.6 / 7.2, 120 x 4096 from 4096 (128) 9.3 / 11.2, 700 x 1500 from 300 (264)
-// 8.4 / 5.3, 300 x 4096 from 4096 (320) 22 / 13.6, 64 x 16384 from 4096 (256) 17.6 / 16.2; 17 x 65536 from 4096
-// 50 / 63.
+// k is shared out where tiles of whole rows would leave half of the chip without one, and for up
+// to 32 positions, half a tile (us, shared / tiles of 64): 500 x 1024 from 1024 (128 tiles) 4.8 /
+// 5.4, 200 x 2048 from 2048 (128) 6.6 / 7.2, 120 x 4096 from 4096 (128) 9.3 / 11.2, 700 x 1500
+// from 300 (264) 8.4 / 5.3, 300 x 4096 from 4096 (320) 22 / 13.6, 64 x 16384 from 4096 (256) 17.6
+// / 16.2; 17 x 65536 from 4096 50 / 63.
 template <class E>
 hipError_t product_any(const project_int8_args &a, hipStream_t s) {
     Project<E> k = project_of<E>(a);
