@@ -235,7 +235,8 @@ __global__ __launch_bounds__(64 * kSliceW) void quantize_slice(Quantize<E> a) {
     const int id = gi::xcd_order(blockIdx.x, gridDim.x), slice = blockIdx.y, slices = gridDim.y;
     const int b = id / a.tiles, t0 = id % a.tiles * TT;
     const int len = length_of(a.lengths, b, a.L);
-    const int group = threadIdx.x % G, quad = threadIdx.x / G, t = t0 + group * V, d = slice * kSlice + quad * 4;
+    const int group = threadIdx.x % G, quad = threadIdx.x / G, t = t0 + group * V;
+    const int d = slice * kSlice + quad * 4;
     uint32_t *const row = a.codes + ((int64_t)b * a.L + t0) * (a.K / 4);   // of position t0
     Some v[4];
 #pragma unroll
