@@ -319,8 +319,9 @@ __global__ __launch_bounds__((W > 8 ? 1024 : 512)) void gated_backward(GatedBwd<
             const Decay v = decay(sr[k], A2);
             av[k] = v.a;
             // 1 / m; where a is 1 the normaliser's slope, infinite there, counts as 0 (and
-            // below the normal range, whose root v_sqrt_f32 too takes for 0).
-            inv[k] = v.n >= 1.17549435e-38f ? __builtin_amdgcn_rsqf(v.n) : 0.f * v.n;
+            // below the normal range, whose root v_sqrt_f32 too takes for 0).  A rate above 0
+            // has no root: NaN, as in the forward call.
+            inv[k] = __builtin_fabsf(v.n) < 1.17549435e-38f ? 0.f : __builtin_amdgcn_rsqf(v.n);
             m[k] = v.n * inv[k];
             e[k] = si[k] * nx.at(k);
             gy[k] = ng.at(k);
