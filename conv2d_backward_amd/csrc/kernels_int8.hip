@@ -410,6 +410,28 @@ __device__ __forceinline__ v4i mfma16(v4i a, v4i b, v4i c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
+// The result sum sx sw + bias.  The scales' product is a float of its own, which the sum then multiplies
+// in one fused step; of rows near either end of the range that product would leave it where the
+// result does not (a sum of 0 times infinity, or digits below the normal range that a sum of 2^30
+// brings back), so a scale `is_far` from 1 takes `far_scaled`: the product of the fractions, and
+// the powers of two dealt over both factors of the fused step.  Where the product is a normal
+// number both give the same bits, so that either may be taken for several results at once.
+__device__ __forceinline__ int is_far(float scale) {
+    const float size = __builtin_fabsf(scale);
+    return (int)(size > 0x1p62f) | ((int)(size < 0x1p-62f) & (int)(size > 0.f));   // (no branches)
+}
+__device__ __forceinline__ float scaled(float sum, float sx, float sw, float bias) {
+    return __builtin_fmaf(sum, sx * sw, bias);
+}
+__device__ __forceinline__ float far_scaled(float sum, float sx, float sw, float bias) {
+    const float fraction = __builtin_amdgcn_frexp_mantf(sx) * __builtin_amdgcn_frexp_mantf(sw);
+    const int power = __builtin_amdgcn_frexp_expf(sx) + __builtin_amdgcn_frexp_expf(sw);
+    // (1 <= |sum| < 2^31 and 1/4 <= |fraction| < 1 stay normal numbers; powers that both ends cut
+    // off make every sum infinite, or nothing.)
+    const int of_sum = min(max(power, -126), 96), of_fraction = min(max(power - of_sum, -124), 128);
+    return __builtin_fmaf(__builtin_amdgcn_ldexpf(sum, of_sum), __builtin_amdgcn_ldexpf(fraction, of_fraction), bias);
+}
+
 // Writes consecutive positions n .. n + V - 1 (n < N, counted over the batch) of channel e.
 template <class E, int V>
 __device__ __forceinline__ void store_positions(const Project<E> &a, int n, int e, float (&v)[V]) {
@@ -478,6 +500,11 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
         sn[k] = scale_of(part * 4 * NB + k);
         if constexpr (SWAPPED) bn[k] = bias_of(part * 4 * NB + k);
     }
+    // Whether any scale is, each lane looking at one of every 64.
+    int far = is_far(scale_of(lane % P));
+#pragma unroll
+    for (int c = 0; c < 16 * RB; c += 64) far |= is_far(w_scale_of(c + lane % (RB < 4 ? 16 * RB : 64)));
+    far = __any(far);
     // Unit u of row c is at u ^ turned(c).
     constexpr int kLine = P * (int)sizeof(T), kRows = sizeof(T) == 2 ? 16 : 8, kUnits = kLine / 16;
     constexpr int kOwn = kUnits / 4, V = 16 / (int)sizeof(T);   // units of a lane, results of a unit
@@ -506,10 +533,18 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
         const float sw = w_scale_of(r * 16 + row);
         float bias = 0.f, v[4 * NB];
         if constexpr (!SWAPPED) bias = bias_of(r * 16 + row);
+        if (__builtin_expect(far, 0)) {
 #pragma unroll
-        for (int k = 0; k < 4 * NB; ++k) {
-            const int one = sum(r, k);
-            v[k] = __builtin_fmaf((float)one, sn[k] * sw, SWAPPED ? bn[SWAPPED ? k : 0] : bias);
+            for (int k = 0; k < 4 * NB; ++k) {
+                const int one = sum(r, k);
+                v[k] = far_scaled((float)one, sn[k], sw, SWAPPED ? bn[SWAPPED ? k : 0] : bias);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4 * NB; ++k) {
+                const int one = sum(r, k);
+                v[k] = scaled((float)one, sn[k], sw, SWAPPED ? bn[SWAPPED ? k : 0] : bias);
+            }
         }
 #pragma unroll
         for (int half = 0; half < 16 / kRows; ++half) {
@@ -938,8 +973,9 @@ struct Split {
     int D, share;
 };
 
+// (128 registers, for two work-groups a compute unit)
 template <class E, int RB, int NB, int S, int FORM>
-__global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
+__global__ __launch_bounds__(64 * S, 4) void project_split(Split<E> t) {
     constexpr bool CODES = FORM == kCodesInside;
     static_assert(!CODES || NB == 1, "the codes of 16 rows");
     constexpr int ROWS = 16 * (RB + (CODES ? 0 : NB)), kLoads = ROWS / 8;
@@ -1010,6 +1046,10 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
         for (int p = 0; p < kLoads; ++p)
             load_lds(p < 2 * RB ? wr : xr, here + p * 1024, from[p], place(j) * kStep);
     };
+    // One of the work-group's scales of each kind, to see whether any is far (asked for behind the first
+    // step they would hold it up: [1, 4096] x 4096 0.2 us more).
+    const float seen_w = a.w_scales[min(e0 + lane % (16 * RB), a.E_ - 1)];
+    const float seen_x = CODES ? 0.f : a.scales[min(n0 + lane % (16 * NB), a.N - 1)];
     if (mine > 0) bring(0);
 
     if constexpr (CODES) {
@@ -1099,11 +1139,12 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
         for (int s = 1; s < S; ++s) sum += meet[(block * S + s) * 64 + lane];
         return sum;
     };
+    const bool far = __any(is_far(seen_w) | is_far(CODES ? own_scales[min(lane % 16, a.N - 1)] : seen_x));
     if constexpr (FORM == kAlongPositions) {
         for (int r = wave; r < RB; r += S) {
             const int e = e0 + r * 16 + row, n = n0 + part * 4 * NB;
             if (e >= a.E_ || n >= a.N) continue;
-            float v[4 * NB];
+            float v[4 * NB], sx[4 * NB];
             const float sw = a.w_scales[e], bias = a.bias ? a.bias[e] : 0.f;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
@@ -1111,9 +1152,16 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int one = sum[k];
-                    v[4 * i + k] = __builtin_fmaf(
-                        (float)one, a.scales[min(n + 4 * i + k, a.N - 1)] * sw, bias);
+                    sx[4 * i + k] = a.scales[min(n + 4 * i + k, a.N - 1)];
+                    v[4 * i + k] = (float)one;
                 }
+            }
+            if (__builtin_expect(far, 0)) {
+#pragma unroll
+                for (int k = 0; k < 4 * NB; ++k) v[k] = far_scaled(v[k], sx[k], sw, bias);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4 * NB; ++k) v[k] = scaled(v[k], sx[k], sw, bias);
             }
             store_positions<E, 4 * NB>(a, n, e, v);
         }
@@ -1127,13 +1175,22 @@ __global__ __launch_bounds__(64 * S) void project_split(Split<E> t) {
             const bool in = l < length_of(a.lengths, b, a.L);
             const float sx = CODES ? own_scales[n] : a.scales[n];
             auto *y = a.y.row(b, e) + l;
-            float v[4];
+            float v[4], sw[4], bias[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int ek = min(e + k, a.E_ - 1), one = sum[k];
-                v[k] = __builtin_fmaf((float)one, sx * a.w_scales[ek], a.bias ? a.bias[ek] : 0.f);
-                v[k] = in ? v[k] : 0.f;
+                const int ek = min(e + k, a.E_ - 1);
+                sw[k] = a.w_scales[ek];
+                bias[k] = a.bias ? a.bias[ek] : 0.f;
             }
+            if (__builtin_expect(far, 0)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = far_scaled((float)sum[k], sx, sw[k], bias[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = scaled((float)sum[k], sx, sw[k], bias[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = in ? v[k] : 0.f;
             if (a.y.channel == 1 && e + 4 <= a.E_) {
                 store_vec<E, 4>(y, v);
             } else {

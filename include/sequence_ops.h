@@ -288,7 +288,8 @@ CONV2D_GI_API int gated_scan_forward(const gated_scan_args *a, hipStream_t strea
  * Where m is 0 (a is 1) the term with 1 / m counts as 0.  dx, dr, di, dz have x's
  * layout rules and type; dA, dr_bias, di_bias [D], dstate [B, D] fp32.  dx, dr, di and
  * dA are required, dz with z, the others may be NULL.  checkpoints: as the forward
- * call on the same inputs wrote them.
+ * call on the same inputs wrote them.  1 - sr and 1 - si are differences in fp32, so that
+ * the slopes of a gate open beyond 16 come out as 0.
  */
 typedef struct gated_scan_backward_args {
     int32_t dtype, B, D, L;
@@ -352,6 +353,8 @@ CONV2D_GI_API int quantize_tokens(const quantize_tokens_args *a, hipStream_t str
  * project_int8: y[b,e,l] = scales[b,l] * w_scales[e] * (sum over k of codes[b,l,k] *
  * w[e,k]) + bias[e], 0 beyond a length.  codes [B, L, K], scales [B, L], w [E, K],
  * w_scales [E], bias [E] (NULL: none); dtype is y's.  The sum is exact, in 32 bits.
+ * Scales may be any fp32 numbers, and their product beyond fp32's range: a sum of 0 leaves
+ * the bias, and results inside y's range keep their digits.
  */
 typedef struct project_int8_args {
     int32_t dtype, B, E, L, K, reserved;
