@@ -337,11 +337,16 @@ int project_int8(const project_int8_args *a, hipStream_t stream) {
     return status(seq::launch_project(*a, stream));
 }
 
-int64_t project_int8_step_workspace(int32_t B, int32_t D, int32_t E) {
-    if (check_codes(SEQ_F32, B, D, 1) != CONV2D_GI_OK ||
-        check_product(SEQ_F32, B, E, 1, int8_row(D)) != CONV2D_GI_OK)
+int64_t project_int8_step_workspace_for(int32_t dtype, int32_t B, int32_t D, int32_t E) {
+    if (check_codes(dtype, B, D, 1) != CONV2D_GI_OK ||
+        check_product(dtype, B, E, 1, int8_row(D)) != CONV2D_GI_OK)
         return -1;
-    return seq::project_step_workspace(B, D);
+    return seq::project_step_workspace(dtype, B, D, E);
+}
+
+int64_t project_int8_step_workspace(int32_t B, int32_t D, int32_t E) {
+    return std::max(project_int8_step_workspace_for(SEQ_F32, B, D, E),
+                    project_int8_step_workspace_for(SEQ_BF16, B, D, E));
 }
 
 int project_int8_step(const project_int8_step_args *a, hipStream_t stream) {
@@ -353,7 +358,7 @@ int project_int8_step(const project_int8_step_args *a, hipStream_t stream) {
         !is_apart(a->y, a->B, a->E, 1))
         return CONV2D_GI_EINVAL;
     if (!is_workspace(a->workspace, a->workspace_bytes,
-                      seq::project_step_workspace(a->B, a->D)))
+                      seq::project_step_workspace(a->dtype, a->B, a->D, a->E)))
         return CONV2D_GI_EINVAL;
     return status(seq::launch_project_step(*a, stream));
 }

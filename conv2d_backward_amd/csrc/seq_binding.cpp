@@ -42,7 +42,7 @@ struct Entry {
     int64_t (*workspace)(int32_t, int32_t, int32_t, int32_t, int32_t);
     int header;                       // sizes in the struct, after the type
     int lead;                         // the operand that has the call's type and device
-    std::vector<int> workspace_sizes; // indices of the workspace function's arguments
+    std::vector<int> workspace_sizes; // indices of the workspace function's arguments (-1: the type)
     std::vector<Operand> operands;
 };
 
@@ -254,7 +254,7 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t count) {
         if (e->workspace) {
             int32_t w[5] = {0, 0, 0, 0, 0};
             for (size_t k = 0; k < e->workspace_sizes.size(); ++k)
-                w[k] = (int32_t)size[e->workspace_sizes[k]];
+                w[k] = e->workspace_sizes[k] < 0 ? code : (int32_t)size[e->workspace_sizes[k]];
             const int64_t bytes = e->workspace(w[0], w[1], w[2], w[3], w[4]);
             // (-1: sizes that the call itself refuses)
             if (bytes > 0) scratch = at::empty({bytes}, lead.options().dtype(at::kByte));

@@ -36,6 +36,6 @@ void gated_plan(int64_t rows, int64_t L, int backward, char *buf, size_t len);
 hipError_t launch_quantize(const quantize_tokens_args &a, hipStream_t s);
 hipError_t launch_project(const project_int8_args &a, hipStream_t s);
 hipError_t launch_project_step(const project_int8_step_args &a, hipStream_t s);
-int64_t project_step_workspace(int B, int D);  // 0: none needed
+int64_t project_step_workspace(int32_t dtype, int B, int D, int E);  // 0: none needed
 
 }  // namespace seq

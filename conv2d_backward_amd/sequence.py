@@ -61,8 +61,9 @@ _ACT, _ACT32, _STATES, _DENSE, _DENSE32, _INDEX, _CODES = range(7)
 _NEEDED, _OPTIONAL, _OUT = range(3)
 
 #: The entries' operands in the order of their structs in sequence_ops.h.  First
-#: the struct's sizes, then sizes that only shapes need; a shape names sizes, "-"
-#: after one takes 1 off.
+#: the struct's sizes, then sizes that only shapes need, then the scratch function
+#: with its arguments (of sizes, or the call's type); a shape names sizes, "-" after one
+#: takes 1 off.
 _ENTRIES = {
     "causal_conv_forward": ("B D L K silu", "", "", [
         ("x", _ACT, _NEEDED, "B D L"), ("out", _ACT, _OUT, "B D L"),
@@ -131,7 +132,7 @@ _ENTRIES = {
         ("weight", _CODES, _NEEDED, "E K"), ("weight_scales", _DENSE32, _NEEDED, "E"),
         ("bias", _DENSE32, _OPTIONAL, "E"), ("out", _ACT, _OUT, "B E L"),
         ("lengths", _INDEX, _OPTIONAL, "B")]),
-    "project_int8_step": ("B D E K reserved", "", "project_int8_step_workspace B D E", [
+    "project_int8_step": ("B D E K reserved", "", "project_int8_step_workspace_for type B D E", [
         ("x", _ACT, _NEEDED, "B D"), ("weight", _CODES, _NEEDED, "E K"),
         ("weight_scales", _DENSE32, _NEEDED, "E"), ("bias", _DENSE32, _OPTIONAL, "E"),
         ("out", _ACT, _OUT, "B E")]),
@@ -169,7 +170,7 @@ def _make(name):
     names = [o[0] for o in operands]
     _made[name] = _sequence.entry(
         address(name), len(header.split()), names.index(next(n for n in ("x", "codes", "y") if n in names)),
-        address(scratch[0]) if scratch else 0, tuple(sizes.index(s) for s in scratch[1:]),
+        address(scratch[0]) if scratch else 0, tuple(-1 if s == "type" else sizes.index(s) for s in scratch[1:]),
         tuple((n, kind, use, tuple((sizes.index(d.rstrip("-")), -d.count("-")) for d in dims.split()))
               for n, kind, use, dims in operands))
     return _made[name]

@@ -382,7 +382,9 @@ typedef struct project_int8_step_args {
     int64_t workspace_bytes;
 } project_int8_step_args;
 CONV2D_GI_API int project_int8_step(const project_int8_step_args *a, hipStream_t stream);
+/* Bytes of scratch for a call of any type, and for one type, which may need less. */
 CONV2D_GI_API int64_t project_int8_step_workspace(int32_t B, int32_t D, int32_t E);
+CONV2D_GI_API int64_t project_int8_step_workspace_for(int32_t dtype, int32_t B, int32_t D, int32_t E);
 
 #ifdef __cplusplus
 }
