@@ -1290,25 +1290,28 @@ hipError_t product_any(const project_int8_args &a, hipStream_t s) {
 int64_t code_row(int64_t D) { return (D + SEQ_INT8_ROW - 1) / SEQ_INT8_ROW * SEQ_INT8_ROW; }
 
 // Whether every work-group makes the codes of a single-position call for itself: one block of
-// positions, few numbers for each, and not too many work-groups to do that again and again.  A row
-// has 512 / P threads, P the rows rounded up to a power of two, with 64 numbers each in registers, and
-// making the codes takes as long as D P / 512 of them; what that saves, a launch and the codes' own
-// kernel, is more the longer the rows are, whatever their number.  The border of the sweeps is a
-// bound on P^2 D; float32 numbers take twice the instructions and registers.  Measured (us, made
-// inside / by a kernel before it, both in graphs, the weights from memory; | the border):
+// positions, few numbers for each thread, and not too many work-groups to do that again and again.  A
+// row has 512 / P threads, P the rows rounded up to a power of two, which keep 64 numbers each in
+// registers; float32 numbers take twice the instructions.  What it saves is the codes' own kernel
+// (longer for long rows, whatever their number) and the host's time for a second launch: eager calls
+// take 5.3 us of the host with the codes made inside and 9.2 without.  So the border is where
+// the product with the codes inside takes longer than those 9.2 too.  Measured (us, made inside / by
+// a kernel before it, both in graphs, the weights from memory; | the border):
 // bf16 x 4096: [1, 8192] 9.3 / 11.5, [1, 32768] 29.3 / 38.5, [3, 10900] 15.7 / 16.6, [8, 2048] 6.3 /
-// 6.5, [8, 4096] 8.2 / 8.2, [16, 1024] 5.2 / 5.4 | [5, 5400] 11.5 / 10.5, [5, 6500] 12.5 / 10.5, [9,
-// 2048] 6.8 / 6.5, [9, 2700] 9.4 / 7.7, [16, 2048] 7.0 / 6.5;
-// f32 x 4096: [1, 32768] 33.1 / 44.9, [2, 16384] 22.8 / 26.2, [4, 4096] 9.0 / 8.7, [8, 1024] 5.5 / 6.0 |
-// [4, 8192] 14.2 / 13.5, [5, 2048] 7.9 / 6.8, [8, 2048] 7.9 / 6.9, [16, 1024] 7.1 / 5.8;
-// bf16 x 16384 | 32768 | 49152: [8, 1024] 7.2 / 7.7 | 12.3 / 11.3 | 18.6 / 14.9, [8, 4096] 16.3 / 18.2 |
-// 29.7 / 29.3 | 42.6 / 40.3, [1, 2048] 8.3 / 10.0 | 17.4 / 18.8 | 23.4 / 21.6, [4, 4096] 15.4 / 18.0 |
-// 27.8 / 29.0 | 39.5 / 39.6.
+// 6.5, [8, 4096] 8.2 / 8.2, [9, 2048] 6.8 / 6.5, [16, 2048] 7.0 / 6.5 | [5, 5400] 11.5 / 10.5, [5,
+// 6500] 12.5 / 10.5, [9, 2700] 9.4 / 7.7, [9, 3640] 11.9 / 8.3;
+// f32 x 4096: [1, 32768] 33.1 / 44.9, [2, 16384] 22.8 / 26.2, [4, 4096] 9.0 / 8.7, [8, 2048] 7.9 / 6.9,
+// [16, 1024] 7.1 / 5.8 | [4, 8192] 14.2 / 13.5, [5, 4096] 11.5 / 8.8, [9, 2048] 10.5 / 7.0, [16, 2048]
+// 11.0 / 7.0;
+// bf16 x 16384 | x 24576, x 32768, x 49152: [1, 1024] 7.2 / 7.7 | 9.7 / 8.7, 11.7 / 11.1, 17.9 / 14.7,
+// [4, 4096] 15.4 / 18.0 | 23.6 / 21.3, 27.8 / 29.0, 39.5 / 39.6, [8, 2048] 9.0 / 10.2 | 16.4 / 14.9, 18.4 /
+// 18.6, 25.4 / 22.0, [16, 1024] 7.9 / 7.8 | 11.0 / 9.1, 13.4 / 11.1, 20.2 / 15.1.
 bool codes_inside(int32_t dtype, int64_t B, int64_t D, int64_t E) {
     if (B > 16 || B * D > 32768) return false;
     int64_t P = 1;
     while (P < B) P *= 2;
-    return P * P * D <= (dtype == SEQ_F32 ? 65536 : 262144) && E <= (P <= 4 ? 32768 : 16384);
+    const bool few = dtype == SEQ_F32 ? P <= 2 || P * D <= 16384 : P <= 4 || P * D <= 32768;
+    return few && E <= 16384;
 }
 
 template <class E>

@@ -22,10 +22,10 @@ def gpu():
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("B,D,E", [
-    (16, 256, 40), (16, 257, 40), (16, 1024, 300), (16, 1025, 300), (9, 1024, 33), (9, 1100, 33), (8, 1024, 70),
-    (7, 1025, 70), (8, 4096, 50), (5, 4097, 50), (5, 6500, 20), (4, 4096, 30), (3, 4097, 30), (3, 10922, 20),
-    (3, 10923, 20), (4, 8192, 20), (2, 16384, 10), (2, 16385, 10), (1, 32768, 10), (1, 32769, 10), (9, 3640, 20),
-    (16, 70, 16384), (16, 70, 16385), (5, 130, 16400), (1, 130, 32768), (2, 130, 32770), (4, 70, 33000)])
+    (16, 1024, 300), (16, 1025, 300), (16, 2048, 40), (16, 2047, 40), (9, 1024, 33), (9, 1100, 33), (9, 2049, 33),
+    (8, 2048, 70), (7, 2049, 70), (8, 4096, 50), (5, 4097, 50), (5, 6500, 20), (4, 4096, 30), (3, 4097, 30),
+    (3, 10922, 20), (3, 10923, 20), (4, 8192, 20), (2, 16384, 10), (2, 16385, 10), (1, 32768, 10), (1, 32769, 10),
+    (9, 3640, 20), (16, 70, 16384), (16, 70, 16385), (5, 130, 16400), (1, 130, 16384), (2, 130, 16387), (4, 70, 33000)])
 def test_either_side_of_a_border(B, D, E, dtype):
     i = Inputs(B + D + E, dtype)
     w, ws = gi.quantize_weight(i.normal(E, D, dtype=torch.float32))
