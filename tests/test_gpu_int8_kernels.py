@@ -95,7 +95,7 @@ def test_positions_that_are_no_numbers(B, L, D, dtype):
     (16, 70000, 1, 256, None, "dense"), (1, 5000, 17, 128, None, "swapped"), (1, 8300, 30, 1408, None, "dense"),
     (7, 4500, 4, 384, "ragged", "padded"), (2, 515, 150, 256, None, "dense"), (3, 300, 130, 1024, "none", "dense"),
     (7, 400, 60, 2048, "ragged", "slice"), (1, 1000, 500, 384, None, "padded"), (5, 1000, 100, 256, "ragged", "dense"),
-    (1, 60, 900, 128, None, "dense")], ids=str)
+    (1, 60, 900, 128, None, "dense"), (60, 8000, 1, 384, None, "dense"), (40, 4200, 1, 128, None, "swapped")], ids=str)
 @pytest.mark.parametrize("dtype", TYPES)
 def test_products_of_few_positions(case, dtype):
     s = Product(case, dtype)

@@ -25,7 +25,7 @@ def gpu():
 SIZES = [  # B, E, L, K: every kernel of the product, along positions and along channels
     (1, 40, 9, 128), (1, 4200, 12, 256), (1, 300, 20, 128), (1, 4200, 30, 128), (2, 1000, 40, 128), (1, 2100, 60, 128),
     (3, 1000, 301, 128), (2, 1700, 700, 256), (2, 4200, 2000, 256),
-    (9, 40, 1, 128), (16, 5000, 1, 256), (30, 200, 1, 128), (30, 5000, 1, 128), (60, 9000, 1, 128), (900, 1500, 1, 128),
+    (9, 40, 1, 128), (16, 5000, 1, 256), (30, 200, 1, 128), (30, 5000, 1, 128), (60, 8000, 1, 128), (60, 9000, 1, 128), (900, 1500, 1, 128),
     (2100, 1800, 1, 128), (4000, 4200, 1, 256),
 ]
 
