@@ -330,12 +330,17 @@ __global__ __launch_bounds__(256) void quantize_row(Quantize<E> a) {
     }
 }
 
-template <class E, int G, int W>
+// For more than LOW channels and at most HIGH: the rounds kept are 1, 2 or 4.
+template <class E, int G, int W, int LOW, int HIGH>
 hipError_t quantize_tiles(Quantize<E> k, hipStream_t s) {
     constexpr int TT = G * 16 / (int)sizeof(typename E::type), kRound = 256 * W / G;
+    constexpr int kFewest = LOW < kRound ? 1 : LOW < 2 * kRound ? 2 : 4;
+    constexpr int kMost = HIGH <= kRound ? 1 : HIGH <= 2 * kRound ? 2 : 4;
     k.tiles = (k.L + TT - 1) / TT;
-    const auto kernel = k.D <= kRound ? quantize_tile<E, G, W, 1>
-                        : k.D <= 2 * kRound ? quantize_tile<E, G, W, 2> : quantize_tile<E, G, W, 4>;
+    const int kept = k.D <= kRound ? 1 : k.D <= 2 * kRound ? 2 : 4;
+    const auto kernel = kept <= kFewest ? quantize_tile<E, G, W, kFewest>
+                        : kept < kMost ? quantize_tile<E, G, W, (kMost > 2 && kFewest < 2 ? 2 : kMost)>
+                                       : quantize_tile<E, G, W, kMost>;
     kernel<<<(unsigned)(k.B * (int64_t)k.tiles), 64 * W, 0, s>>>(k);
     return hipGetLastError();
 }
@@ -367,12 +372,13 @@ hipError_t quantize(const quantize_tokens_args &a, hipStream_t s) {
     // 2051, 777] f32 13.2 - 9.5 10.1 11.3, [2, 1024, 1000] bf16 6.7 5.8 6.1 5.1 5.6, [5, 1000,
     // 301] f16 8.3 7.3 7.7 6.9 5.8, [512, 2048, 16] bf16 18.5 16.2 15.3 13.3 15.0; 1, 8 / 1, 4:
     // [1024, 2048, 2] 10.7 / 9.0, [2000, 300, 3] 13.3 / 8.4, [256, 4096, 4] 11.7 / 12.3.
-    if (groups < 256) return quantize_tiles<E, 1, 8>(k, s);
-    if (bytes <= 16) return a.D <= 2048 ? quantize_tiles<E, 1, 4>(k, s) : quantize_tiles<E, 1, 8>(k, s);
+    constexpr int kAll = SEQ_MAX_INT8_CHANNELS, kHalf = 8192 / (int)sizeof(typename E::type);
+    if (groups < 256) return quantize_tiles<E, 1, 8, 0, kAll>(k, s);
+    if (bytes <= 16)
+        return a.D <= 2048 ? quantize_tiles<E, 1, 4, 0, 2048>(k, s) : quantize_tiles<E, 1, 8, 2048, kAll>(k, s);
     if (groups >= 1024 && bytes > 32)
-        return a.D <= 2048 ? quantize_tiles<E, 4, 8>(k, s) : quantize_tiles<E, 4, 16>(k, s);
-    return a.D * (int64_t)sizeof(typename E::type) <= 8192 ? quantize_tiles<E, 2, 8>(k, s)
-                                                           : quantize_tiles<E, 2, 16>(k, s);
+        return a.D <= 2048 ? quantize_tiles<E, 4, 8, 0, 2048>(k, s) : quantize_tiles<E, 4, 16, 2048, kAll>(k, s);
+    return a.D <= kHalf ? quantize_tiles<E, 2, 8, 0, kHalf>(k, s) : quantize_tiles<E, 2, 16, kHalf, kAll>(k, s);
 }
 
 // ---- the product ---------------------------------------------------------------------------------
