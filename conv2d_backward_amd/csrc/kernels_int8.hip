@@ -438,6 +438,15 @@ __device__ __forceinline__ float far_scaled(float sum, float sx, float sw, float
     return __builtin_fmaf(__builtin_amdgcn_ldexpf(sum, of_sum), __builtin_amdgcn_ldexpf(fraction, of_fraction), bias);
 }
 
+// Between the fused step and the rounding to 16 bits: merged into one instruction (v_fma_mixlo_f16)
+// they would round once, in some kernels and for some channels, and a result would depend on how many
+// positions a call has.
+template <int V>
+__device__ __forceinline__ void keep_apart(float (&v)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) asm("" : "+v"(v[k]));
+}
+
 // Writes consecutive positions n .. n + V - 1 (n < N, counted over the batch) of channel e.
 template <class E, int V>
 __device__ __forceinline__ void store_positions(const Project<E> &a, int n, int e, float (&v)[V]) {
@@ -552,6 +561,7 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
                 v[k] = scaled((float)one, sn[k], sw, SWAPPED ? bn[SWAPPED ? k : 0] : bias);
             }
         }
+        keep_apart(v);
 #pragma unroll
         for (int half = 0; half < 16 / kRows; ++half) {
             if (row / kRows == half) {
@@ -1169,6 +1179,7 @@ __global__ __launch_bounds__(64 * S, 4) void project_split(Split<E> t) {
 #pragma unroll
                 for (int k = 0; k < 4 * NB; ++k) v[k] = scaled(v[k], sx[k], sw, bias);
             }
+            keep_apart(v);
             store_positions<E, 4 * NB>(a, n, e, v);
         }
     } else {
@@ -1195,6 +1206,7 @@ __global__ __launch_bounds__(64 * S, 4) void project_split(Split<E> t) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = scaled((float)sum[k], sx, sw[k], bias[k]);
             }
+            keep_apart(v);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = in ? v[k] : 0.f;
             if (a.y.channel == 1 && e + 4 <= a.E_) {
