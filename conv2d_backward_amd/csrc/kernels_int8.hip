@@ -494,9 +494,9 @@ __device__ __forceinline__ uint4 packed(const float *v) {
 // not all in one batch item and inside its length, or channels are missing, they leave one by
 // one, a lane a position, all of them read before the first leaves (3000 positions, 1024 -> 4096
 // channels in tiles of 256: 20.5 us; read one by one 27.5).  Returns whether that took exactly
-// RB NB sizeof(T) / 4 stores.  SWAPPED: the bias goes by positions.
+// RB NB sizeof(T) / 4 stores.  SWAPPED: the bias goes by positions.  far: a scale of the wave's is.
 template <class E, int NB, int RB, bool SWAPPED, class Sx, class Sw, class Bias, class Sum>
-__device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t *turn, Sx scale_of,
+__device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t *turn, bool far, Sx scale_of,
                                       Sw w_scale_of, Bias bias_of, Sum sum) {
     using T = typename E::type;
     // (opaque: addresses that depend on the lane alone would be kept over the caller's steps)
@@ -515,11 +515,6 @@ __device__ __forceinline__ bool leave(const Project<E> &a, int n, int e, uint8_t
         sn[k] = scale_of(part * 4 * NB + k);
         if constexpr (SWAPPED) bn[k] = bias_of(part * 4 * NB + k);
     }
-    // Whether any scale is, each lane looking at one of every 64.
-    int far = is_far(scale_of(lane % P));
-#pragma unroll
-    for (int c = 0; c < 16 * RB; c += 64) far |= is_far(w_scale_of(c + lane % (RB < 4 ? 16 * RB : 64)));
-    far = __any(far);
     // Unit u of row c is at u ^ turned(c).
     constexpr int kLine = P * (int)sizeof(T), kRows = sizeof(T) == 2 ? 16 : 8, kUnits = kLine / 16;
     constexpr int kOwn = kUnits / 4, V = 16 / (int)sizeof(T);   // units of a lane, results of a unit
@@ -657,6 +652,10 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) acc[r][n] = v4i{0, 0, 0, 0};
 
+    // One of the wave's scales of each kind in a lane; on their way beside the first steps.
+    const int n = n0 + wm * 16 * NB, e = e0 + we * 16 * RB;
+    const float seen_x = a.scales[min(n + lane % (16 * NB), a.N - 1)];
+    const float seen_w = a.w_scales[min(e + lane % (16 * RB), a.E_ - 1)];
     if (any) {
         // Each thread's share of a step: unit tid + p kThreads, at the same offset in every
         // step.  Rows past the end are the last one again.
@@ -730,9 +729,9 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
     }
 
     // (every wave has read its last operands before the last barrier)
-    const int n = n0 + wm * 16 * NB, e = e0 + we * 16 * RB;
+    const bool far = __any(is_far(seen_x) | is_far(seen_w));
     leave<E, NB, RB, SWAPPED>(
-        a, n, e, smem + wave * 2048, [&](int k) { return a.scales[min(n + k, a.N - 1)]; },
+        a, n, e, smem + wave * 2048, far, [&](int k) { return a.scales[min(n + k, a.N - 1)]; },
         [&](int c) { return a.w_scales[min(e + c, a.E_ - 1)]; },
         [&](int i) {
             return !a.bias ? 0.f : SWAPPED ? a.bias[min(n + i, a.N - 1)] : a.bias[min(e + i, a.E_ - 1)];
@@ -916,9 +915,11 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void project_stream(Project<E
             multiply(second, first, at ^ 1, 0, std::true_type{}, at, k + 2 < steps ? k + 2 : k + 2 - steps);
         }
         const float *sx = reinterpret_cast<const float *>(smem + kStreamScales + set * 4096);
+        const float *const sw = sx + 256 + we * 128;
+        const bool far = __any(is_far(sx[wm * 64 + lane]) | is_far(sw[lane]) | is_far(sw[64 + lane]));
         whole_stores = leave<E, NB, RB, SWAPPED>(
-            a, now.n0 + wm * 64, now.e0 + we * 128, smem + kStreamTurn + wave * 2048,
-            [&](int k) { return sx[wm * 64 + k]; }, [&](int c) { return sx[256 + we * 128 + c]; },
+            a, now.n0 + wm * 64, now.e0 + we * 128, smem + kStreamTurn + wave * 2048, far,
+            [&](int k) { return sx[wm * 64 + k]; }, [&](int c) { return sw[c]; },
             [&](int i) { return sx[512 + (SWAPPED ? wm * 64 : we * 128) + i]; },
             [&](int r, int k) { return acc[r][k / 4][k % 4]; });
         now = next;
