@@ -628,6 +628,7 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
     constexpr int kThreads = 64 * WM * WE, TM = 16 * WM * NB, TE = 16 * WE * RB;
     constexpr int kLoads = (TM + TE) * 8 / kThreads, kStage = (TM + TE) * kStep;
     static_assert((TM + TE) * 8 % kThreads == 0 && TM * 8 % kThreads == 0, "whole rounds of loads");
+    static_assert(NB <= 4 && RB <= 4, "a wave's scales of a kind in its lanes");
     extern __shared__ uint8_t smem[];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int id = gi::xcd_order(blockIdx.x, gridDim.x);
@@ -995,6 +996,7 @@ template <class E, int RB, int NB, int S, int FORM>
 __global__ __launch_bounds__(64 * S, 4) void project_split(Split<E> t) {
     constexpr bool CODES = FORM == kCodesInside;
     static_assert(!CODES || NB == 1, "the codes of 16 rows");
+    static_assert(NB <= 4 && RB <= 4, "the scales of a kind in a wave's lanes");
     constexpr int ROWS = 16 * (RB + (CODES ? 0 : NB)), kLoads = ROWS / 8;
     const Project<E> &a = t.p;
     extern __shared__ uint8_t smem[];

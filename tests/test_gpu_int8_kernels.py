@@ -101,3 +101,23 @@ def test_products_of_few_positions(case, dtype):
     s = Product(case, dtype)
     y = s.check()
     assert torch.equal(s.run(), y)
+
+
+@pytest.mark.parametrize("case", [   # single positions of which some are empty
+    (7, 40, 1, 256, "ragged", "dense"), (30, 5000, 1, 128, "ragged", "slice"), (60, 8000, 1, 128, "ragged", "dense"),
+    (900, 1500, 1, 384, "ragged", "swapped"), (2100, 1800, 1, 128, "ragged", "dense"),
+    (4000, 4200, 1, 256, "ragged", "dense"), (3, 70, 1, 128, "none", "dense")], ids=str)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_products_of_single_positions_with_lengths(case, dtype):
+    s = Product(case, dtype)
+    y = s.check()
+    assert torch.equal(s.run(), y)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_codes_of_single_positions_with_lengths(dtype):
+    for layout in ("dense", "slice", "swapped"):
+        n = lengths_of("ragged", 7, 1)
+        x = poison(Inputs(3, dtype).normal(7, 700, 1, layout=layout), n)
+        codes, scales = gi.quantize_tokens(x, lengths=n)
+        check_codes(x, codes, scales, n)
