@@ -13,9 +13,12 @@
 //
 // What bounds it: memory, with the instructions close behind.  A position has 5 activations
 // forward and 9 backward, and some 40 and 70 fp32 instructions beside 8 of the slow ones
-// (exponentials, roots, reciprocals).  bf16 with z, from memory: [1, 4096, 8192] forward 70 us
-// (4.8 TB/s), backward 122 (4.95); [4, 2048, 2048] 34 (4.9) and 73 (4.1); [2, 602, 777] f32, from the
-// caches, 6.1 and 12.8, the latency of a chunk.
+// (exponentials, roots, reciprocals).  With z, operands from memory (the same ones again, of which the
+// memory-side cache has a part): bf16 [1, 4096, 8192] forward 70 us, 4.8 TB/s (67), backward 123, 4.9
+// TB/s (123); [4, 2048, 2048] 40 (33) and 76 (66); f32 [2, 602, 777] 9.7 (6.1) and 17.4 (13.0), the
+// latency of a chunk.  Backward, a SIMD has three waves of 16-bit types (150 to 158 registers) and of
+// float32 with one wave a row (166), two of float32 with more (170 to 178); 16 waves a row are held to
+// 128 registers, for which 16-bit types spill 2 and float32 29.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -462,7 +465,8 @@ struct GatedStep {
 
 // One position: each number is read and written once, V channels a thread (contiguous ones
 // where V > 1), 16 bytes of states for V = 4.  Up to some 100000 channels the launch and one
-// round trip ([1, 4096] bf16 2.3 us), beyond memory ([256, 4096] 4.6 us, 4.1 TB/s).
+// round trip ([8, 2048] bf16 2.4 us), beyond memory ([256, 4096] 4.5 us and 4.2 TB/s where the
+// operands are in the memory-side cache, 7.2 from memory).
 template <class E, int V>
 __global__ __launch_bounds__(256) void gated_step(GatedStep<E> a) {
     const int d = (blockIdx.x * 256 + threadIdx.x) * V, b = blockIdx.y;
@@ -514,7 +518,8 @@ struct Deal {
 // [4, 2000, 500] bf16 13 14 21 34 70 165 / 24 27 43 73 183 268,
 // [1, 600, 500] f32 8.4 4.8 5.3 6.1 8.9 16 / 15.5 9.6 10.2 14 21 34.
 // Forward, a row that two or four waves cover in one chunk, with little over, takes them: all of
-// it is on its way at once.  From memory (1, 2, 4 waves): [4, 2048, 2048] bf16 38.6 37.6 34.5,
+// it is on its way at once.  On three sets of operands in turn (1, 2, 4 waves): [4, 2048, 2048] bf16
+// 38.6 37.6 34.5,
 // [2, 4096, 2048] 38.9 36.8 32.5, [16, 1024, 1024] 36.3 33.9 59.
 Deal pick_deal(int64_t rows, int64_t L, bool backward) {
     if (L <= 4 * T) return {4, 1};

@@ -147,8 +147,11 @@ __device__ __forceinline__ uint32_t codes_of(const typename Vec<typename E::type
 // waves V of them (16 bytes) and four channels at a time, 256 W / G channels in a round.  The
 // first KEPT rounds stay in registers between the two passes, over the maximum and over the
 // codes; what is beyond is read again.  With G = 4 a wave's loads are 64 bytes of 16
-// channels, its stores 64 bytes of codes of 4 positions.  Bound by memory: [1, 4096, 8192]
-// bf16 23.7 us, 4.25 TB/s of the 4.85 that a copy reaches, [4, 2048, 2048] 12.8 us.
+// channels, its stores 64 bytes of codes of 4 positions.  [1, 4096, 8192] bf16 33.6 us from memory, 3.0
+// TB/s of the 4.9 that a copy reaches (23.9 for operands of which the memory-side cache has a part): one
+// work-group of 16 waves a compute unit (109 registers), which all read, then all write.
+// [4, 2048, 2048] 19.2 (13.1); f32 [2, 2051, 777] 11.9 (8.9): 196 work-groups, one each for 256 units,
+// whose numbers take twice the instructions.
 template <class E, int G, int W, int KEPT>
 __global__ __launch_bounds__(64 * W) void quantize_tile(Quantize<E> a) {
     using T = typename E::type;
@@ -298,7 +301,7 @@ hipError_t quantize_slices(Quantize<E> k, hipStream_t s) {
 }
 
 // Channels along the lanes (one position, contiguous channels): a work-group a row.  Two round
-// trips and the launch: [64, 4096] bf16 3.0 us.
+// trips and the launch: [64, 4096] bf16 3.2 us.
 template <class E>
 __global__ __launch_bounds__(256) void quantize_row(Quantize<E> a) {
     __shared__ uint32_t meet[4];
@@ -356,8 +359,8 @@ hipError_t quantize(const quantize_tokens_args &a, hipStream_t s) {
     const int64_t bytes = a.L * (int64_t)sizeof(typename E::type);
     // The channels are shared out too where even the finest share leaves half of the compute
     // units without positions and each of the others with many channels, which bound it ([1,
-    // 4096, 100] as long as [1, 4096, 500]); it costs a second launch.  Measured (us, shared out
-    // / not, bf16): [1, 4096, 500] 8.3 / 11.2, [1, 8192, 100] 7.7 / 18.7, [1, 4096, 2000] 13.7 /
+    // 4096, 100] as long as [1, 4096, 500]); it costs a second launch.  Measured (us, the same operands
+    // again and again as in the next table, shared out / not, bf16): [1, 4096, 500] 8.3 / 11.2, [1, 8192, 100] 7.7 / 18.7, [1, 4096, 2000] 13.7 /
     // 11.0, [1, 2048, 500] 7.7 / 7.2, [64, 4096, 8] 8.5 / 6.1 (a slice has 64 bytes of
     // positions).
     const int64_t groups = a.B * ((bytes + 15) / 16);
@@ -611,10 +614,11 @@ __device__ __forceinline__ int position_turn(int row) {
 // the barrier that hands over a step lies between the halves, so that the matrix cores have
 // work across it.
 //
-// What bounds it: a step's way from the caches through LDS, which a compute unit hides with what
-// other work-groups it has (tiles of 64: three).  [5, 1000, 301] x 2000 bf16 9.1 us, [2, 2051, 777]
-// x 1027 f32 10.2 us, 650 TOP/s both.  Two groups of waves that share the steps of a tile, with
-// half as many barriers: 11.6 and 10.4.
+// What bounds it: the latency of a step's way from the caches through LDS, which a compute unit hides
+// with what other work-groups it has (tiles of 64: three fit; 425 tiles are one or two a unit).
+// [5, 1000, 301] x 2000 bf16 12.1 us from memory, 8.9 again (680 TOP/s), [2, 2051, 777] x 1027 f32 13.6
+// and 10.1 (650).  Two groups of waves that share the steps of a tile, with half as many barriers,
+// took 11.6 and 10.4 where this took 9.1 and 10.2.
 //
 // SWAPPED: single positions, whose results lie along the channels.  The caller gives the weights
 // as positions and the positions as weights; the bias then goes by positions.
@@ -743,11 +747,13 @@ __global__ __launch_bounds__(64 * WM * WE, 2) void project(Project<E> a) {
 // The same for products that fill the chip: tiles of 256 x 256, one work-group a compute
 // unit, which goes through its tiles as one stream of steps: the first steps of the next tile
 // are on their way before the last products of this one, and the results leave while they
-// come.  [1, 4096, 8192] x 8192 bf16: 207 us, 2660 TOP/s (a tile by a work-group of its own: 250
-// us); 8192 x 8192 x 8192: 387 us, 2840 TOP/s, where the library's product with int32 results
-// takes 467.  What bounds it: power.  A step takes 1.33 us on numbers that use all bits and 1.13
-// on zeros, at the clock of which the matrix cores alone would need 0.85; the results of a tile take
-// 2.9 us beside the steps.
+// come.  [1, 4096, 8192] x 8192 bf16: 224 us from memory, 200 again, 2450 and 2750 TOP/s (a tile by a
+// work-group of its own took 250 where this took 207); 8192 x 8192 x 8192: 417 and 381 us, where the
+// library's product with int32 results takes 456 again.  What bounds it: LDS and power.  A step takes
+// 1.33 us on numbers that use all bits and 1.13 on zeros, at the clock of which the matrix cores alone
+// would need 0.85: its 192 KB of reads by eight waves and 64 KB of loads are 2048 cycles of LDS, as many
+// as its products take, and do not all lie beside them; the other 0.2 us are power.  The results
+// of a tile take 2.9 us beside the steps.
 constexpr int kStreamWM = 4, kStreamWE = 2, kStreamNB = 4, kStreamRB = 8;
 constexpr int kStreamTile = 256, kStreamWaves = kStreamWM * kStreamWE;
 constexpr int kStreamStage = 2 * kStreamTile * kStep;
@@ -973,8 +979,9 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lanes) {
 // while this one's products run; one more ahead was slower ([32, 4096] x 8192 9.1 us for 8.0,
 // [8, 2048] x 4096 3.33 for 3.30): fewer work-groups share a compute unit.
 // Rows are swizzled as in `project`.  Bound by memory where the weights are many ([64, 4096] x 8192
-// bf16 8.1 us, 4.3 TB/s with all of its operands), else by the chain of launch, one round trip
-// to memory, one through LDS and the sums' meeting ([8, 2048] x 4096 3.2 us).
+// bf16 8.3 us and 4.2 TB/s with weights in the memory-side cache, 12.2 from memory), else by the chain
+// of launch, one round trip to memory, one through LDS and the sums' meeting ([8, 2048] x 4096
+// 3.4 and 4.6 us).
 //
 // What the results are laid out along decides which operand is the first: a lane has four
 // consecutive rows of it.  Along channels (one position a row), the weights.  Along
