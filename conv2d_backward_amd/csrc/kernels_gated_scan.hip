@@ -519,8 +519,7 @@ struct Deal {
 // [1, 600, 500] f32 8.4 4.8 5.3 6.1 8.9 16 / 15.5 9.6 10.2 14 21 34.
 // Forward, a row that two or four waves cover in one chunk, with little over, takes them: all of
 // it is on its way at once.  On three sets of operands in turn (1, 2, 4 waves): [4, 2048, 2048] bf16
-// 38.6 37.6 34.5,
-// [2, 4096, 2048] 38.9 36.8 32.5, [16, 1024, 1024] 36.3 33.9 59.
+// 38.6 37.6 34.5, [2, 4096, 2048] 38.9 36.8 32.5, [16, 1024, 1024] 36.3 33.9 59.
 Deal pick_deal(int64_t rows, int64_t L, bool backward) {
     if (L <= 4 * T) return {4, 1};
     if (L <= kRow || (L <= 4 * kRow && rows >= 4096)) return {16, 1};

@@ -359,10 +359,10 @@ hipError_t quantize(const quantize_tokens_args &a, hipStream_t s) {
     const int64_t bytes = a.L * (int64_t)sizeof(typename E::type);
     // The channels are shared out too where even the finest share leaves half of the compute
     // units without positions and each of the others with many channels, which bound it ([1,
-    // 4096, 100] as long as [1, 4096, 500]); it costs a second launch.  Measured (us, the same operands
-    // again and again as in the next table, shared out / not, bf16): [1, 4096, 500] 8.3 / 11.2, [1, 8192, 100] 7.7 / 18.7, [1, 4096, 2000] 13.7 /
-    // 11.0, [1, 2048, 500] 7.7 / 7.2, [64, 4096, 8] 8.5 / 6.1 (a slice has 64 bytes of
-    // positions).
+    // 4096, 100] as long as [1, 4096, 500]); it costs a second launch.  Measured (us, the same
+    // operands again and again, as in the table below; shared out / not, bf16): [1, 4096, 500] 8.3 /
+    // 11.2, [1, 8192, 100] 7.7 / 18.7, [1, 4096, 2000] 13.7 / 11.0, [1, 2048, 500] 7.7 / 7.2, [64, 4096,
+    // 8] 8.5 / 6.1 (a slice has 64 bytes of positions).
     const int64_t groups = a.B * ((bytes + 15) / 16);
     const int slices = (a.D + kSlice - 1) / kSlice;
     if (groups <= 128 && slices > 5 && slices <= kMaxSlices && bytes >= 64)
